@@ -11,10 +11,27 @@
 #include "kda.h"
 #include "kda_internal.h"
 #include "kda_kernels.h"
+#include "kda_layer.h"
 #include "kda_validate.h"
 
 namespace {
+thread_local int g_last_hip_error = 0;
+}
 
+namespace kda {
+int finish_launch() {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) {
+    g_last_hip_error = static_cast<int>(e);
+    return KDA_ERR_HIP;
+  }
+  return KDA_OK;
+}
+}  // namespace kda
+
+namespace {
+
+using kda::finish_launch;
 using kda::backward_workspace_need;
 using kda::check_backward;
 using kda::check_carry;
@@ -24,8 +41,6 @@ using kda::check_summaries;
 using kda::workspace_need;
 using kda::PieceLayout;
 
-thread_local int g_last_hip_error = 0;
-
 // Grid of a chunk kernel: F * hn workgroups numbered linearly (head fastest),
 // laid out as x = hn * a, y = ceil(F / a) with the smallest a that keeps y
 // within 65535.  x must stay within 2^31 - 1 work-items.
@@ -34,15 +49,6 @@ int chunk_grid(int32_t F, int32_t hn, int threads, dim3* grid) {
   const int64_t x = static_cast<int64_t>(hn) * (a > 0 ? a : 1);
   if (x * threads > 2147483647LL) return KDA_ERR_UNSUPPORTED;
   *grid = dim3(static_cast<uint32_t>(x), static_cast<uint32_t>((F + x / hn - 1) / (x / hn)), 1);
-  return KDA_OK;
-}
-
-int finish_launch() {
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) {
-    g_last_hip_error = static_cast<int>(e);
-    return KDA_ERR_HIP;
-  }
   return KDA_OK;
 }
 

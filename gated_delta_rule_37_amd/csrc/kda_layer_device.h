@@ -1,0 +1,103 @@
+// Device helpers of the operators around the recurrence: typed loads and
+// stores of a few neighbouring elements as FP32, sums over lane groups.
+#ifndef KDA_LAYER_DEVICE_H_
+#define KDA_LAYER_DEVICE_H_
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "kda_device.h"
+
+namespace kda {
+
+// Element storage: FP32 or the raw bits of a bf16.
+typedef float fp32_t;
+typedef uint16_t bf16_t;
+
+// VEC (1 or 8) neighbouring elements at p as FP32.  With VEC = 8, p is
+// aligned to 16 bytes.
+template <int VEC>
+__device__ __forceinline__ void load(const bf16_t* p, float (&x)[VEC]) {
+  if constexpr (VEC == 8) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+    static_assert(VEC == 1, "");
+    x[0] = bf2f(*p);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void load(const fp32_t* p, float (&x)[VEC]) {
+  if constexpr (VEC == 8) {
+    const f32x4 a = ld4(p), b = ld4(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = a[i];
+      x[4 + i] = b[i];
+    }
+  } else {
+    static_assert(VEC == 1, "");
+    x[0] = *p;
+  }
+}
+
+// The same, rounded to nearest even for bf16.
+template <int VEC>
+__device__ __forceinline__ void store(bf16_t* p, const float (&x)[VEC]) {
+  if constexpr (VEC == 8) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+    *reinterpret_cast<u32x4*>(p) = w;
+  } else {
+    *p = static_cast<uint16_t>(pack_bf16(x[0], 0.f));
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store(fp32_t* p, const float (&x)[VEC]) {
+  if constexpr (VEC == 8) {
+    f32x4 a, b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = x[i];
+      b[i] = x[4 + i];
+    }
+    st4(p, a);
+    st4(p + 4, b);
+  } else {
+    *p = x[0];
+  }
+}
+
+// Sum over the 16 lanes of a DPP row, the same bits in each lane (rotations
+// by 8, 4, 2 and 1 add the same pairs everywhere).
+template <int N>
+__device__ __forceinline__ float row_rotate(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + N, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float sum16(float x) {
+  x += row_rotate<8>(x);
+  x += row_rotate<4>(x);
+  x += row_rotate<2>(x);
+  x += row_rotate<1>(x);
+  return x;
+}
+__device__ __forceinline__ float sum64(float x) {
+  x = sum16(x);
+  x += __shfl_xor(x, 16);
+  x += __shfl_xor(x, 32);
+  return x;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float sigmoidf(float z) { return 1.f / (1.f + __expf(-z)); }
+
+}  // namespace kda
+
+#endif  // KDA_LAYER_DEVICE_H_

@@ -11,7 +11,6 @@
 #include "kda_internal.h"
 
 namespace kda {
-namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -20,18 +19,6 @@ int check_heads(int32_t H, int32_t head_begin, int32_t head_count) {
   return KDA_OK;
 }
 
-// A device buffer of the call: its address, the bytes the caller has there
-// and the bytes the call needs.  `optional` buffers may be null (then the
-// size is not checked).
-struct Buf {
-  const void* ptr;
-  size_t have;
-  size_t need;
-  bool optional;
-};
-
-// Null pointers first, then alignment, then sizes, so that each error is
-// reported the same way whichever buffer has it.
 int check_buffers(std::initializer_list<Buf> bufs) {
   for (const Buf& b : bufs) {
     if (b.ptr == nullptr && !b.optional) return KDA_ERR_INVALID_ARG;
@@ -44,6 +31,8 @@ int check_buffers(std::initializer_list<Buf> bufs) {
   }
   return KDA_OK;
 }
+
+namespace {
 
 // Byte sizes of the tensors of a plan, for H heads of K = V = 128.
 struct Sizes {

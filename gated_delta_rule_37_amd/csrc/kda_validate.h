@@ -6,10 +6,28 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <initializer_list>
 
 #include "kda_internal.h"
 
 namespace kda {
+
+// A device buffer of the call: its address, the bytes the caller has there
+// and the bytes the call needs.  `optional` buffers may be null (then the
+// size is not checked).
+struct Buf {
+  const void* ptr;
+  size_t have;
+  size_t need;
+  bool optional;
+};
+// Null pointers first, then alignment, then sizes, so that each error is
+// reported the same way whichever buffer has it.
+int check_buffers(std::initializer_list<Buf> bufs);
+bool aligned16(const void* p);
+
+// The head range [head_begin, head_begin + head_count) of H heads.
+int check_heads(int32_t H, int32_t head_begin, int32_t head_count);
 
 // The forward's workspace for H heads: the chunk cache (256-byte aligned),
 // then, for a plan with pieces, the pieces' transitions, updates and

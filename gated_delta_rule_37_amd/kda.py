@@ -18,6 +18,9 @@ Entry points mirror the C names:
 * :func:`forward` runs the three device calls in order (optionally per head
   group, with the compose launches on a second stream) on fresh output buffers.
 
+The operators around the recurrence (input preparation, output norm, the
+per-channel scan, single-token steps) are bound in :mod:`.layer`.
+
 Every device tensor is passed as its address and its size in bytes, so the
 library can refuse an undersized buffer before it launches anything.
 """
@@ -52,6 +55,10 @@ SYMBOLS = (
     "kda_summary_bytes", "kda_workspace_bytes", "kda_segment_summaries", "kda_compose_summaries",
     "kda_apply_carry", "kda_forward", "kda_forward_noalloc", "kda_noalloc_max_workspace_bytes",
     "kda_backward", "kda_backward_from_forward", "kda_backward_workspace_bytes", "kda_status_string", "kda_last_hip_error",
+    # the operators around the recurrence, bound in layer.py
+    "kda_prepare_inputs", "kda_prepare_inputs_backward", "kda_prepare_inputs_backward_workspace_bytes",
+    "kda_output_norm", "kda_output_norm_backward", "kda_output_norm_backward_workspace_bytes",
+    "kda_scan_forward", "kda_scan_backward", "kda_scan_workspace_bytes", "kda_scan_step", "kda_step",
 )
 
 
@@ -118,6 +125,27 @@ def lib() -> ctypes.CDLL:
     L.kda_backward_from_forward.restype = ctypes.c_int
     L.kda_backward_workspace_bytes.argtypes = [p, i32, i32, i32]
     L.kda_backward_workspace_bytes.restype = sz
+    i64 = ctypes.c_int64
+    rows = [p, sz, i64]      # a device pointer, its size in bytes and its token stride
+    raw = [i32] * 4 + rows * 4 + buf * 2 + [f32] * 2
+    L.kda_prepare_inputs.argtypes = [*raw, *buf * 4, p]
+    L.kda_prepare_inputs_backward.argtypes = [*raw, *buf * 4, *buf * 4, *buf * 2, *buf, p]
+    L.kda_output_norm.argtypes = [*[i32] * 3, *buf, i32, *rows, i32, *buf * 3, i32, f32, *buf, p]
+    L.kda_output_norm_backward.argtypes = [*[i32] * 3, *buf * 2, i32, *rows, i32, *buf * 2, i32, f32, *buf, i32,
+                                           *buf * 3, *buf, p]
+    scan = [p, *buf, i32, i32, *rows, *rows, i32, *buf]
+    L.kda_scan_forward.argtypes = [*scan, *buf, i32, *buf, *buf, p]
+    L.kda_scan_backward.argtypes = [*scan, *buf * 2, i32, *buf, *buf * 3, *buf, p]
+    L.kda_scan_step.argtypes = [*[i32] * 3, *buf * 2, i32, *buf, i32, *buf * 3, p]
+    L.kda_step.argtypes = [*[i32] * 6, *buf * 5, f32, *buf, i32, *buf * 3, i32, p]
+    for name in ("kda_prepare_inputs", "kda_prepare_inputs_backward", "kda_output_norm", "kda_output_norm_backward",
+                 "kda_scan_forward", "kda_scan_backward", "kda_scan_step", "kda_step"):
+        getattr(L, name).restype = ctypes.c_int
+    for name in ("kda_prepare_inputs_backward_workspace_bytes", "kda_output_norm_backward_workspace_bytes"):
+        getattr(L, name).argtypes = [i32] * 3
+        getattr(L, name).restype = sz
+    L.kda_scan_workspace_bytes.argtypes = [p, i32]
+    L.kda_scan_workspace_bytes.restype = sz
     L.kda_noalloc_max_workspace_bytes.argtypes = []
     L.kda_noalloc_max_workspace_bytes.restype = sz
     L.kda_status_string.argtypes = [ctypes.c_int]

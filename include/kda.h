@@ -429,6 +429,220 @@ int kda_backward_from_forward(const kda_plan* plan, const int32_t* plan_dev, siz
  * A state is 64 KiB.  0 for a NULL plan, H <= 0 or K, V other than 128. */
 size_t kda_backward_workspace_bytes(const kda_plan* plan, int32_t H, int32_t K, int32_t V);
 
+/* ------------------------------------------------------------------------
+ * Operators around the recurrence: what one layer runs before and after it,
+ * its form for single tokens, and a recurrence with one state per channel.
+ * The conventions above hold (statuses, host checks before anything is
+ * enqueued, byte counts, 16-byte alignment, asynchronous on `stream`), with
+ * these additions:
+ *   - dtype names the element type of the activations of a call (kda_dtype);
+ *     parameters, states and their gradients are FP32.  Arithmetic runs in
+ *     FP32; a BF16 output is rounded once, to nearest even.
+ *   - A stride is the number of elements from one token's row to the next
+ *     one's; rows themselves are dense.  It is at least the row's length
+ *     (KDA_ERR_INVALID_ARG otherwise), so a call can read a slice of one
+ *     wider projection.  The byte count of such an input covers
+ *     (T - 1) * stride + row elements.  Tensors without a stride are dense.
+ *   - Outputs do not overlap inputs, except where a call says so.
+ *   - T, B, H, V, D are positive (KDA_ERR_INVALID_ARG); T <= 2^30, B <= 2^20,
+ *     H <= 65535, D <= 2^20 and the output norm's V <= 8192, H * V <= 2^24
+ *     (KDA_ERR_UNSUPPORTED).
+ *   - Check order: sizes and options, null pointers, alignment, byte counts,
+ *     workspace.
+ * Every result is the same on every run of the same call: sums over tokens
+ * are taken in a fixed order, without atomics. */
+
+/* Element types; the same values as kda_o_format. */
+typedef enum kda_dtype {
+  KDA_FP32 = 0,
+  KDA_BF16 = 1
+} kda_dtype;
+
+/* Activation of the output norm's gate. */
+typedef enum kda_activation {
+  KDA_ACT_NONE = 0,     /* no gate: pass NULL */
+  KDA_ACT_SIGMOID = 1,  /* 1 / (1 + exp(-z)) */
+  KDA_ACT_SILU = 2      /* z / (1 + exp(-z)) */
+} kda_activation;
+
+/*
+ * kda_prepare_inputs -- the norms before the recurrence and its gates: from
+ * a layer's raw projections to the q, k, g and beta that kda_forward takes.
+ * Per token t and head h, over the K = 128 key channels c:
+ *     q = q_scale * q_raw / sqrt(sum_c q_raw^2 + eps)
+ *     k =           k_raw / sqrt(sum_c k_raw^2 + eps)
+ *     g = -exp(a_log[h]) * softplus(gate_raw + dt_bias[h, c])
+ *     beta = 1 / (1 + exp(-beta_raw))
+ *   q_raw, k_raw, gate_raw  [T, H, K] dtype, rows of H * K elements each
+ *                  with its own token stride, a multiple of 16 bytes
+ *                  (KDA_ERR_MISALIGNED)
+ *   beta_raw       [T, H] dtype, any token stride
+ *   a_log          [H]; dt_bias [H, K] or NULL (zero)
+ *   q_scale        finite; eps positive and finite (KDA_ERR_INVALID_ARG).  A
+ *                  row of zeros gives zeros.  sum_c x^2 has to stay finite in
+ *                  FP32.
+ *   q, k, g        [T, H, K] bf16; beta [T, H] bf16 (dense)
+ */
+int kda_prepare_inputs(int32_t T, int32_t H, int32_t K, int32_t dtype,
+                       const void* q_raw, size_t q_raw_bytes, int64_t q_raw_stride,
+                       const void* k_raw, size_t k_raw_bytes, int64_t k_raw_stride,
+                       const void* gate_raw, size_t gate_raw_bytes, int64_t gate_raw_stride,
+                       const void* beta_raw, size_t beta_raw_bytes, int64_t beta_raw_stride,
+                       const float* a_log, size_t a_log_bytes, const float* dt_bias, size_t dt_bias_bytes,
+                       float q_scale, float eps,
+                       uint16_t* q, size_t q_bytes, uint16_t* k, size_t k_bytes,
+                       uint16_t* g, size_t g_bytes, uint16_t* beta, size_t beta_bytes, hipStream_t stream);
+
+/*
+ * kda_prepare_inputs_backward -- gradients of kda_prepare_inputs for the
+ * cotangents dq, dk, dg [T, H, K] and dbeta [T, H], FP32 as kda_backward
+ * writes them:
+ *   dq_raw, dk_raw, dgate_raw [T, H, K] and dbeta_raw [T, H] in dtype (dense);
+ *   da_log [H] and ddt_bias [H, K] FP32, sums over the tokens (ddt_bias NULL
+ *   exactly when dt_bias is NULL).
+ * The rounding of q, k, g and beta to BF16 counts as the identity.
+ * Workspace: kda_prepare_inputs_backward_workspace_bytes(T, H, K) bytes.
+ */
+int kda_prepare_inputs_backward(int32_t T, int32_t H, int32_t K, int32_t dtype,
+                                const void* q_raw, size_t q_raw_bytes, int64_t q_raw_stride,
+                                const void* k_raw, size_t k_raw_bytes, int64_t k_raw_stride,
+                                const void* gate_raw, size_t gate_raw_bytes, int64_t gate_raw_stride,
+                                const void* beta_raw, size_t beta_raw_bytes, int64_t beta_raw_stride,
+                                const float* a_log, size_t a_log_bytes, const float* dt_bias, size_t dt_bias_bytes,
+                                float q_scale, float eps,
+                                const float* dq, size_t dq_bytes, const float* dk, size_t dk_bytes,
+                                const float* dg, size_t dg_bytes, const float* dbeta, size_t dbeta_bytes,
+                                void* dq_raw, size_t dq_raw_bytes, void* dk_raw, size_t dk_raw_bytes,
+                                void* dgate_raw, size_t dgate_raw_bytes, void* dbeta_raw, size_t dbeta_raw_bytes,
+                                float* da_log, size_t da_log_bytes, float* ddt_bias, size_t ddt_bias_bytes,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t kda_prepare_inputs_backward_workspace_bytes(int32_t T, int32_t H, int32_t K);
+
+/*
+ * kda_output_norm -- the norm after the recurrence with its gate and residual
+ * scale, per (token, head) row over V channels (any V up to 8192; H = 1 gives
+ * a norm over whole rows):
+ *     y = residual + res_scale[h, v] * act(gate) * weight[v] * o / sqrt(mean_v o^2 + eps)
+ *   o         [T, H, V] in o_format (kda_forward's o, or any activation)
+ *   gate      [T, H, V] dtype with a token stride, NULL exactly when
+ *             activation is KDA_ACT_NONE
+ *   weight    [V]; res_scale [H, V] or NULL (one); residual [T, H, V] dtype or
+ *             NULL (zero)
+ *   y         [T, H, V] dtype; it may be the residual itself, in place
+ */
+int kda_output_norm(int32_t T, int32_t H, int32_t V, const void* o, size_t o_bytes, int32_t o_format,
+                    const void* gate, size_t gate_bytes, int64_t gate_stride, int32_t activation,
+                    const float* weight, size_t weight_bytes, const float* res_scale, size_t res_scale_bytes,
+                    const void* residual, size_t residual_bytes, int32_t dtype, float eps,
+                    void* y, size_t y_bytes, hipStream_t stream);
+
+/*
+ * kda_output_norm_backward -- gradients of kda_output_norm for the cotangent
+ * dy [T, H, V] dtype:
+ *   d_o          [T, H, V] in d_o_format (kda_backward takes FP32)
+ *   d_gate       [T, H, V] dtype, dense; NULL exactly when there is no gate
+ *   d_weight     [V]; d_res_scale [H, V], NULL exactly when res_scale is NULL
+ * The residual's gradient is dy itself.
+ * Workspace: kda_output_norm_backward_workspace_bytes(T, H, V) bytes.
+ */
+int kda_output_norm_backward(int32_t T, int32_t H, int32_t V, const void* dy, size_t dy_bytes,
+                             const void* o, size_t o_bytes, int32_t o_format,
+                             const void* gate, size_t gate_bytes, int64_t gate_stride, int32_t activation,
+                             const float* weight, size_t weight_bytes,
+                             const float* res_scale, size_t res_scale_bytes, int32_t dtype, float eps,
+                             void* d_o, size_t d_o_bytes, int32_t d_o_format, void* d_gate, size_t d_gate_bytes,
+                             float* d_weight, size_t d_weight_bytes,
+                             float* d_res_scale, size_t d_res_scale_bytes,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t kda_output_norm_backward_workspace_bytes(int32_t T, int32_t H, int32_t V);
+
+/*
+ * kda_scan_forward -- a gated linear recurrence with one state per channel
+ * over the plan's packed sequences: for every channel d of D,
+ *     h_t = exp(g_t) h_{t-1} + u_t,   u_t = x_t, or (1 - exp(g_t)) x_t when tied
+ * where h before a sequence's first token is its initial state.
+ *   x, g           [T, D] dtype, each with its own token stride; g <= 0,
+ *                  finite or -inf (exp(-inf) = 0 forgets the channel)
+ *   tied           0 or 1
+ *   initial_state  [N, D] FP32 or NULL (zero)
+ *   h              [T, D] in h_format; final_state [N, D] FP32
+ * The plan's segments are the tokens that run at the same time where the
+ * sequences and channels alone are too few to fill the GPU; they change
+ * results by rounding only.  Workspace: kda_scan_workspace_bytes(plan, D)
+ * bytes, NULL where that is 0 (no segment cuts a sequence).
+ */
+int kda_scan_forward(const kda_plan* plan, const int32_t* plan_dev, size_t plan_dev_bytes, int32_t D, int32_t dtype,
+                     const void* x, size_t x_bytes, int64_t x_stride, const void* g, size_t g_bytes, int64_t g_stride,
+                     int32_t tied, const float* initial_state, size_t initial_state_bytes,
+                     void* h, size_t h_bytes, int32_t h_format, float* final_state, size_t final_state_bytes,
+                     void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * kda_scan_backward -- gradients of kda_scan_forward: with the cotangents dh
+ * [T, D] (in h_format) of h and d_final [N, D] (FP32, or NULL for zero) of the
+ * final states, and within every sequence
+ *     l_t = dh_t + exp(g_{t+1}) l_{t+1}   (l_T = dh_T + d_final)
+ *     dx_t = l_t, or (1 - exp(g_t)) l_t when tied
+ *     dg_t = l_t exp(g_t) (h_{t-1} - (tied ? x_t : 0))
+ *     d_initial_state = exp(g_1) l_1
+ *   h              [T, D] in h_format, as the forward wrote it (its rounding
+ *                  to BF16, if any, enters dg)
+ *   dx, dg         [T, D] dtype, dense; d_initial_state [N, D] FP32 or NULL
+ *   x              read when tied only; NULL is allowed otherwise
+ * Workspace as for kda_scan_forward.
+ */
+int kda_scan_backward(const kda_plan* plan, const int32_t* plan_dev, size_t plan_dev_bytes, int32_t D, int32_t dtype,
+                      const void* x, size_t x_bytes, int64_t x_stride,
+                      const void* g, size_t g_bytes, int64_t g_stride, int32_t tied,
+                      const float* initial_state, size_t initial_state_bytes,
+                      const void* h, size_t h_bytes, const void* dh, size_t dh_bytes, int32_t h_format,
+                      const float* d_final, size_t d_final_bytes,
+                      void* dx, size_t dx_bytes, void* dg, size_t dg_bytes,
+                      float* d_initial_state, size_t d_initial_state_bytes,
+                      void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t kda_scan_workspace_bytes(const kda_plan* plan, int32_t D);
+
+/*
+ * Single tokens over a pool of states (kda_scan_step, kda_step).  Row b of the
+ * batch is the next token of the sequence whose state lies in slot slots[b] of
+ * the pool; slots NULL means slot b.
+ *   - A slot outside [0, num_slots) marks an unused row: its output row and
+ *     every state stay as they were.
+ *   - Rows that name the same slot are consecutive tokens of that sequence, in
+ *     the order of the rows.
+ *   - state is read and state_out written, for the slots that rows name; the
+ *     other slots of state_out stay as they were.  state_out may be state
+ *     itself (the usual case); ranges that overlap otherwise give
+ *     KDA_ERR_INVALID_ARG.
+ * The slots are read on the device, so a captured call follows what they hold
+ * at each replay.  num_slots >= 1, and >= B where slots is NULL.
+ *
+ * kda_scan_step -- one token of the recurrence of kda_scan_forward:
+ *   x, g   [B, D] dtype (dense); state, state_out [num_slots, D] FP32
+ *   h      [B, D] dtype
+ */
+int kda_scan_step(int32_t B, int32_t D, int32_t dtype, const void* x, size_t x_bytes, const void* g, size_t g_bytes,
+                  int32_t tied, const int32_t* slots, size_t slots_bytes, int32_t num_slots,
+                  const float* state, size_t state_bytes, float* state_out, size_t state_out_bytes,
+                  void* h, size_t h_bytes, hipStream_t stream);
+
+/*
+ * kda_step -- one token of the KDA recurrence (kda_forward's, from a state as
+ * it writes final_state):
+ *   q, k, g  [B, H, K] bf16, v [B, H, V] bf16, beta [B, H] bf16 (K = V = 128)
+ *   gate_lower_bound  the safe gate, as for kda_forward
+ *   state, state_out  [num_slots, H, K, V] FP32
+ *   o        [B, H, V] in o_format
+ * The head range works as for kda_forward.
+ */
+int kda_step(int32_t B, int32_t H, int32_t K, int32_t V, int32_t head_begin, int32_t head_count,
+             const uint16_t* q, size_t q_bytes, const uint16_t* k, size_t k_bytes,
+             const uint16_t* v, size_t v_bytes, const uint16_t* g, size_t g_bytes,
+             const uint16_t* beta, size_t beta_bytes, float gate_lower_bound,
+             const int32_t* slots, size_t slots_bytes, int32_t num_slots,
+             const float* state, size_t state_bytes, float* state_out, size_t state_out_bytes,
+             void* o, size_t o_bytes, int32_t o_format, hipStream_t stream);
+
 /* Human-readable name of a kda_status value. */
 const char* kda_status_string(int status);
 
