@@ -14,15 +14,23 @@ namespace kda {
 // Element storage: FP32 or the raw bits of a bf16.
 typedef float fp32_t;
 typedef uint16_t bf16_t;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// VEC (1 or 8) neighbouring elements at p as FP32.  With VEC = 8, p is
-// aligned to 16 bytes.
+// VEC (1, 4 or 8) neighbouring elements at p as FP32.  p is aligned to the
+// bytes loaded, or to 16.
 template <int VEC>
 __device__ __forceinline__ void load(const bf16_t* p, float (&x)[VEC]) {
   if constexpr (VEC == 8) {
     const u32x4 w = *reinterpret_cast<const u32x4*>(p);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else if constexpr (VEC == 4) {
+    const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
       x[2 * i] = __uint_as_float(w[i] << 16);
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
@@ -40,6 +48,10 @@ __device__ __forceinline__ void load(const fp32_t* p, float (&x)[VEC]) {
       x[i] = a[i];
       x[4 + i] = b[i];
     }
+  } else if constexpr (VEC == 4) {
+    const f32x4 a = ld4(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = a[i];
   } else {
     static_assert(VEC == 1, "");
     x[0] = *p;
@@ -54,6 +66,11 @@ __device__ __forceinline__ void store(bf16_t* p, const float (&x)[VEC]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
     *reinterpret_cast<u32x4*>(p) = w;
+  } else if constexpr (VEC == 4) {
+    u32x2 w;
+    w[0] = pack_bf16(x[0], x[1]);
+    w[1] = pack_bf16(x[2], x[3]);
+    *reinterpret_cast<u32x2*>(p) = w;
   } else {
     *p = static_cast<uint16_t>(pack_bf16(x[0], 0.f));
   }
@@ -69,6 +86,11 @@ __device__ __forceinline__ void store(fp32_t* p, const float (&x)[VEC]) {
     }
     st4(p, a);
     st4(p + 4, b);
+  } else if constexpr (VEC == 4) {
+    f32x4 a;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = x[i];
+    st4(p, a);
   } else {
     *p = x[0];
   }
@@ -95,6 +117,74 @@ __device__ __forceinline__ float sum64(float x) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+
+// Raw storage of VEC elements, so that a load can stay in flight unconverted.
+template <typename E, int VEC>
+struct RawVec {
+  E e[VEC];
+};
+template <>
+struct RawVec<bf16_t, 8> {
+  u32x4 w;
+};
+template <>
+struct RawVec<fp32_t, 8> {
+  f32x4 a, b;
+};
+template <>
+struct RawVec<bf16_t, 4> {
+  u32x2 w;
+};
+template <>
+struct RawVec<fp32_t, 4> {
+  f32x4 a;
+};
+template <typename E, int VEC>
+__device__ __forceinline__ void load_raw(const E* p, RawVec<E, VEC>& r) {
+  static_assert(VEC == 1, "");
+  r.e[0] = *p;
+}
+template <>
+__device__ __forceinline__ void load_raw<bf16_t, 8>(const bf16_t* p, RawVec<bf16_t, 8>& r) {
+  r.w = *reinterpret_cast<const u32x4*>(p);
+}
+template <>
+__device__ __forceinline__ void load_raw<fp32_t, 8>(const fp32_t* p, RawVec<fp32_t, 8>& r) {
+  r.a = ld4(p);
+  r.b = ld4(p + 4);
+}
+template <>
+__device__ __forceinline__ void load_raw<bf16_t, 4>(const bf16_t* p, RawVec<bf16_t, 4>& r) {
+  r.w = *reinterpret_cast<const u32x2*>(p);
+}
+template <>
+__device__ __forceinline__ void load_raw<fp32_t, 4>(const fp32_t* p, RawVec<fp32_t, 4>& r) {
+  r.a = ld4(p);
+}
+__device__ __forceinline__ float element(const RawVec<bf16_t, 1>& r, int) { return bf2f(r.e[0]); }
+__device__ __forceinline__ float element(const RawVec<fp32_t, 1>& r, int) { return r.e[0]; }
+__device__ __forceinline__ float element(const RawVec<bf16_t, 8>& r, int i) {
+  return __uint_as_float(i % 2 == 0 ? r.w[i / 2] << 16 : r.w[i / 2] & 0xffff0000u);
+}
+__device__ __forceinline__ float element(const RawVec<bf16_t, 4>& r, int i) {
+  return __uint_as_float(i % 2 == 0 ? r.w[i / 2] << 16 : r.w[i / 2] & 0xffff0000u);
+}
+__device__ __forceinline__ float element(const RawVec<fp32_t, 4>& r, int i) { return r.a[i]; }
+__device__ __forceinline__ float element(const RawVec<fp32_t, 8>& r, int i) { return i < 4 ? r.a[i] : r.b[i - 4]; }
+
+// 1 - e^g for g <= 0, given a = e^g.  The difference cancels near 0, where a
+// Taylor sum of the terms to g^8 / 8! is exact to 2^-25 (|g| < 3/8).
+__device__ __forceinline__ float one_minus_exp(float g, float a) {
+  float s = 1.f / 40320.f;
+  s = s * g + 1.f / 5040.f;
+  s = s * g + 1.f / 720.f;
+  s = s * g + 1.f / 120.f;
+  s = s * g + 1.f / 24.f;
+  s = s * g + 1.f / 6.f;
+  s = s * g + 0.5f;
+  s = s * g + 1.f;
+  return g > -0.375f ? -g * s : 1.f - a;
+}
 
 __device__ __forceinline__ float sigmoidf(float z) { return 1.f / (1.f + __expf(-z)); }
 
