@@ -101,8 +101,19 @@ NormBwdLayout norm_bwd_layout(int32_t T, int32_t H, int32_t V, const NormShape& 
 size_t norm_bwd_workspace(int32_t T, int32_t H, int32_t V);
 bool norm_vector_rows(const NormArgs& a);
 
-// Summaries (decay product and state) of every fragment and channel.
-size_t scan_workspace(const kda_plan* plan, int32_t D);
+// The scan's tiles: kScanTile tokens of kScanChannels channels, one workgroup
+// each.  More than one token tile need words of workspace in which tiles leave
+// their maps (8 bytes a channel) and end states (4), and a ticket counter a
+// channel block on a cache line of its own (byte offsets).
+constexpr int kScanThreads = 256;
+constexpr int kScanTile = 128;
+constexpr int kScanChannels = 64;
+constexpr int64_t kMaxScanStride = 1 << 22;   // byte offsets inside a tile stay below 2^32
+struct ScanLayout {
+  int32_t tiles, columns;
+  size_t tickets, maps, states, total;
+};
+ScanLayout scan_layout(int32_t T, int32_t D);
 
 int check_prepare(const PrepareArgs& a, bool backward);
 int check_norm(const NormArgs& a, bool backward);

@@ -199,7 +199,7 @@ int kda_scan_backward(const kda_plan* plan, const int32_t* plan_dev, size_t plan
 }
 
 size_t kda_scan_workspace_bytes(const kda_plan* plan, int32_t D) {
-  return plan == nullptr || D <= 0 ? 0 : kda::scan_workspace(plan, D);
+  return plan == nullptr || D <= 0 || D > (1 << 20) ? 0 : kda::scan_layout(plan->T, D).total;
 }
 
 int kda_scan_step(int32_t B, int32_t D, int32_t dtype, const void* x, size_t x_bytes, const void* g, size_t g_bytes,

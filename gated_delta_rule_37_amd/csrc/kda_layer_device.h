@@ -16,8 +16,13 @@ typedef float fp32_t;
 typedef uint16_t bf16_t;
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// VEC (1, 4 or 8) neighbouring elements at p as FP32.  p is aligned to the
-// bytes loaded, or to 16.
+// Vectors at any address that suits their elements (the hardware reads and
+// writes them whole; aligned ones cost nothing extra).
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
+// VEC (1, 4 or 8) neighbouring elements at p as FP32.  With VEC = 8, p is
+// aligned to 16 bytes; with VEC = 4 to the element.
 template <int VEC>
 __device__ __forceinline__ void load(const bf16_t* p, float (&x)[VEC]) {
   if constexpr (VEC == 8) {
@@ -28,7 +33,7 @@ __device__ __forceinline__ void load(const bf16_t* p, float (&x)[VEC]) {
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   } else if constexpr (VEC == 4) {
-    const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+    const u32x2 w = *reinterpret_cast<const u32x2_any*>(p);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       x[2 * i] = __uint_as_float(w[i] << 16);
@@ -49,7 +54,7 @@ __device__ __forceinline__ void load(const fp32_t* p, float (&x)[VEC]) {
       x[4 + i] = b[i];
     }
   } else if constexpr (VEC == 4) {
-    const f32x4 a = ld4(p);
+    const f32x4 a = *reinterpret_cast<const f32x4_any*>(p);
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = a[i];
   } else {
@@ -70,7 +75,7 @@ __device__ __forceinline__ void store(bf16_t* p, const float (&x)[VEC]) {
     u32x2 w;
     w[0] = pack_bf16(x[0], x[1]);
     w[1] = pack_bf16(x[2], x[3]);
-    *reinterpret_cast<u32x2*>(p) = w;
+    *reinterpret_cast<u32x2_any*>(p) = w;
   } else {
     *p = static_cast<uint16_t>(pack_bf16(x[0], 0.f));
   }
@@ -90,7 +95,7 @@ __device__ __forceinline__ void store(fp32_t* p, const float (&x)[VEC]) {
     f32x4 a;
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = x[i];
-    st4(p, a);
+    *reinterpret_cast<f32x4_any*>(p) = a;
   } else {
     *p = x[0];
   }
@@ -139,6 +144,17 @@ template <>
 struct RawVec<fp32_t, 4> {
   f32x4 a;
 };
+// Makes what follows compute from the raw registers again, instead of keeping
+// the values that were computed from them before alive.
+__device__ __forceinline__ void forget(RawVec<bf16_t, 1>& r) {
+  uint32_t w = r.e[0];
+  asm volatile("" : "+v"(w));
+  r.e[0] = static_cast<bf16_t>(w);
+}
+__device__ __forceinline__ void forget(RawVec<fp32_t, 1>& r) { asm volatile("" : "+v"(r.e[0])); }
+__device__ __forceinline__ void forget(RawVec<bf16_t, 4>& r) { asm volatile("" : "+v"(r.w)); }
+__device__ __forceinline__ void forget(RawVec<fp32_t, 4>& r) { asm volatile("" : "+v"(r.a)); }
+
 template <typename E, int VEC>
 __device__ __forceinline__ void load_raw(const E* p, RawVec<E, VEC>& r) {
   static_assert(VEC == 1, "");
@@ -155,11 +171,11 @@ __device__ __forceinline__ void load_raw<fp32_t, 8>(const fp32_t* p, RawVec<fp32
 }
 template <>
 __device__ __forceinline__ void load_raw<bf16_t, 4>(const bf16_t* p, RawVec<bf16_t, 4>& r) {
-  r.w = *reinterpret_cast<const u32x2*>(p);
+  r.w = *reinterpret_cast<const u32x2_any*>(p);
 }
 template <>
 __device__ __forceinline__ void load_raw<fp32_t, 4>(const fp32_t* p, RawVec<fp32_t, 4>& r) {
-  r.a = ld4(p);
+  r.a = *reinterpret_cast<const f32x4_any*>(p);
 }
 __device__ __forceinline__ float element(const RawVec<bf16_t, 1>& r, int) { return bf2f(r.e[0]); }
 __device__ __forceinline__ float element(const RawVec<fp32_t, 1>& r, int) { return r.e[0]; }
@@ -172,21 +188,23 @@ __device__ __forceinline__ float element(const RawVec<bf16_t, 4>& r, int i) {
 __device__ __forceinline__ float element(const RawVec<fp32_t, 4>& r, int i) { return r.a[i]; }
 __device__ __forceinline__ float element(const RawVec<fp32_t, 8>& r, int i) { return i < 4 ? r.a[i] : r.b[i - 4]; }
 
-// 1 - e^g for g <= 0, given a = e^g.  The difference cancels near 0, where a
-// Taylor sum of the terms to g^8 / 8! is exact to 2^-25 (|g| < 3/8).
+// 1 - e^g for g <= 0, given a = e^g.  The difference cancels near 0; above
+// -1/4 the Taylor sum to g^6 / 6! replaces it, exact to 2^-24 relative.
 __device__ __forceinline__ float one_minus_exp(float g, float a) {
-  float s = 1.f / 40320.f;
-  s = s * g + 1.f / 5040.f;
-  s = s * g + 1.f / 720.f;
+  float s = 1.f / 720.f;
   s = s * g + 1.f / 120.f;
   s = s * g + 1.f / 24.f;
   s = s * g + 1.f / 6.f;
   s = s * g + 0.5f;
   s = s * g + 1.f;
-  return g > -0.375f ? -g * s : 1.f - a;
+  return g > -0.25f ? -g * s : 1.f - a;
 }
 
-__device__ __forceinline__ float sigmoidf(float z) { return 1.f / (1.f + __expf(-z)); }
+// e^x by the hardware's 2^x: relative error about 1 + |x| units of 2^-24,
+// results below 2^-126 are 0.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+__device__ __forceinline__ float sigmoidf(float z) { return __builtin_amdgcn_rcpf(1.f + fast_exp(-z)); }
 
 }  // namespace kda
 

@@ -127,9 +127,17 @@ bool norm_vector_rows(const NormArgs& a) {
   return a.V % 8 == 0 && (a.gate.ptr == nullptr || a.gate.stride * static_cast<int64_t>(size_of(a.dtype)) % 16 == 0);
 }
 
-size_t scan_workspace(const kda_plan* plan, int32_t D) {
-  if (plan->F == plan->N) return 0;
-  return 2 * up256(static_cast<size_t>(plan->F) * static_cast<size_t>(D) * sizeof(float));
+ScanLayout scan_layout(int32_t T, int32_t D) {
+  ScanLayout L{};
+  L.tiles = static_cast<int32_t>((static_cast<int64_t>(T) + kScanTile - 1) / kScanTile);
+  L.columns = (D + kScanChannels - 1) / kScanChannels;
+  if (L.tiles == 1) return L;
+  const size_t cells = static_cast<size_t>(L.tiles) * static_cast<size_t>(L.columns) * kScanChannels;
+  L.tickets = 0;
+  L.maps = static_cast<size_t>(L.columns) * 128;
+  L.states = L.maps + cells * 8;
+  L.total = L.states + cells * 4;
+  return L;
 }
 
 int check_prepare(const PrepareArgs& a, bool backward) {
@@ -211,6 +219,7 @@ int check_scan(const ScanArgs& a, bool backward) {
                nh = n * size_of(a.h_format), state = static_cast<size_t>(a.plan->N) * D * 4;
   int st = first_error({need_x ? check_stride(a.x, a.D) : KDA_OK, check_stride(a.g, a.D)});
   if (st != KDA_OK) return st;
+  if ((need_x && a.x.stride > kMaxScanStride) || a.g.stride > kMaxScanStride) return KDA_ERR_UNSUPPORTED;
   st = check_buffers({{a.plan_dev.ptr, a.plan_dev.bytes, a.plan->blob.size() * sizeof(int32_t), false},
                       {a.x.ptr, a.x.bytes, need_x ? rows_need(a.x, T, D, e) : 0, !need_x},
                       {a.g.ptr, a.g.bytes, rows_need(a.g, T, D, e), false},
@@ -224,7 +233,7 @@ int check_scan(const ScanArgs& a, bool backward) {
                       {a.dg.ptr, a.dg.bytes, n * e, !backward},
                       {a.d_initial_state.ptr, a.d_initial_state.bytes, state, true}});
   if (st != KDA_OK) return st;
-  return check_workspace(a.workspace, scan_workspace(a.plan, a.D));
+  return check_workspace(a.workspace, scan_layout(a.plan->T, a.D).total);
 }
 
 int check_scan_step(const ScanStepArgs& a) {

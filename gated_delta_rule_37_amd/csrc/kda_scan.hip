@@ -7,14 +7,18 @@
 //
 // A run of tokens is the map h -> A h + B, A the product of its decays and B
 // its end state from zero; two neighbouring runs compose to
-// (A2 A1, A2 B1 + B2).  A workgroup owns a few channels of one sequence and
-// walks its tokens in tiles, the whole sequence's state never leaving it: a
-// thread scans R tokens of VEC channels in registers, the threads' maps are
-// composed across the wave by shuffles and across the waves through LDS, and
-// every state follows as (state from zero) + (product of decays) * carry.  So
-// each element is read and written once, HBM bandwidth being the bound.
+// (A2 A1, A2 B1 + B2).  A sequence's first token is the constant map
+// (0, a_1 h_0 + u_1), so packed sequences need nothing else.
+//
+// One pass: a workgroup keeps a tile of kScanTile tokens of 64 channels in
+// registers (a 128-byte line of bf16 a row), scans it from zero, publishes its
+// map, gets the state before its tile from the maps of the tiles before it
+// (look_back), publishes the state behind it, and only then walks its tokens
+// from that state and writes.  Each element is read and written once, HBM bandwidth being the bound.
 #include "kda_layer.h"
 #include "kda_layer_device.h"
+
+#include <type_traits>
 
 #include "kda.h"
 
@@ -25,7 +29,6 @@ struct ScanParams {
   const int32_t* plan;
   BlobLayout L;
   int32_t T, N, F, D;
-  int32_t tied;
   const void *x, *g;
   int64_t x_stride, g_stride;
   const float *initial_state, *d_final;
@@ -34,270 +37,446 @@ struct ScanParams {
   const void *h_in, *dh;
   void *dx, *dg;
   float* d_initial_state;
-  int32_t blocks, bundles;   // channel blocks, and bundles of them, of a unit
-  int64_t total_bundles;
+  int32_t tiles, columns;   // token tiles, channel blocks
+  uint32_t* tickets;        // [columns] 32 words apart
+  uint64_t* maps;           // [tiles][columns][64]: A, B of a tile
+  uint32_t* states;         // [tiles][columns][64]: the state behind a tile
 };
 
-// The first fragment of sequence n: n itself where no segment cuts a
-// sequence, else found in the sorted frag_seq.
-__device__ __forceinline__ int32_t first_fragment(const ScanParams& p, int32_t n) {
-  if (p.F == p.N) return n;
+// LPR lanes of VEC channels make a row of 64 channels; a thread takes R
+// tokens, so that every geometry has the same tile.
+template <int VEC_, int LPR_, int R_>
+struct Geometry {
+  static constexpr int VEC = VEC_, LPR = LPR_, R = R_;
+  static_assert(VEC * LPR == kScanChannels && kScanThreads / LPR * R == kScanTile, "");
+};
+static_assert(kScanTile < kScanThreads, "a thread for each token boundary of a tile");
+
+// The map (A, B) of h; a constant map (A = 0, as a sequence's start gives) is B
+// whatever h is, so that an infinity or NaN stays in its own sequence.
+__device__ __forceinline__ float apply(float A, float B, float h) { return A == 0.f ? B : __fmaf_rn(A, h, B); }
+
+// ------------------------------------------------ the tiles' maps and states
+// Words that other workgroups wait for carry their own readiness: all ones
+// until written (a NaN that no arithmetic here gives: NaNs are written as the
+// canonical one).  So no ordering between words is needed, only agent-scope
+// atomics, which reach past the XCDs' own L2 caches.
+constexpr uint32_t kEmpty = 0xffffffffu;
+__device__ __forceinline__ uint32_t float_bits(float x) { return x != x ? 0x7fc00000u : __float_as_uint(x); }
+
+// The next tile of this workgroup's channel block.  Tickets are handed out in
+// the order of the tiles, so every tile before this one belongs to a workgroup
+// that already runs, and the oldest of them waits for nothing: all waits end.
+__device__ __forceinline__ int32_t take_ticket(const ScanParams& p, int32_t column, uint32_t* box) {
+  if (p.tiles == 1) return 0;
+  if (threadIdx.x == 0) {
+    *box = __hip_atomic_fetch_add(p.tickets + column * 32, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
+  }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(static_cast<int32_t>(*box));
+}
+
+__device__ __forceinline__ int64_t word_of(const ScanParams& p, int32_t tile, int32_t column) {
+  return (static_cast<int64_t>(tile) * p.columns + column) * kScanChannels;
+}
+
+// The state before tile `tile`, for this wave's lane: channel `lane` of the
+// block.  Looks at the kLook tiles before it until, for every channel, one of
+// them has its state and those after it their maps, then applies those maps in
+// order: exactly what each of these tiles does itself, so the result does not
+// depend on which states were there.  Polls are bounded, so that a workspace
+// that another call overwrites gives NaN instead of a hang.
+constexpr int kLook = 4;
+constexpr int kMaxPolls = 1 << 22;
+__device__ __forceinline__ float look_back(const ScanParams& p, int32_t tile, int32_t column) {
+  const int32_t lane = threadIdx.x & 63;
+  for (int polls = 0; polls < kMaxPolls; ++polls) {
+    uint32_t state[kLook];
+    uint64_t map[kLook];
+#pragma unroll
+    for (int i = 0; i < kLook; ++i) {
+      const int64_t w = word_of(p, max(tile - 1 - i, 0), column);
+      state[i] = __hip_atomic_load(p.states + w + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      map[i] = __hip_atomic_load(p.maps + w + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    bool have = false;
+    float h = 0.f;
+#pragma unroll
+    for (int i = kLook - 1; i >= 0; --i) {
+      if (i >= tile) continue;
+      const uint32_t a = static_cast<uint32_t>(map[i]);
+      if (state[i] != kEmpty) {
+        h = __uint_as_float(state[i]);
+        have = true;
+      } else if (a == kEmpty) {
+        have = false;
+      } else {
+        h = apply(__uint_as_float(a), __uint_as_float(static_cast<uint32_t>(map[i] >> 32)), h);
+      }
+    }
+    if (__ballot(!have) == 0) return h;
+    __builtin_amdgcn_s_sleep(1);
+  }
+  return __uint_as_float(0x7fc00000u);
+}
+
+// ------------------------------------------------ sequence boundaries
+// mark[i] = n + 1 where sequence n begins at token base + i, for i in
+// [0, kScanTile], and N + 1 at the tokens' end; else 0.  Returns whether the
+// tile has any.  The whole workgroup calls.
+__device__ __forceinline__ bool mark_sequences(const ScanParams& p, int32_t base, int32_t* mark) {
+  const int32_t from = max(base, 0);
   int32_t lo = 0, hi = p.F;
   while (lo < hi) {
     const int32_t mid = (lo + hi) >> 1;
-    if (p.plan[p.L.frag_seq + mid] < n) {
+    if (p.plan[p.L.frag_begin + mid] < from) {
       lo = mid + 1;
     } else {
       hi = mid;
     }
   }
-  return lo;
-}
-__device__ __forceinline__ int32_t sequence_begin(const ScanParams& p, int32_t n) {
-  return n >= p.N ? p.T : p.plan[p.L.frag_begin + first_fragment(p, n)];
-}
-
-// A workgroup's work: sequence n, channels from `channel`, and its tokens.
-// Workgroups go round the 8 XCDs in launch order; neighbouring channel blocks
-// share cache lines, so a bundle of kBundle blocks stays on one XCD.
-constexpr int kXcds = 8;
-struct Unit {
-  int32_t n, block, begin, end;
-};
-template <int BUNDLE>
-__device__ __forceinline__ bool unit_of(const ScanParams& p, Unit& u) {
-  const uint32_t id = blockIdx.x, xcd = id % kXcds, i = id / kXcds;
-  const int64_t bundle = static_cast<int64_t>(i / BUNDLE) * kXcds + xcd;
-  if (bundle >= p.total_bundles) return false;
-  const int32_t seq = static_cast<int32_t>(bundle / p.bundles);
-  u.block = static_cast<int32_t>(bundle - static_cast<int64_t>(seq) * p.bundles) * BUNDLE + static_cast<int32_t>(i % BUNDLE);
-  if (u.block >= p.blocks) return false;
-  u.n = seq;
-  u.begin = sequence_begin(p, u.n);
-  u.end = sequence_begin(p, u.n + 1);
-  return true;
+  for (int32_t i = threadIdx.x; i <= kScanTile; i += kScanThreads) mark[i] = 0;
+  __syncthreads();
+  bool any = false;
+  // at most kScanTile + 1 fragments begin here: one a thread
+  const int32_t f = lo + static_cast<int32_t>(threadIdx.x);
+  const int32_t at = f < p.F ? p.plan[p.L.frag_begin + f] : p.T;
+  if (f <= p.F && at - base <= kScanTile) {
+    const bool carried = f < p.F && (p.plan[p.L.frag_flags + f] & kFragCarried) != 0;
+    if (!carried) {
+      mark[at - base] = f < p.F ? p.plan[p.L.frag_seq + f] + 1 : p.N + 1;
+      any = true;
+    }
+  }
+  return __builtin_amdgcn_readfirstlane(__syncthreads_or(any)) != 0;   // a scalar: the callers' branches too
 }
 
-// LPR lanes of VEC channels each make a row; a thread takes R tokens.
-template <int VEC_, int LPR_, int R_, int THREADS_>
-struct Geometry {
-  static constexpr int VEC = VEC_, LPR = LPR_, R = R_, THREADS = THREADS_;
-  static constexpr int kWaves = THREADS / 64, kTile = THREADS / LPR * R, kChannels = LPR * VEC;
+// ------------------------------------------------ composition in the tile
+// A thread group is the LPR threads that share R tokens.
+template <typename G>
+struct TileLds {
+  static constexpr int kGroups = kScanThreads / G::LPR;
+  float map[kGroups][2][kScanChannels];   // the groups' maps
+  float before[kGroups][kScanChannels];   // the states before the groups
+  int32_t mark[kScanTile + 1];
+  uint32_t ticket;
 };
 
-// Composes the maps (A, B) of the thread groups before this one in the wave:
-// on return (A, B) is this group's own prefix without itself (the identity
-// for the first), and (TA, TB) the whole wave's.  Groups are LPR lanes apart.
-template <int VEC, int LPR>
-__device__ __forceinline__ void wave_scan(float (&A)[VEC], float (&B)[VEC], float (&TA)[VEC], float (&TB)[VEC]) {
-  const int32_t lane = threadIdx.x & 63;
+// Given the thread group's map (A, B), the state before it; publishes the
+// tile's map and the state behind the tile.  The first wave works alone, a
+// lane a channel, from group to group.
+template <typename G>
+__device__ __forceinline__ void tile_states(const ScanParams& p, int32_t tile, int32_t column, TileLds<G>& lds,
+                                            const float (&A)[G::VEC], const float (&B)[G::VEC], float (&in)[G::VEC]) {
+  constexpr int VEC = G::VEC, kGroups = TileLds<G>::kGroups;
+  const int32_t lane = threadIdx.x & 63, group = threadIdx.x / G::LPR, c0 = (threadIdx.x % G::LPR) * VEC;
+  store<VEC>(&lds.map[group][0][c0], A);
+  store<VEC>(&lds.map[group][1][c0], B);
+  __syncthreads();
+  if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) == 0) {
+    float state = 0.f;
+    if (p.tiles > 1) {
+      float a = 1.f, b = 0.f;
 #pragma unroll
-  for (int off = LPR; off < 64; off *= 2) {
+      for (int i = 0; i < kGroups; ++i) {
+        const float ga = lds.map[i][0][lane];
+        b = apply(ga, lds.map[i][1][lane], b);
+        a *= ga;
+      }
+      const int64_t w = word_of(p, tile, column) + lane;
+      if (tile > 0) {
+        __hip_atomic_store(p.maps + w, static_cast<uint64_t>(float_bits(b)) << 32 | float_bits(a), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+        state = look_back(p, tile, column);
+      }
+      __hip_atomic_store(p.states + w, float_bits(apply(a, b, state)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const float a = __shfl_up(A[i], off), b = __shfl_up(B[i], off);
-      if (lane >= off) {
-        B[i] += A[i] * b;
-        A[i] *= a;
+    for (int i = 0; i < kGroups; ++i) {
+      lds.before[i][lane] = state;
+      state = apply(lds.map[i][0][lane], lds.map[i][1][lane], state);
+    }
+  }
+  __syncthreads();
+  load<VEC>(&lds.before[group][c0], in);
+}
+
+// A thread's rows of a tensor: an address that the whole workgroup shares and
+// a 32-bit byte offset (kMaxScanStride keeps a tile's within 2^32), so that a
+// row costs no address registers.
+template <typename E>
+struct Span {
+  const char* base;   // token `from`, channel 0
+  int64_t step;       // bytes from a token to the next
+  __device__ __forceinline__ Span(const void* p, int64_t stride, int64_t from)
+      : base(static_cast<const char*>(p) + from * stride * static_cast<int64_t>(sizeof(E))),
+        step(stride * static_cast<int64_t>(sizeof(E))) {}
+  __device__ __forceinline__ uint32_t offset(int32_t token, int32_t channel) const {
+    return static_cast<uint32_t>(token) * static_cast<uint32_t>(step) + static_cast<uint32_t>(channel) * sizeof(E);
+  }
+  // `shift` tokens (the same for the workgroup) from the one at `offset`
+  __device__ __forceinline__ E* at(uint32_t offset, int32_t shift) const {
+    return reinterpret_cast<E*>(const_cast<char*>(base + shift * step) + offset);
+  }
+};
+
+// Rows row, row + DIR, ... (tokens from the span's first) of channel dl; where
+// not FULL, limited to [0, most].
+template <int DIR, bool FULL, int VEC, int R, typename E>
+__device__ __forceinline__ void fetch_rows(const Span<E>& s, int32_t row, int32_t dl, int32_t most, RawVec<E, VEC> (&x)[R]) {
+  const uint32_t off = s.offset(row, dl);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if constexpr (FULL) {
+      load_raw<E, VEC>(s.at(off, DIR * r), x[r]);
+    } else {
+      load_raw<E, VEC>(s.at(s.offset(max(min(row + DIR * r, most), 0), dl), 0), x[r]);
+    }
+  }
+}
+
+template <typename F>
+__device__ __forceinline__ void with_flag(bool flag, F&& f) {
+  if (flag) {
+    f(std::true_type{});
+  } else {
+    f(std::false_type{});
+  }
+}
+
+// Row n of per-sequence states [N, D], or zeros where there are none.
+template <int VEC>
+__device__ __forceinline__ void load_state(const float* states, int32_t n, int32_t D, int32_t d, float (&x)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) x[i] = 0.f;
+  if (states != nullptr) load<VEC>(states + static_cast<int64_t>(n) * D + d, x);
+}
+
+// Row r's map (a, v) after the map (A, B) of the rows before it.  Unless PLAIN:
+// where a sequence begins (mark > 0, in the direction of the walk) it takes in
+// that sequence's state (row mark - less of `states`) and is constant; a row
+// that does not exist is the identity.
+template <bool PLAIN, int VEC>
+__device__ __forceinline__ void step_map(int r, int32_t mark, bool valid, const float* states, int32_t less, int32_t D,
+                                         int32_t d, float (&a)[VEC], const float (&v)[VEC], float (&A)[VEC],
+                                         float (&B)[VEC]) {
+  float b[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) b[i] = v[i];
+  if (!PLAIN) {
+    if (!valid) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        a[i] = 1.f;
+        b[i] = 0.f;
+      }
+    } else if (mark > 0) {
+      float s[VEC];
+      load_state(states, mark - less, D, d, s);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        b[i] += a[i] * s[i];
+        a[i] = 0.f;
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
-    TA[i] = __shfl(A[i], 64 - LPR + lane % LPR);
-    TB[i] = __shfl(B[i], 64 - LPR + lane % LPR);
-    const float a = __shfl_up(A[i], LPR), b = __shfl_up(B[i], LPR);
-    A[i] = lane >= LPR ? a : 1.f;
-    B[i] = lane >= LPR ? b : 0.f;
+    B[i] = r == 0 ? b[i] : PLAIN ? a[i] * B[i] + b[i] : apply(a[i], b[i], B[i]);
+    A[i] = r == 0 ? a[i] : A[i] * a[i];
   }
 }
 
-// The carry into this thread group, given its wave's prefix (A, B) and total
-// (TA, TB), and the workgroup's carry moved on behind the tile.
-template <typename G>
-__device__ __forceinline__ void tile_carry(float (*box)[2][G::kChannels], const float (&A)[G::VEC],
-                                           const float (&B)[G::VEC], const float (&TA)[G::VEC],
-                                           const float (&TB)[G::VEC], float (&carry)[G::VEC], float (&in)[G::VEC]) {
-  const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c0 = (lane % G::LPR) * G::VEC;
-  if (lane < G::LPR) {
-#pragma unroll
-    for (int i = 0; i < G::VEC; ++i) {
-      box[wave][0][c0 + i] = TA[i];
-      box[wave][1][c0 + i] = TB[i];
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < G::kWaves; ++w) {
-    if (w == wave) {
-#pragma unroll
-      for (int i = 0; i < G::VEC; ++i) in[i] = A[i] * carry[i] + B[i];
-    }
-#pragma unroll
-    for (int i = 0; i < G::VEC; ++i) carry[i] = box[w][0][c0 + i] * carry[i] + box[w][1][c0 + i];
-  }
-}
-
-template <typename E, typename O, typename G>
-__global__ __launch_bounds__(G::THREADS) void scan_kernel(ScanParams p) {
+template <typename E, typename O, typename G, bool TIED>
+__global__ __launch_bounds__(kScanThreads) void scan_kernel(ScanParams p) {
   constexpr int VEC = G::VEC, R = G::R;
-  __shared__ __align__(16) float box[2][G::kWaves][2][G::kChannels];
-  Unit u;
-  if (!unit_of<4>(p, u)) return;
+  __shared__ __align__(16) TileLds<G> lds;
+  const int32_t column = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(p.columns));
+  const int32_t tile = take_ticket(p, column, &lds.ticket);
+  if (tile >= p.tiles) return;
   const int32_t row = threadIdx.x / G::LPR * R;                                // first token in the tile
-  const int32_t d = u.block * G::kChannels + (threadIdx.x % G::LPR) * VEC;
+  const int32_t d = column * kScanChannels + (threadIdx.x % G::LPR) * VEC;
   const bool owner = d < p.D;
-  const int32_t dl = owner ? d : p.D - VEC;                                    // a channel that can be read
-  const E* x0 = static_cast<const E*>(p.x) + dl;
-  const E* g0 = static_cast<const E*>(p.g) + dl;
-  float carry[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) carry[i] = 0.f;
-  if (p.initial_state != nullptr) load<VEC>(p.initial_state + static_cast<int64_t>(u.n) * p.D + dl, carry);
-
+  // a vector inside the row: the last one shares channels with its neighbour,
+  // which computes and writes the same values
+  const int32_t dl = min(d, p.D - VEC);
+  const int32_t begin = tile * kScanTile, left = min(p.T - begin, kScanTile);
+  const Span<E> xs(p.x, p.x_stride, begin), gs(p.g, p.g_stride, begin);
+  const Span<O> hs(p.h, p.D, begin);
   RawVec<E, VEC> x[R], g[R];
-  const auto fetch = [&](int32_t tile) {
+  with_flag(left == kScanTile, [&](auto full) {
+    fetch_rows<1, full.value>(gs, row, dl, left - 1, g);
+    fetch_rows<1, full.value>(xs, row, dl, left - 1, x);
+  });
+  const bool marked = mark_sequences(p, begin, lds.mark);
+  const uint32_t out = hs.offset(row, dl);
+  // PLAIN: a whole tile inside one sequence
+  with_flag(left == kScanTile && !marked, [&](auto plain) {
+    // the map of this thread's tokens
+    constexpr bool kKeep = TIED && plain.value;   // u is kept, else x
+    float u[R][VEC], A[VEC], B[VEC], h[VEC];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t t = min(tile + row + r, u.end - 1);
-      load_raw<E, VEC>(x0 + t * p.x_stride, x[r]);
-      load_raw<E, VEC>(g0 + t * p.g_stride, g[r]);
-    }
-  };
-  fetch(u.begin);
-  int parity = 0;
-  for (int32_t tile = u.begin; tile < u.end; tile += G::kTile, parity ^= 1) {
-    // states from zero and products of decays, in this thread's tokens
-    float h[R][VEC], P[R][VEC], A[VEC], B[VEC], TA[VEC], TB[VEC], in[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      A[i] = 1.f;
-      B[i] = 0.f;
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const bool valid = tile + row + r < u.end;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float gi = element(g[r], i), xi = element(x[r], i);
-        float a = __expf(gi);
-        float v = p.tied ? one_minus_exp(gi, a) * xi : xi;
-        a = valid ? a : 1.f;
-        v = valid ? v : 0.f;
-        B[i] = a * B[i] + v;
-        A[i] *= a;
-        h[r][i] = B[i];
-        P[r][i] = A[i];
-      }
-    }
-    if (tile + G::kTile < u.end) fetch(tile + G::kTile);
-    wave_scan<VEC, G::LPR>(A, B, TA, TB);
-    tile_carry<G>(box[parity], A, B, TA, TB, carry, in);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t t = tile + row + r;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) h[r][i] += P[r][i] * in[i];
-      if (t < u.end && owner) store<VEC>(static_cast<O*>(p.h) + t * p.D + d, h[r]);
-    }
-  }
-  if (threadIdx.x < G::LPR && owner) store<VEC>(p.final_state + static_cast<int64_t>(u.n) * p.D + d, carry);
-}
-
-// The backward: tiles from the sequence's end, row 0 of a tile its last token.
-template <typename E, typename O, typename G>
-__global__ __launch_bounds__(G::THREADS) void scan_backward_kernel(ScanParams p) {
-  constexpr int VEC = G::VEC, R = G::R;
-  __shared__ __align__(16) float box[2][G::kWaves][2][G::kChannels];
-  Unit u;
-  if (!unit_of<4>(p, u)) return;
-  const int32_t row = threadIdx.x / G::LPR * R;
-  const int32_t d = u.block * G::kChannels + (threadIdx.x % G::LPR) * VEC;
-  const bool owner = d < p.D;
-  const int32_t dl = owner ? d : p.D - VEC;
-  const int64_t nd = static_cast<int64_t>(u.n) * p.D + dl;
-  const E* x0 = static_cast<const E*>(p.x) + dl;
-  const E* g0 = static_cast<const E*>(p.g) + dl;
-  const O* h0 = static_cast<const O*>(p.h_in) + dl;
-  const O* dh0 = static_cast<const O*>(p.dh) + dl;
-  float carry[VEC], first[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) carry[i] = first[i] = 0.f;
-  if (p.d_final != nullptr) load<VEC>(p.d_final + nd, carry);
-  if (p.initial_state != nullptr) load<VEC>(p.initial_state + nd, first);
-
-  RawVec<E, VEC> g[R];
-  RawVec<O, VEC> dh[R];
-  const auto fetch = [&](int32_t last) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t t = max(last - row - r, u.begin);
-      load_raw<E, VEC>(g0 + t * p.g_stride, g[r]);
-      load_raw<O, VEC>(dh0 + t * p.D, dh[r]);
-    }
-  };
-  fetch(u.end - 1);
-  int parity = 0;
-  for (int32_t last = u.end - 1; last >= u.begin; last -= G::kTile, parity ^= 1) {
-    // what this tile's outputs need besides the scan
-    RawVec<E, VEC> x[R];
-    RawVec<O, VEC> before[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t t = max(last - row - r, u.begin);
-      load_raw<O, VEC>(h0 + max(t - 1, static_cast<int64_t>(u.begin)) * p.D, before[r]);
-      if (p.tied) load_raw<E, VEC>(x0 + t * p.x_stride, x[r]);
-    }
-    float c[R][VEC], P[R][VEC], l[R][VEC], share[R][VEC], A[VEC], B[VEC], TA[VEC], TB[VEC], in[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      A[i] = 1.f;
-      B[i] = 0.f;
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const bool valid = last - row - r >= u.begin;
+      float a[VEC], v[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         const float gi = element(g[r], i);
-        float a = __expf(gi), v = element(dh[r], i);
-        share[r][i] = p.tied ? one_minus_exp(gi, a) : 1.f;
-        l[r][i] = v;
-        a = valid ? a : 1.f;
-        v = valid ? v : 0.f;
-        B[i] = valid ? a * (B[i] + v) : B[i];
-        A[i] *= a;
-        c[r][i] = B[i];
-        P[r][i] = A[i];
+        a[i] = fast_exp(gi);
+        v[i] = TIED ? one_minus_exp(gi, a[i]) * element(x[r], i) : element(x[r], i);
+        if (kKeep) u[r][i] = v[i];
       }
+      step_map<plain.value>(r, lds.mark[row + r], row + r < left, p.initial_state, 1, p.D, dl, a, v, A, B);
     }
-    if (last - G::kTile >= u.begin) fetch(last - G::kTile);
-    wave_scan<VEC, G::LPR>(A, B, TA, TB);
-    tile_carry<G>(box[parity], A, B, TA, TB, carry, in);
-    float next[VEC];   // c_{t+1}
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) next[i] = in[i];
+    tile_states<G>(p, tile, column, lds, A, B, h);
+    // the states: decays again from g, which takes fewer registers than their values
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t t = last - row - r;
-      float dx[VEC], dg[VEC];
+      forget(g[r]);
+      if (!kKeep) forget(x[r]);
+      if (!plain.value) {
+        const int32_t start = lds.mark[row + r];
+        if (start > 0 && row + r < left) load_state(p.initial_state, start - 1, p.D, dl, h);
+      }
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        dx[i] = share[r][i] * (l[r][i] + next[i]);
-        next[i] = c[r][i] + P[r][i] * in[i];
-        const float h = t > u.begin ? element(before[r], i) : first[i];
-        dg[i] = next[i] * (p.tied ? h - element(x[r], i) : h);
+        const float gi = element(g[r], i), a = fast_exp(gi);
+        float v = kKeep ? u[r][i] : element(x[r], i);
+        if (TIED && !kKeep) v *= one_minus_exp(gi, a);
+        h[i] = a * h[i] + v;
       }
-      if (t >= u.begin && owner) {
-        store<VEC>(static_cast<E*>(p.dx) + t * p.D + d, dx);
-        store<VEC>(static_cast<E*>(p.dg) + t * p.D + d, dg);
+      if (owner && (plain.value || row + r < left)) {
+        store<VEC>(hs.at(out, r), h);
+        if (!plain.value) {
+          const int32_t next = lds.mark[row + r + 1];   // the sequence after one that ends here
+          if (next > 0) store<VEC>(p.final_state + static_cast<int64_t>(next - 2) * p.D + dl, h);
+        }
       }
     }
-  }
-  if (p.d_initial_state != nullptr && threadIdx.x < G::LPR && owner) store<VEC>(p.d_initial_state + nd, carry);
+  });
 }
 
-ScanParams params_of(const ScanArgs& a) {
+// The backward: tiles in order from the tokens' end, row 0 of a tile its last
+// token.
+template <typename E, typename O, typename G, bool TIED>
+__global__ __launch_bounds__(kScanThreads) void scan_backward_kernel(ScanParams p) {
+  constexpr int VEC = G::VEC, R = G::R;
+  __shared__ __align__(16) TileLds<G> lds;
+  const int32_t column = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(p.columns));
+  const int32_t tile = take_ticket(p, column, &lds.ticket);
+  if (tile >= p.tiles) return;
+  const int32_t row = threadIdx.x / G::LPR * R;
+  const int32_t d = column * kScanChannels + (threadIdx.x % G::LPR) * VEC;
+  const bool owner = d < p.D;
+  const int32_t dl = min(d, p.D - VEC);   // as in the forward
+  const int32_t end = p.T - tile * kScanTile, left = min(end, kScanTile), base = end - kScanTile;
+  // tokens from the tile's first one; this thread's go down from `token`
+  const int32_t from = max(base, 0), token = left - 1 - row;
+  const Span<E> xs(p.x, p.x_stride, from), gs(p.g, p.g_stride, from), dxs(p.dx, p.D, from), dgs(p.dg, p.D, from);
+  const Span<O> dhs(p.dh, p.D, from), hs(p.h_in, p.D, max(from - 1, 0));
+  RawVec<E, VEC> x[R], g[R];
+  RawVec<O, VEC> dh[R], before[R];                                      // before: h_{t-1}
+  with_flag(base >= 1, [&](auto full) {
+    fetch_rows<-1, full.value>(gs, token, dl, left - 1, g);
+    fetch_rows<-1, full.value>(dhs, token, dl, left - 1, dh);
+    if (TIED) fetch_rows<-1, full.value>(xs, token, dl, left - 1, x);
+    // token - 1 of the tensor; where there is none (the first token of all), that one
+    fetch_rows<-1, full.value>(hs, base >= 1 ? token : token - 1, dl, left - 1, before);
+  });
+  const bool marked = mark_sequences(p, base, lds.mark);
+  const uint32_t out = dxs.offset(max(token, 0), dl);
+  with_flag(base >= 1 && !marked, [&](auto plain) {
+    float A[VEC], B[VEC], c[VEC];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float a[VEC], v[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        a[i] = fast_exp(element(g[r], i));
+        v[i] = a[i] * element(dh[r], i);
+      }
+      // a sequence's last token: c = a (dh + d_final)
+      step_map<plain.value>(r, lds.mark[kScanTile - row - r], row + r < left, p.d_final, 2, p.D, dl, a, v, A, B);
+    }
+    tile_states<G>(p, tile, column, lds, A, B, c);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool valid = plain.value || row + r < left;
+      forget(g[r]);   // as in the forward
+      forget(dh[r]);
+      float hp[VEC], dx[VEC], dg[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) hp[i] = element(before[r], i);
+      int32_t start = 0;
+      if (!plain.value && valid) {
+        start = lds.mark[kScanTile - 1 - row - r];
+        if (start > 0) load_state(p.initial_state, start - 1, p.D, dl, hp);
+        const int32_t next = lds.mark[kScanTile - row - r];
+        if (next > 0) load_state(p.d_final, next - 2, p.D, dl, c);
+      }
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float gi = element(g[r], i), a = fast_exp(gi), l = element(dh[r], i) + c[i];
+        dx[i] = TIED ? one_minus_exp(gi, a) * l : l;
+        c[i] = a * l;
+        dg[i] = c[i] * (TIED ? hp[i] - element(x[r], i) : hp[i]);
+      }
+      if (owner && valid) {
+        store<VEC>(dxs.at(out, -r), dx);
+        store<VEC>(dgs.at(out, -r), dg);
+        if (start > 0 && p.d_initial_state != nullptr) {
+          store<VEC>(p.d_initial_state + static_cast<int64_t>(start - 1) * p.D + dl, c);
+        }
+      }
+    }
+  });
+}
+
+// All ones over the tickets, maps and states of a call: n 16-byte words.
+__global__ __launch_bounds__(256) void scan_clear_kernel(u32x4* words, int64_t n) {
+  const u32x4 ones = {kEmpty, kEmpty, kEmpty, kEmpty};
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+    words[i] = ones;
+  }
+}
+
+template <typename E, typename O, typename G>
+int run(ScanParams p, bool tied, bool backward, void* workspace, hipStream_t stream) {
+  const ScanLayout L = scan_layout(p.T, p.D);
+  p.tiles = L.tiles;
+  p.columns = L.columns;
+  const int64_t grid = static_cast<int64_t>(p.tiles) * p.columns;
+  if (grid * kScanThreads > 4294967295LL) return KDA_ERR_UNSUPPORTED;
+  (void)hipGetLastError();
+  if (L.total > 0) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.tickets = reinterpret_cast<uint32_t*>(ws + L.tickets);
+    p.maps = reinterpret_cast<uint64_t*>(ws + L.maps);
+    p.states = reinterpret_cast<uint32_t*>(ws + L.states);
+    const int64_t words = static_cast<int64_t>(L.total / 16), blocks = (words + 255) / 256;
+    hipLaunchKernelGGL(scan_clear_kernel, dim3(static_cast<uint32_t>(blocks < 2048 ? blocks : 2048)), dim3(256), 0, stream,
+                       reinterpret_cast<u32x4*>(ws), words);
+    const int st = finish_launch();
+    if (st != KDA_OK) return st;
+  }
+  void (*kernel)(ScanParams) = backward ? (tied ? scan_backward_kernel<E, O, G, true> : scan_backward_kernel<E, O, G, false>)
+                                        : (tied ? scan_kernel<E, O, G, true> : scan_kernel<E, O, G, false>);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)), dim3(kScanThreads), 0, stream, p);
+  return finish_launch();
+}
+
+using Vector = Geometry<4, 16, 8>;    // rows of at least one 4-element vector
+using Scalar = Geometry<1, 64, 32>;   // shorter ones
+
+template <typename G>
+int run_types(const ScanArgs& a, bool backward, const ScanParams& p, hipStream_t stream) {
+  const bool e16 = a.dtype == KDA_BF16, o16 = a.h_format == KDA_BF16, tied = a.tied != 0;
+  if (e16 && o16) return run<bf16_t, bf16_t, G>(p, tied, backward, a.workspace.ptr, stream);
+  if (e16) return run<bf16_t, fp32_t, G>(p, tied, backward, a.workspace.ptr, stream);
+  if (o16) return run<fp32_t, bf16_t, G>(p, tied, backward, a.workspace.ptr, stream);
+  return run<fp32_t, fp32_t, G>(p, tied, backward, a.workspace.ptr, stream);
+}
+
+int launch_either(const ScanArgs& a, bool backward, hipStream_t stream) {
   ScanParams p{};
   p.plan = static_cast<const int32_t*>(a.plan_dev.ptr);
   p.L = a.plan->layout;
@@ -305,7 +484,6 @@ ScanParams params_of(const ScanArgs& a) {
   p.N = a.plan->N;
   p.F = a.plan->F;
   p.D = a.D;
-  p.tied = a.tied;
   p.x = a.x.ptr;
   p.g = a.g.ptr;
   p.x_stride = a.x.stride;
@@ -319,62 +497,12 @@ ScanParams params_of(const ScanArgs& a) {
   p.dx = a.dx.ptr;
   p.dg = a.dg.ptr;
   p.d_initial_state = static_cast<float*>(a.d_initial_state.ptr);
-  return p;
+  return a.D >= Vector::VEC ? run_types<Vector>(a, backward, p, stream) : run_types<Scalar>(a, backward, p, stream);
 }
-
-template <typename G>
-int launch(void (*kernel)(ScanParams), ScanParams p, hipStream_t stream) {
-  p.blocks = (p.D + G::kChannels - 1) / G::kChannels;
-  p.bundles = (p.blocks + 3) / 4;
-  p.total_bundles = static_cast<int64_t>(p.bundles) * p.N;
-  const int64_t grid = (p.total_bundles + kXcds - 1) / kXcds * kXcds * 4;
-  if (grid * G::THREADS > 2147483647LL) return KDA_ERR_UNSUPPORTED;
-  (void)hipGetLastError();
-  hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)), dim3(G::THREADS), 0, stream, p);
-  return finish_launch();
-}
-
-// Rows of 16-byte pieces: whole vectors and strides.
-bool vector_rows(const ScanArgs& a, bool with_x) {
-  const int64_t per = a.dtype == KDA_BF16 ? 8 : 4;
-  return a.D % 8 == 0 && a.g.stride % per == 0 && (!with_x || a.x.stride % per == 0);
-}
-
-using Vector = Geometry<4, 4, 8, 512>;
-using VectorBackward = Geometry<4, 4, 4, 512>;
-using Wide = Geometry<8, 2, 4, 512>;
-using Scalar = Geometry<1, 16, 8, 512>;
 
 }  // namespace
 
-int launch_scan(const ScanArgs& a, hipStream_t stream) {
-  const ScanParams p = params_of(a);
-  const bool e16 = a.dtype == KDA_BF16, o16 = a.h_format == KDA_BF16;
-  if (vector_rows(a, true)) {
-    if (e16 && o16) return launch<Vector>(scan_kernel<bf16_t, bf16_t, Vector>, p, stream);
-    if (e16) return launch<Vector>(scan_kernel<bf16_t, fp32_t, Vector>, p, stream);
-    if (o16) return launch<Wide>(scan_kernel<fp32_t, bf16_t, Wide>, p, stream);
-    return launch<Wide>(scan_kernel<fp32_t, fp32_t, Wide>, p, stream);
-  }
-  if (e16 && o16) return launch<Scalar>(scan_kernel<bf16_t, bf16_t, Scalar>, p, stream);
-  if (e16) return launch<Scalar>(scan_kernel<bf16_t, fp32_t, Scalar>, p, stream);
-  if (o16) return launch<Scalar>(scan_kernel<fp32_t, bf16_t, Scalar>, p, stream);
-  return launch<Scalar>(scan_kernel<fp32_t, fp32_t, Scalar>, p, stream);
-}
-
-int launch_scan_backward(const ScanArgs& a, hipStream_t stream) {
-  const ScanParams p = params_of(a);
-  const bool e16 = a.dtype == KDA_BF16, o16 = a.h_format == KDA_BF16;
-  if (vector_rows(a, a.tied != 0)) {
-    if (e16 && o16) return launch<VectorBackward>(scan_backward_kernel<bf16_t, bf16_t, VectorBackward>, p, stream);
-    if (e16) return launch<VectorBackward>(scan_backward_kernel<bf16_t, fp32_t, VectorBackward>, p, stream);
-    if (o16) return launch<Wide>(scan_backward_kernel<fp32_t, bf16_t, Wide>, p, stream);
-    return launch<Wide>(scan_backward_kernel<fp32_t, fp32_t, Wide>, p, stream);
-  }
-  if (e16 && o16) return launch<Scalar>(scan_backward_kernel<bf16_t, bf16_t, Scalar>, p, stream);
-  if (e16) return launch<Scalar>(scan_backward_kernel<bf16_t, fp32_t, Scalar>, p, stream);
-  if (o16) return launch<Scalar>(scan_backward_kernel<fp32_t, bf16_t, Scalar>, p, stream);
-  return launch<Scalar>(scan_backward_kernel<fp32_t, fp32_t, Scalar>, p, stream);
-}
+int launch_scan(const ScanArgs& a, hipStream_t stream) { return launch_either(a, false, stream); }
+int launch_scan_backward(const ScanArgs& a, hipStream_t stream) { return launch_either(a, true, stream); }
 
 }  // namespace kda

@@ -566,10 +566,11 @@ size_t kda_output_norm_backward_workspace_bytes(int32_t T, int32_t H, int32_t V)
  *   tied           0 or 1
  *   initial_state  [N, D] FP32 or NULL (zero)
  *   h              [T, D] in h_format; final_state [N, D] FP32
- * The plan's segments are the tokens that run at the same time where the
- * sequences and channels alone are too few to fill the GPU; they change
- * results by rounding only.  Workspace: kda_scan_workspace_bytes(plan, D)
- * bytes, NULL where that is 0 (no segment cuts a sequence).
+ * Only the plan's sequences count: its segments and pieces change nothing.
+ * Workspace: kda_scan_workspace_bytes(plan, D) bytes, NULL where that is 0 (at
+ * most 256 tokens).  Its contents are not needed afterwards.  Two calls that
+ * may run at the same time need a workspace each: sharing one gives undefined
+ * results (wrong values or NaN).
  */
 int kda_scan_forward(const kda_plan* plan, const int32_t* plan_dev, size_t plan_dev_bytes, int32_t D, int32_t dtype,
                      const void* x, size_t x_bytes, int64_t x_stride, const void* g, size_t g_bytes, int64_t g_stride,

@@ -233,6 +233,45 @@ def test_scan_of_pieces_and_repeats():
         assert torch.equal(r["h"], runs[0]["h"]) and torch.equal(r["final_state"], runs[0]["final_state"])
 
 
+def test_scan_repeats_of_many_tiles():
+    """The same bits on every run, however the tiles' workgroups race."""
+    cu, D = [0, 9000, 20011], 200
+    x, g, h0, dev = _scan_case(cu, D, BF, False, True, False, seed=13, slow=True)
+    plan, dh = kda.Plan(cu, 1), _d(_randn(cu[-1], D, seed=14))
+    f = [layer.scan_forward(plan, *dev, initial_state=_d(h0), h_dtype=F32) for _ in range(6)]
+    b = [layer.scan_backward(plan, *dev, f[0]["h"], dh, initial_state=_d(h0)) for _ in range(6)]
+    for runs in (f, b):
+        for r in runs[1:]:
+            assert all(torch.equal(r[n], runs[0][n]) for n in r)
+
+
+@pytest.mark.parametrize("D,dtype", [(72, F32), (13, BF)])
+def test_scan_keeps_sequences_apart(D, dtype):
+    """An infinity or NaN in one sequence does not reach the others, wherever
+    the boundaries lie, in either direction."""
+    cu = [0, 100, 101, 400, 900, 905, 1300]
+    x, g, h0, dev = _scan_case(cu, D, dtype, True, True, False, seed=9, slow=True)
+    g[:, 1:3] = g[:, 3:5]                    # finite everywhere
+    dev[1] = _d(g)
+    plan = kda.Plan(cu, 3)
+    dh, d_final = _d(_randn(1300, D, seed=70, dtype=dtype)), _d(_randn(6, D, seed=71))
+    ref = layer.scan_forward(plan, *dev, initial_state=_d(h0), tied=True)
+    back = layer.scan_backward(plan, *dev, ref["h"], dh, d_final=d_final, initial_state=_d(h0), tied=True)
+    for bad in (float("nan"), float("inf")):
+        x2, dh2 = dev[0].clone(), dh.clone()
+        for n in (1, 3):
+            x2[cu[n + 1] - 1], dh2[cu[n]] = bad, bad
+        got = layer.scan_forward(plan, x2, dev[1], initial_state=_d(h0), tied=True)
+        grads = layer.scan_backward(plan, dev[0], dev[1], ref["h"], dh2, d_final=d_final, initial_state=_d(h0), tied=True)
+        for n in (0, 2, 4, 5):
+            rows = slice(cu[n], cu[n + 1])
+            assert torch.equal(got["h"][rows], ref["h"][rows]) and torch.equal(got["final_state"][n], ref["final_state"][n])
+            assert all(torch.equal(grads[k][rows], back[k][rows]) for k in ("dx", "dg"))
+            assert torch.equal(grads["dh0"][n], back["dh0"][n])
+        assert not torch.isfinite(got["final_state"][[1, 3]]).any()
+        assert not torch.isfinite(grads["dh0"][[1, 3]]).any()
+
+
 # ------------------------------------------------------------- single tokens
 
 SLOTS = [

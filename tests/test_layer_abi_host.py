@@ -54,7 +54,8 @@ def _norm(T=5, H=3, V=40, backward=False):
                 **_buffers("d_gate", "d_weight", "d_res_scale", "workspace"))
 
 
-_PLAN = kda.Plan([0, 3, 10], 2)     # a segment cuts the second sequence
+_PLAN = kda.Plan([0, 3, 10], 2)
+_LONG = kda.Plan([0, 3, 300], 2)    # more than one tile of tokens
 
 
 def _scan(backward=False, plan=_PLAN, D=6, tied=1):
@@ -193,14 +194,15 @@ def test_optional_pairs():
 @pytest.mark.parametrize("call,need", [
     ("prepare_bwd", lambda: kda.lib().kda_prepare_inputs_backward_workspace_bytes(5, 3, 128)),
     ("norm_bwd", lambda: kda.lib().kda_output_norm_backward_workspace_bytes(5, 3, 40)),
-    ("scan", lambda: kda.lib().kda_scan_workspace_bytes(_PLAN.handle, 6)),
-    ("scan_bwd", lambda: kda.lib().kda_scan_workspace_bytes(_PLAN.handle, 6))])
+    ("scan_long", lambda: kda.lib().kda_scan_workspace_bytes(_LONG.handle, 6)),
+    ("scan_bwd_long", lambda: kda.lib().kda_scan_workspace_bytes(_LONG.handle, 6))])
 def test_workspace(call, need):
     size = need()
     assert size > 0
-    assert CALLS[call](workspace=[None, BIG]) == INVALID
-    assert CALLS[call](workspace=[FAKE + 4, BIG]) == MISALIGNED
-    assert CALLS[call](workspace=[FAKE, size - 1]) == WORKSPACE
+    run = {**CALLS, "scan_long": _scan(plan=_LONG), "scan_bwd_long": _scan(True, _LONG)}[call]
+    assert run(workspace=[None, BIG]) == INVALID
+    assert run(workspace=[FAKE + 4, BIG]) == MISALIGNED
+    assert run(workspace=[FAKE, size - 1]) == WORKSPACE
 
 
 def test_workspace_sizes():
@@ -210,10 +212,13 @@ def test_workspace_sizes():
     assert L.kda_output_norm_backward_workspace_bytes(5, 3, 8193) == 0
     assert L.kda_output_norm_backward_workspace_bytes(5, 0, 8) == 0
     assert L.kda_scan_workspace_bytes(None, 6) == 0
-    assert L.kda_scan_workspace_bytes(_PLAN.handle, 0) == 0
-    # no segment cuts a sequence
-    assert L.kda_scan_workspace_bytes(kda.Plan([0, 3, 10], 1).handle, 6) == 0
-    assert L.kda_scan_workspace_bytes(kda.Plan([0, 3, 10], 2, [0, 3, 10]).handle, 6) == 0
+    assert L.kda_scan_workspace_bytes(_LONG.handle, 0) == 0
+    # at most 256 tokens need none; then 12 bytes a channel of whole blocks of
+    # 64 and tile of 256 tokens, and a 128-byte ticket a block
+    assert L.kda_scan_workspace_bytes(_PLAN.handle, 6) == 0
+    assert L.kda_scan_workspace_bytes(kda.Plan([0, 256], 1).handle, 6) == 0
+    assert L.kda_scan_workspace_bytes(kda.Plan([0, 257], 1).handle, 6) == 2 * 64 * 12 + 128
+    assert L.kda_scan_workspace_bytes(kda.Plan([0, 65536], 1).handle, 4096) == 256 * 4096 * 12 + 64 * 128
 
 
 def test_pools():
