@@ -197,7 +197,9 @@ __device__ __forceinline__ float one_minus_exp(float g, float a) {
   s = s * g + 1.f / 6.f;
   s = s * g + 0.5f;
   s = s * g + 1.f;
-  return g > -0.25f ? -g * s : 1.f - a;
+  float near = -g * s;
+  asm("" : "+v"(near));   // both sides and a select: cheaper than branching around the sum
+  return g > -0.25f ? near : 1.f - a;
 }
 
 // e^x by the hardware's 2^x: relative error about 1 + |x| units of 2^-24,

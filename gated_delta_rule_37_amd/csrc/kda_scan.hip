@@ -44,10 +44,10 @@ struct ScanParams {
 };
 
 // LPR lanes of VEC channels make a row of 64 channels; a thread takes R
-// tokens, so that every geometry has the same tile.
-template <int VEC_, int LPR_, int R_>
+// tokens, so that every geometry has the same tile.  LOOK: see look_back.
+template <int VEC_, int LPR_, int R_, int LOOK_>
 struct Geometry {
-  static constexpr int VEC = VEC_, LPR = LPR_, R = R_;
+  static constexpr int VEC = VEC_, LPR = LPR_, R = R_, LOOK = LOOK_;
   static_assert(VEC * LPR == kScanChannels && kScanThreads / LPR * R == kScanTile, "");
 };
 static_assert(kScanTile < kScanThreads, "a thread for each token boundary of a tile");
@@ -81,41 +81,42 @@ __device__ __forceinline__ int64_t word_of(const ScanParams& p, int32_t tile, in
 }
 
 // The state before tile `tile`, for this wave's lane: channel `lane` of the
-// block.  Looks at the kLook tiles before it until, for every channel, one of
+// block.  Looks at the LOOK tiles before it until, for every channel, one of
 // them has its state and those after it their maps, then applies those maps in
 // order: exactly what each of these tiles does itself, so the result does not
 // depend on which states were there.  Polls are bounded, so that a workspace
 // that another call overwrites gives NaN instead of a hang.
-constexpr int kLook = 4;
 constexpr int kMaxPolls = 1 << 22;
+template <int LOOK>
 __device__ __forceinline__ float look_back(const ScanParams& p, int32_t tile, int32_t column) {
   const int32_t lane = threadIdx.x & 63;
   for (int polls = 0; polls < kMaxPolls; ++polls) {
-    uint32_t state[kLook];
-    uint64_t map[kLook];
+    uint32_t state[LOOK];
+    uint64_t map[LOOK];
 #pragma unroll
-    for (int i = 0; i < kLook; ++i) {
+    for (int i = 0; i < LOOK; ++i) {
       const int64_t w = word_of(p, max(tile - 1 - i, 0), column);
       state[i] = __hip_atomic_load(p.states + w + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      map[i] = __hip_atomic_load(p.maps + w + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      // the farthest tile's map would need a state behind the window
+      map[i] = i < LOOK - 1 ? __hip_atomic_load(p.maps + w + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
     }
     bool have = false;
     float h = 0.f;
 #pragma unroll
-    for (int i = kLook - 1; i >= 0; --i) {
+    for (int i = LOOK - 1; i >= 0; --i) {
       if (i >= tile) continue;
       const uint32_t a = static_cast<uint32_t>(map[i]);
       if (state[i] != kEmpty) {
         h = __uint_as_float(state[i]);
         have = true;
-      } else if (a == kEmpty) {
+      } else if (i == LOOK - 1 || a == kEmpty) {
         have = false;
       } else {
         h = apply(__uint_as_float(a), __uint_as_float(static_cast<uint32_t>(map[i] >> 32)), h);
       }
     }
     if (__ballot(!have) == 0) return h;
-    __builtin_amdgcn_s_sleep(1);
+    __builtin_amdgcn_s_sleep(8);
   }
   return __uint_as_float(0x7fc00000u);
 }
@@ -187,7 +188,7 @@ __device__ __forceinline__ void tile_states(const ScanParams& p, int32_t tile, i
       if (tile > 0) {
         __hip_atomic_store(p.maps + w, static_cast<uint64_t>(float_bits(b)) << 32 | float_bits(a), __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
-        state = look_back(p, tile, column);
+        state = look_back<G::LOOK>(p, tile, column);
       }
       __hip_atomic_store(p.states + w, float_bits(apply(a, b, state)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
@@ -284,6 +285,8 @@ __device__ __forceinline__ void step_map(int r, int32_t mark, bool valid, const 
   for (int i = 0; i < VEC; ++i) {
     B[i] = r == 0 ? b[i] : PLAIN ? a[i] * B[i] + b[i] : apply(a[i], b[i], B[i]);
     A[i] = r == 0 ? a[i] : A[i] * a[i];
+    // row by row: composing all rows at the end would keep their maps in registers
+    if (!PLAIN) asm volatile("" : "+v"(A[i]), "+v"(B[i]));
   }
 }
 
@@ -464,8 +467,15 @@ int run(ScanParams p, bool tied, bool backward, void* workspace, hipStream_t str
   return finish_launch();
 }
 
-using Vector = Geometry<4, 16, 8>;    // rows of at least one 4-element vector
-using Scalar = Geometry<1, 64, 32>;   // shorter ones
+// Many tiles of a channel block are in flight where there are few blocks, and
+// a wide window lets a state pass over more of them at once; where there are
+// many, its registers cost more than it gives.  Forward, 32768 tokens, bf16, a
+// window of 4 against one of 16: 4096 channels (64 blocks) 193 and 227 us,
+// 2048 109 and 122, 1024 77 and 68, 512 65 and 44, 64 57 and 36.
+constexpr int32_t kNarrowBlocks = 24;
+using Vector = Geometry<4, 16, 8, 4>;         // rows of at least one 4-element vector
+using VectorNarrow = Geometry<4, 16, 8, 16>;  // the same, of fewer than kNarrowBlocks blocks
+using Scalar = Geometry<1, 64, 32, 16>;       // rows of up to three elements
 
 template <typename G>
 int run_types(const ScanArgs& a, bool backward, const ScanParams& p, hipStream_t stream) {
@@ -497,7 +507,9 @@ int launch_either(const ScanArgs& a, bool backward, hipStream_t stream) {
   p.dx = a.dx.ptr;
   p.dg = a.dg.ptr;
   p.d_initial_state = static_cast<float*>(a.d_initial_state.ptr);
-  return a.D >= Vector::VEC ? run_types<Vector>(a, backward, p, stream) : run_types<Scalar>(a, backward, p, stream);
+  if (a.D < Vector::VEC) return run_types<Scalar>(a, backward, p, stream);
+  if (a.D < kNarrowBlocks * kScanChannels) return run_types<VectorNarrow>(a, backward, p, stream);
+  return run_types<Vector>(a, backward, p, stream);
 }
 
 }  // namespace
