@@ -100,9 +100,10 @@ NormShape norm_shape(int32_t V, bool vector_rows) {
     if (V <= 4096) return {256, 8, 2};
     return {256, 8, 4};
   }
-  if (V <= 512) return {64, 1, 8};
-  if (V <= 2048) return {256, 1, 8};
-  return {256, 1, 32};
+  if (V <= 256) return {64, 4, 1};
+  if (V <= 1024) return {256, 4, 1};
+  if (V <= 2048) return {256, 4, 2};
+  return {256, 4, 8};
 }
 
 NormBwdLayout norm_bwd_layout(int32_t T, int32_t H, int32_t V, const NormShape& shape) {

@@ -11,7 +11,8 @@
 // A row stays in the registers of its lane group (16 lanes for a head of 128,
 // up to a workgroup for 8192 channels): each element is read and written
 // once, HBM bandwidth is the bound.  Rows whose width or stride is not a
-// multiple of 16 bytes take one element a lane and load.
+// multiple of 16 bytes take four elements a load, at any address, and what is
+// left of the row one by one.
 #include "kda_layer.h"
 #include "kda_layer_device.h"
 
@@ -62,6 +63,8 @@ struct Share {
   int32_t lane, V;
   __device__ __forceinline__ int32_t at(int j) const { return (j * LANES + lane) * VEC; }
   __device__ __forceinline__ bool has(int j) const { return at(j) < V; }
+  // a row's last vector may be cut off (VEC = 4), else rows are whole ones
+  __device__ __forceinline__ bool whole(int j) const { return VEC == 4 ? at(j) + VEC <= V : has(j); }
 };
 
 // Elements of a row of `src`, or `fill` behind its end and where src is null.
@@ -70,8 +73,15 @@ __device__ __forceinline__ void load_row(const Share<LANES, VEC, NV>& sh, const 
                                          float (&x)[NV][VEC]) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    if (src != nullptr && sh.has(j)) {
+    if (src != nullptr && sh.whole(j)) {
       load<VEC>(src + sh.at(j), x[j]);
+    } else if (VEC == 4 && src != nullptr && sh.has(j)) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        float e[1] = {fill};
+        if (sh.at(j) + i < sh.V) load<1>(src + sh.at(j) + i, e);
+        x[j][i] = e[0];
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) x[j][i] = fill;
@@ -82,7 +92,15 @@ template <int LANES, int VEC, int NV, typename E>
 __device__ __forceinline__ void store_row(const Share<LANES, VEC, NV>& sh, E* dst, const float (&x)[NV][VEC]) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    if (sh.has(j)) store<VEC>(dst + sh.at(j), x[j]);
+    if (sh.whole(j)) {
+      store<VEC>(dst + sh.at(j), x[j]);
+    } else if (VEC == 4 && sh.has(j)) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float e[1] = {x[j][i]};
+        if (sh.at(j) + i < sh.V) store<1>(dst + sh.at(j) + i, e);
+      }
+    }
   }
 }
 
@@ -261,9 +279,10 @@ void with_shape(const NormShape& s, F&& f) {
     if (s.nv == 2) return f.template operator()<256, 8, 2>();
     return f.template operator()<256, 8, 4>();
   }
-  if (s.lanes == 64) return f.template operator()<64, 1, 8>();
-  if (s.nv == 8) return f.template operator()<256, 1, 8>();
-  return f.template operator()<256, 1, 32>();
+  if (s.lanes == 64) return f.template operator()<64, 4, 1>();
+  if (s.nv == 1) return f.template operator()<256, 4, 1>();
+  if (s.nv == 2) return f.template operator()<256, 4, 2>();
+  return f.template operator()<256, 4, 8>();
 }
 
 template <typename O, typename E>

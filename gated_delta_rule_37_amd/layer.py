@@ -40,8 +40,6 @@ raises ValueError.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from . import kda
@@ -61,19 +59,26 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return code
 
 
+# The checks below run on every call, which for one token is most of its time:
+# they ask each tensor for as little as they can.
 def _buf(t, dtype, shape, name, device):
     """(address, size in bytes) of a dense tensor on ``device``."""
     if t is None:
         return _NULL
+    if t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return (t.data_ptr(), t.nbytes)
+    raise _refusal(t, dtype, shape, name, device) or ValueError(f"{name}: must be contiguous")
+
+
+def _refusal(t, dtype, shape, name, device):
+    """The error for a tensor of another type, shape or device, else None."""
     if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+        return TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
+        return ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the other tensors on {device}")
-    return (t.data_ptr(), t.nbytes)
+        return ValueError(f"{name}: on {t.device}, the other tensors on {device}")
+    return None
 
 
 def _made(t):
@@ -97,25 +102,35 @@ def _rows(t, dtype, shape, name, device):
     """(address, size in bytes, token stride) of a tensor of rows."""
     if t is None:
         return _NULL_ROWS
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the other tensors on {device}")
-    stride, n = _row_stride(t, name), shape[0]
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        raise _refusal(t, dtype, shape, name, device)
+    n = shape[0]
+    if n and t.is_contiguous():
+        return (t.data_ptr(), t.nbytes, t.numel() // n)
+    stride = _row_stride(t, name)
     span = (n - 1) * stride + t.numel() // n if n else 0
     return (t.data_ptr(), span * t.element_size(), stride)
+
+
+_functions = {}
 
 
 def _call(name, device, args, stream):
     """One C call on ``stream``, with the tensors' device current."""
     if device.type != "cuda":
         raise ValueError(f"{name}: needs device tensors")
-    with torch.cuda.device(device):
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        kda._check(getattr(kda.lib(), name)(*args, ctypes.c_void_p(stream.cuda_stream)), name)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(kda.lib(), name)
+    index = device.index
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status != 0:
+        raise kda.KdaError(status, name)
 
 
 def _raw(q_raw, k_raw, gate_raw, beta_raw, a_log, dt_bias, q_scale, eps):
@@ -143,9 +158,12 @@ def prepare_inputs(q_raw, k_raw, gate_raw, beta_raw, a_log, dt_bias=None, q_scal
     if out is None:
         out = {n: torch.empty(T, H, K, dtype=bf, device=dev) for n in ("q", "k", "g")}
         out["beta"] = torch.empty(T, H, dtype=bf, device=dev)
-    for n in ("q", "k", "g"):
-        args += _buf(out[n], bf, (T, H, K), n, dev)
-    args += _buf(out["beta"], bf, (T, H), "beta", dev)
+        for t in out.values():
+            args += _made(t)
+    else:
+        for n in ("q", "k", "g"):
+            args += _buf(out[n], bf, (T, H, K), n, dev)
+        args += _buf(out["beta"], bf, (T, H), "beta", dev)
     _call("kda_prepare_inputs", dev, args, stream)
     return out
 

@@ -561,14 +561,16 @@ size_t kda_output_norm_backward_workspace_bytes(int32_t T, int32_t H, int32_t V)
  * over the plan's packed sequences: for every channel d of D,
  *     h_t = exp(g_t) h_{t-1} + u_t,   u_t = x_t, or (1 - exp(g_t)) x_t when tied
  * where h before a sequence's first token is its initial state.
- *   x, g           [T, D] dtype, each with its own token stride; g <= 0,
- *                  finite or -inf (exp(-inf) = 0 forgets the channel)
+ *   x, g           [T, D] dtype, each with its own token stride (at most
+ *                  2^22 elements, KDA_ERR_UNSUPPORTED); g <= 0, finite or
+ *                  -inf (exp(-inf) = 0 forgets the channel)
  *   tied           0 or 1
  *   initial_state  [N, D] FP32 or NULL (zero)
  *   h              [T, D] in h_format; final_state [N, D] FP32
- * Only the plan's sequences count: its segments and pieces change nothing.
+ * Only the plan's sequences count: its segments and pieces change nothing.  An
+ * infinity or NaN stays in its own sequence.
  * Workspace: kda_scan_workspace_bytes(plan, D) bytes, NULL where that is 0 (at
- * most 256 tokens).  Its contents are not needed afterwards.  Two calls that
+ * most 128 tokens).  Its contents are not needed afterwards.  Two calls that
  * may run at the same time need a workspace each: sharing one gives undefined
  * results (wrong values or NaN).
  */

@@ -213,12 +213,12 @@ def test_workspace_sizes():
     assert L.kda_output_norm_backward_workspace_bytes(5, 0, 8) == 0
     assert L.kda_scan_workspace_bytes(None, 6) == 0
     assert L.kda_scan_workspace_bytes(_LONG.handle, 0) == 0
-    # at most 256 tokens need none; then 12 bytes a channel of whole blocks of
-    # 64 and tile of 256 tokens, and a 128-byte ticket a block
+    # at most 128 tokens need none; then 12 bytes a channel of whole blocks of
+    # 64 and tile of 128 tokens, and a 128-byte ticket a block
     assert L.kda_scan_workspace_bytes(_PLAN.handle, 6) == 0
-    assert L.kda_scan_workspace_bytes(kda.Plan([0, 256], 1).handle, 6) == 0
-    assert L.kda_scan_workspace_bytes(kda.Plan([0, 257], 1).handle, 6) == 2 * 64 * 12 + 128
-    assert L.kda_scan_workspace_bytes(kda.Plan([0, 65536], 1).handle, 4096) == 256 * 4096 * 12 + 64 * 128
+    assert L.kda_scan_workspace_bytes(kda.Plan([0, 128], 1).handle, 6) == 0
+    assert L.kda_scan_workspace_bytes(kda.Plan([0, 129], 1).handle, 6) == 2 * 64 * 12 + 128
+    assert L.kda_scan_workspace_bytes(kda.Plan([0, 65536], 1).handle, 4096) == 512 * 4096 * 12 + 64 * 128
 
 
 def test_pools():
