@@ -76,6 +76,7 @@ struct RowGrid {
 RowGrid row_grid(int64_t T, int64_t H, int32_t groups_per_block, int32_t max_blocks);
 
 constexpr int kRowThreads = 256;        // row-wise kernels
+constexpr int64_t kStreamBytes = int64_t(256) << 20;   // the last-level cache: larger calls go past it
 constexpr int kPrepareGroups = 16;      // 16-lane groups of 8 channels a workgroup
 constexpr int kPrepareBwdBlocks = 512;  // backward grid at most: two workgroups a CU
 constexpr int kNormBwdBlocks = 512;

@@ -21,12 +21,29 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
+// 16 bytes; STREAM: past the caches, which pays where a call's tensors are
+// larger than the 256 MB last-level cache (kStreamBytes) and costs where the
+// next launch finds them there.
+template <bool STREAM, typename V>
+__device__ __forceinline__ V fetch(const V* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(p);
+  return *p;
+}
+template <bool STREAM, typename V>
+__device__ __forceinline__ void put(V* p, V v) {
+  if constexpr (STREAM) {
+    __builtin_nontemporal_store(v, p);
+  } else {
+    *p = v;
+  }
+}
+
 // VEC (1, 4 or 8) neighbouring elements at p as FP32.  With VEC = 8, p is
 // aligned to 16 bytes; with VEC = 4 to the element.
-template <int VEC>
+template <int VEC, bool STREAM = false>
 __device__ __forceinline__ void load(const bf16_t* p, float (&x)[VEC]) {
   if constexpr (VEC == 8) {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+    const u32x4 w = fetch<STREAM>(reinterpret_cast<const u32x4*>(p));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = __uint_as_float(w[i] << 16);
@@ -44,10 +61,10 @@ __device__ __forceinline__ void load(const bf16_t* p, float (&x)[VEC]) {
     x[0] = bf2f(*p);
   }
 }
-template <int VEC>
+template <int VEC, bool STREAM = false>
 __device__ __forceinline__ void load(const fp32_t* p, float (&x)[VEC]) {
   if constexpr (VEC == 8) {
-    const f32x4 a = ld4(p), b = ld4(p + 4);
+    const f32x4 a = fetch<STREAM>(reinterpret_cast<const f32x4*>(p)), b = fetch<STREAM>(reinterpret_cast<const f32x4*>(p + 4));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[i] = a[i];
@@ -64,13 +81,13 @@ __device__ __forceinline__ void load(const fp32_t* p, float (&x)[VEC]) {
 }
 
 // The same, rounded to nearest even for bf16.
-template <int VEC>
+template <int VEC, bool STREAM = false>
 __device__ __forceinline__ void store(bf16_t* p, const float (&x)[VEC]) {
   if constexpr (VEC == 8) {
     u32x4 w;
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-    *reinterpret_cast<u32x4*>(p) = w;
+    put<STREAM>(reinterpret_cast<u32x4*>(p), w);
   } else if constexpr (VEC == 4) {
     u32x2 w;
     w[0] = pack_bf16(x[0], x[1]);
@@ -80,7 +97,7 @@ __device__ __forceinline__ void store(bf16_t* p, const float (&x)[VEC]) {
     *p = static_cast<uint16_t>(pack_bf16(x[0], 0.f));
   }
 }
-template <int VEC>
+template <int VEC, bool STREAM = false>
 __device__ __forceinline__ void store(fp32_t* p, const float (&x)[VEC]) {
   if constexpr (VEC == 8) {
     f32x4 a, b;
@@ -89,8 +106,8 @@ __device__ __forceinline__ void store(fp32_t* p, const float (&x)[VEC]) {
       a[i] = x[i];
       b[i] = x[4 + i];
     }
-    st4(p, a);
-    st4(p + 4, b);
+    put<STREAM>(reinterpret_cast<f32x4*>(p), a);
+    put<STREAM>(reinterpret_cast<f32x4*>(p + 4), b);
   } else if constexpr (VEC == 4) {
     f32x4 a;
 #pragma unroll
@@ -119,6 +136,21 @@ __device__ __forceinline__ float sum64(float x) {
   x += __shfl_xor(x, 16);
   x += __shfl_xor(x, 32);
   return x;
+}
+
+// Sum of the rows first, first + 16, ... below `rows` of one column of a
+// row-major matrix (p: the column's first element), eight loads in flight.
+__device__ __forceinline__ float column_sum(const float* p, int64_t row, int32_t first, int32_t rows) {
+  float part[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) part[i] = 0.f;
+  int32_t r = first;
+  for (; r + 7 * 16 < rows; r += 8 * 16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[i] += p[(r + i * 16) * row];
+  }
+  for (; r < rows; r += 16) part[0] += p[r * row];
+  return ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
 }
 
 constexpr float kLog2e = 1.4426950408889634f;

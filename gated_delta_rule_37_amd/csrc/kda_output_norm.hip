@@ -68,13 +68,13 @@ struct Share {
 };
 
 // Elements of a row of `src`, or `fill` behind its end and where src is null.
-template <int LANES, int VEC, int NV, typename E>
+template <bool STREAM = false, int LANES, int VEC, int NV, typename E>
 __device__ __forceinline__ void load_row(const Share<LANES, VEC, NV>& sh, const E* src, float fill,
                                          float (&x)[NV][VEC]) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     if (src != nullptr && sh.whole(j)) {
-      load<VEC>(src + sh.at(j), x[j]);
+      load<VEC, STREAM>(src + sh.at(j), x[j]);
     } else if (VEC == 4 && src != nullptr && sh.has(j)) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
@@ -88,12 +88,12 @@ __device__ __forceinline__ void load_row(const Share<LANES, VEC, NV>& sh, const 
     }
   }
 }
-template <int LANES, int VEC, int NV, typename E>
+template <bool STREAM = false, int LANES, int VEC, int NV, typename E>
 __device__ __forceinline__ void store_row(const Share<LANES, VEC, NV>& sh, E* dst, const float (&x)[NV][VEC]) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     if (sh.whole(j)) {
-      store<VEC>(dst + sh.at(j), x[j]);
+      store<VEC, STREAM>(dst + sh.at(j), x[j]);
     } else if (VEC == 4 && sh.has(j)) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
@@ -104,7 +104,7 @@ __device__ __forceinline__ void store_row(const Share<LANES, VEC, NV>& sh, E* ds
   }
 }
 
-template <typename O, typename E, int LANES, int VEC, int NV>
+template <typename O, typename E, bool STREAM, int LANES, int VEC, int NV>
 __global__ __launch_bounds__(kRowThreads) void norm_kernel(NormParams p) {
   __shared__ float scratch[4];
   constexpr int kGroups = kRowThreads / LANES;
@@ -124,9 +124,9 @@ __global__ __launch_bounds__(kRowThreads) void norm_kernel(NormParams p) {
   for (int64_t t = token; t < p.T; t += p.lanes) {
     const int64_t row = (t * p.H + head) * p.V;
     float o[NV][VEC], z[NV][VEC], res[NV][VEC];
-    load_row(sh, static_cast<const O*>(p.o) + row, 0.f, o);
-    load_row(sh, p.gate == nullptr ? nullptr : static_cast<const E*>(p.gate) + t * p.gate_stride + head * p.V, 0.f, z);
-    load_row(sh, p.residual == nullptr ? nullptr : static_cast<const E*>(p.residual) + row, 0.f, res);
+    load_row<STREAM>(sh, static_cast<const O*>(p.o) + row, 0.f, o);
+    load_row<STREAM>(sh, p.gate == nullptr ? nullptr : static_cast<const E*>(p.gate) + t * p.gate_stride + head * p.V, 0.f, z);
+    load_row<STREAM>(sh, p.residual == nullptr ? nullptr : static_cast<const E*>(p.residual) + row, 0.f, res);
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(kRowThreads) void norm_kernel(NormParams p) {
         o[j][i] = y + res[j][i];
       }
     }
-    store_row(sh, static_cast<E*>(p.y) + row, o);
+    store_row<STREAM>(sh, static_cast<E*>(p.y) + row, o);
   }
 }
 
@@ -232,10 +232,7 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormParams p, int32_t
   const int64_t col = static_cast<int64_t>(is_weight ? block : block - weight_blocks) * 64 + lane;
   const float* src = is_weight ? p.weight_part : p.scale_part;
   const int32_t rows = is_weight ? blocks : p.lanes;
-  float sum = 0.f;
-  if (col < columns) {
-    for (int32_t r = wave; r < rows; r += 16) sum += src[r * columns + col];
-  }
+  float sum = col < columns ? column_sum(src + col, columns, wave, rows) : 0.f;
   part[wave][lane] = sum;
   __syncthreads();
   if (wave == 0 && col < columns) {
@@ -289,10 +286,14 @@ template <typename O, typename E>
 struct LaunchForward {
   NormParams p;
   RowGrid grid;
+  bool past_caches;
   hipStream_t stream;
   template <int LANES, int VEC, int NV>
   void operator()() const {
-    hipLaunchKernelGGL((norm_kernel<O, E, LANES, VEC, NV>), dim3(grid.blocks), dim3(kRowThreads), 0, stream, p);
+    // only 16-byte accesses have the choice
+    void (*kernel)(NormParams) = VEC == 8 && past_caches ? norm_kernel<O, E, VEC == 8, LANES, VEC, NV>
+                                                         : norm_kernel<O, E, false, LANES, VEC, NV>;
+    hipLaunchKernelGGL(kernel, dim3(grid.blocks), dim3(kRowThreads), 0, stream, p);
   }
 };
 template <typename O, typename E, typename G>
@@ -307,7 +308,7 @@ struct LaunchBackward {
   }
 };
 
-constexpr int kNormBlocks = 2048;
+constexpr int kNormBlocks = 1024;   // four workgroups a CU: 415 us at 65536 x 32 heads, 461 with eight
 
 }  // namespace
 
@@ -317,10 +318,14 @@ int launch_norm(const NormArgs& a, hipStream_t stream) {
   const NormParams p = params_of(a, grid);
   (void)hipGetLastError();
   const bool o16 = a.o_format == KDA_BF16, e16 = a.dtype == KDA_BF16;
-  if (o16 && e16) with_shape(shape, LaunchForward<bf16_t, bf16_t>{p, grid, stream});
-  if (o16 && !e16) with_shape(shape, LaunchForward<bf16_t, fp32_t>{p, grid, stream});
-  if (!o16 && e16) with_shape(shape, LaunchForward<fp32_t, bf16_t>{p, grid, stream});
-  if (!o16 && !e16) with_shape(shape, LaunchForward<fp32_t, fp32_t>{p, grid, stream});
+  // Gate, fp32 o, bf16: at 2.1 GB past the caches 381 us against 415, at 268 MB
+  // 95 and 101, at 134 MB (a quarter of it from the cache) 27 and 25.
+  const int64_t per = (o16 ? 2 : 4) + (e16 ? 2 : 4) * (1 + (a.gate.ptr != nullptr) + (a.residual.ptr != nullptr));
+  const bool past = static_cast<int64_t>(a.T) * a.H * a.V * per >= kStreamBytes;
+  if (o16 && e16) with_shape(shape, LaunchForward<bf16_t, bf16_t>{p, grid, past, stream});
+  if (o16 && !e16) with_shape(shape, LaunchForward<bf16_t, fp32_t>{p, grid, past, stream});
+  if (!o16 && e16) with_shape(shape, LaunchForward<fp32_t, bf16_t>{p, grid, past, stream});
+  if (!o16 && !e16) with_shape(shape, LaunchForward<fp32_t, fp32_t>{p, grid, past, stream});
   return finish_launch();
 }
 
