@@ -21,9 +21,9 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
-// 16 bytes; STREAM: past the caches, which pays where a call's tensors are
-// larger than the 256 MB last-level cache (kStreamBytes) and costs where the
-// next launch finds them there.
+// One aligned vector; STREAM: past the caches, which pays where a call's
+// tensors are larger than the 256 MB last-level cache (kStreamBytes) and costs
+// where the next launch finds them there.
 template <bool STREAM, typename V>
 __device__ __forceinline__ V fetch(const V* p) {
   if constexpr (STREAM) return __builtin_nontemporal_load(p);
@@ -35,6 +35,33 @@ __device__ __forceinline__ void put(V* p, V v) {
     __builtin_nontemporal_store(v, p);
   } else {
     *p = v;
+  }
+}
+// The same at any address; with STREAM it is an aligned one.
+template <bool STREAM>
+__device__ __forceinline__ u32x2 fetch4(const bf16_t* p) {
+  if constexpr (STREAM) return fetch<true>(reinterpret_cast<const u32x2*>(p));
+  return *reinterpret_cast<const u32x2_any*>(p);
+}
+template <bool STREAM>
+__device__ __forceinline__ f32x4 fetch4(const fp32_t* p) {
+  if constexpr (STREAM) return fetch<true>(reinterpret_cast<const f32x4*>(p));
+  return *reinterpret_cast<const f32x4_any*>(p);
+}
+template <bool STREAM>
+__device__ __forceinline__ void put4(bf16_t* p, u32x2 v) {
+  if constexpr (STREAM) {
+    put<true>(reinterpret_cast<u32x2*>(p), v);
+  } else {
+    *reinterpret_cast<u32x2_any*>(p) = v;
+  }
+}
+template <bool STREAM>
+__device__ __forceinline__ void put4(fp32_t* p, f32x4 v) {
+  if constexpr (STREAM) {
+    put<true>(reinterpret_cast<f32x4*>(p), v);
+  } else {
+    *reinterpret_cast<f32x4_any*>(p) = v;
   }
 }
 
@@ -50,7 +77,7 @@ __device__ __forceinline__ void load(const bf16_t* p, float (&x)[VEC]) {
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   } else if constexpr (VEC == 4) {
-    const u32x2 w = *reinterpret_cast<const u32x2_any*>(p);
+    const u32x2 w = fetch4<STREAM>(p);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       x[2 * i] = __uint_as_float(w[i] << 16);
@@ -71,7 +98,7 @@ __device__ __forceinline__ void load(const fp32_t* p, float (&x)[VEC]) {
       x[4 + i] = b[i];
     }
   } else if constexpr (VEC == 4) {
-    const f32x4 a = *reinterpret_cast<const f32x4_any*>(p);
+    const f32x4 a = fetch4<STREAM>(p);
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = a[i];
   } else {
@@ -92,7 +119,7 @@ __device__ __forceinline__ void store(bf16_t* p, const float (&x)[VEC]) {
     u32x2 w;
     w[0] = pack_bf16(x[0], x[1]);
     w[1] = pack_bf16(x[2], x[3]);
-    *reinterpret_cast<u32x2_any*>(p) = w;
+    put4<STREAM>(p, w);
   } else {
     *p = static_cast<uint16_t>(pack_bf16(x[0], 0.f));
   }
@@ -112,7 +139,7 @@ __device__ __forceinline__ void store(fp32_t* p, const float (&x)[VEC]) {
     f32x4 a;
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = x[i];
-    *reinterpret_cast<f32x4_any*>(p) = a;
+    put4<STREAM>(p, a);
   } else {
     *p = x[0];
   }
@@ -161,14 +188,6 @@ struct RawVec {
   E e[VEC];
 };
 template <>
-struct RawVec<bf16_t, 8> {
-  u32x4 w;
-};
-template <>
-struct RawVec<fp32_t, 8> {
-  f32x4 a, b;
-};
-template <>
 struct RawVec<bf16_t, 4> {
   u32x2 w;
 };
@@ -187,38 +206,22 @@ __device__ __forceinline__ void forget(RawVec<fp32_t, 1>& r) { asm volatile("" :
 __device__ __forceinline__ void forget(RawVec<bf16_t, 4>& r) { asm volatile("" : "+v"(r.w)); }
 __device__ __forceinline__ void forget(RawVec<fp32_t, 4>& r) { asm volatile("" : "+v"(r.a)); }
 
-template <typename E, int VEC>
-__device__ __forceinline__ void load_raw(const E* p, RawVec<E, VEC>& r) {
-  static_assert(VEC == 1, "");
-  r.e[0] = *p;
+template <bool STREAM, typename E>
+__device__ __forceinline__ void load_raw(const E* p, RawVec<E, 1>& r) { r.e[0] = fetch<STREAM>(p); }
+template <bool STREAM>
+__device__ __forceinline__ void load_raw(const bf16_t* p, RawVec<bf16_t, 4>& r) {
+  r.w = fetch4<STREAM>(p);
 }
-template <>
-__device__ __forceinline__ void load_raw<bf16_t, 8>(const bf16_t* p, RawVec<bf16_t, 8>& r) {
-  r.w = *reinterpret_cast<const u32x4*>(p);
-}
-template <>
-__device__ __forceinline__ void load_raw<fp32_t, 8>(const fp32_t* p, RawVec<fp32_t, 8>& r) {
-  r.a = ld4(p);
-  r.b = ld4(p + 4);
-}
-template <>
-__device__ __forceinline__ void load_raw<bf16_t, 4>(const bf16_t* p, RawVec<bf16_t, 4>& r) {
-  r.w = *reinterpret_cast<const u32x2_any*>(p);
-}
-template <>
-__device__ __forceinline__ void load_raw<fp32_t, 4>(const fp32_t* p, RawVec<fp32_t, 4>& r) {
-  r.a = *reinterpret_cast<const f32x4_any*>(p);
+template <bool STREAM>
+__device__ __forceinline__ void load_raw(const fp32_t* p, RawVec<fp32_t, 4>& r) {
+  r.a = fetch4<STREAM>(p);
 }
 __device__ __forceinline__ float element(const RawVec<bf16_t, 1>& r, int) { return bf2f(r.e[0]); }
 __device__ __forceinline__ float element(const RawVec<fp32_t, 1>& r, int) { return r.e[0]; }
-__device__ __forceinline__ float element(const RawVec<bf16_t, 8>& r, int i) {
-  return __uint_as_float(i % 2 == 0 ? r.w[i / 2] << 16 : r.w[i / 2] & 0xffff0000u);
-}
 __device__ __forceinline__ float element(const RawVec<bf16_t, 4>& r, int i) {
   return __uint_as_float(i % 2 == 0 ? r.w[i / 2] << 16 : r.w[i / 2] & 0xffff0000u);
 }
 __device__ __forceinline__ float element(const RawVec<fp32_t, 4>& r, int i) { return r.a[i]; }
-__device__ __forceinline__ float element(const RawVec<fp32_t, 8>& r, int i) { return i < 4 ? r.a[i] : r.b[i - 4]; }
 
 // 1 - e^g for g <= 0, given a = e^g.  The difference cancels near 0; above
 // -1/4 the Taylor sum to g^6 / 6! replaces it, exact to 2^-24 relative.

@@ -44,10 +44,12 @@ struct ScanParams {
 };
 
 // LPR lanes of VEC channels make a row of 64 channels; a thread takes R
-// tokens, so that every geometry has the same tile.  LOOK: see look_back.
-template <int VEC_, int LPR_, int R_, int LOOK_>
+// tokens, so that every geometry has the same tile.  LOOK: see look_back;
+// STREAM: past the caches.
+template <int VEC_, int LPR_, int R_, int LOOK_, bool STREAM_>
 struct Geometry {
   static constexpr int VEC = VEC_, LPR = LPR_, R = R_, LOOK = LOOK_;
+  static constexpr bool STREAM = STREAM_;
   static_assert(VEC * LPR == kScanChannels && kScanThreads / LPR * R == kScanTile, "");
 };
 static_assert(kScanTile < kScanThreads, "a thread for each token boundary of a tile");
@@ -63,6 +65,16 @@ __device__ __forceinline__ float apply(float A, float B, float h) { return A == 
 // atomics, which reach past the XCDs' own L2 caches.
 constexpr uint32_t kEmpty = 0xffffffffu;
 __device__ __forceinline__ uint32_t float_bits(float x) { return x != x ? 0x7fc00000u : __float_as_uint(x); }
+
+// This workgroup's channel block; each block gets as many workgroups as there
+// are tiles.  Workgroups go round the 8 XCDs in launch order: without the shift
+// from round to round, an XCD would keep the same blocks where their number is
+// a multiple of 8, lines 1 KiB apart, and use few of its L2's channels (65536 x
+// 4096 forward: 310 us against 363).
+__device__ __forceinline__ int32_t column_of(const ScanParams& p) {
+  const uint32_t columns = static_cast<uint32_t>(p.columns), round = blockIdx.x / columns;
+  return static_cast<int32_t>((blockIdx.x + 5 * round) % columns);
+}
 
 // The next tile of this workgroup's channel block.  Tickets are handed out in
 // the order of the tiles, so every tile before this one belongs to a workgroup
@@ -223,15 +235,15 @@ struct Span {
 
 // Rows row, row + DIR, ... (tokens from the span's first) of channel dl; where
 // not FULL, limited to [0, most].
-template <int DIR, bool FULL, int VEC, int R, typename E>
+template <int DIR, bool FULL, bool STREAM, int VEC, int R, typename E>
 __device__ __forceinline__ void fetch_rows(const Span<E>& s, int32_t row, int32_t dl, int32_t most, RawVec<E, VEC> (&x)[R]) {
   const uint32_t off = s.offset(row, dl);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     if constexpr (FULL) {
-      load_raw<E, VEC>(s.at(off, DIR * r), x[r]);
+      load_raw<STREAM>(s.at(off, DIR * r), x[r]);
     } else {
-      load_raw<E, VEC>(s.at(s.offset(max(min(row + DIR * r, most), 0), dl), 0), x[r]);
+      load_raw<STREAM>(s.at(s.offset(max(min(row + DIR * r, most), 0), dl), 0), x[r]);
     }
   }
 }
@@ -294,7 +306,7 @@ template <typename E, typename O, typename G, bool TIED>
 __global__ __launch_bounds__(kScanThreads) void scan_kernel(ScanParams p) {
   constexpr int VEC = G::VEC, R = G::R;
   __shared__ __align__(16) TileLds<G> lds;
-  const int32_t column = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(p.columns));
+  const int32_t column = column_of(p);
   const int32_t tile = take_ticket(p, column, &lds.ticket);
   if (tile >= p.tiles) return;
   const int32_t row = threadIdx.x / G::LPR * R;                                // first token in the tile
@@ -308,8 +320,8 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(ScanParams p) {
   const Span<O> hs(p.h, p.D, begin);
   RawVec<E, VEC> x[R], g[R];
   with_flag(left == kScanTile, [&](auto full) {
-    fetch_rows<1, full.value>(gs, row, dl, left - 1, g);
-    fetch_rows<1, full.value>(xs, row, dl, left - 1, x);
+    fetch_rows<1, full.value, G::STREAM>(gs, row, dl, left - 1, g);
+    fetch_rows<1, full.value, G::STREAM>(xs, row, dl, left - 1, x);
   });
   const bool marked = mark_sequences(p, begin, lds.mark);
   const uint32_t out = hs.offset(row, dl);
@@ -348,7 +360,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(ScanParams p) {
         h[i] = a * h[i] + v;
       }
       if (owner && (plain.value || row + r < left)) {
-        store<VEC>(hs.at(out, r), h);
+        store<VEC, G::STREAM>(hs.at(out, r), h);
         if (!plain.value) {
           const int32_t next = lds.mark[row + r + 1];   // the sequence after one that ends here
           if (next > 0) store<VEC>(p.final_state + static_cast<int64_t>(next - 2) * p.D + dl, h);
@@ -364,7 +376,7 @@ template <typename E, typename O, typename G, bool TIED>
 __global__ __launch_bounds__(kScanThreads) void scan_backward_kernel(ScanParams p) {
   constexpr int VEC = G::VEC, R = G::R;
   __shared__ __align__(16) TileLds<G> lds;
-  const int32_t column = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(p.columns));
+  const int32_t column = column_of(p);
   const int32_t tile = take_ticket(p, column, &lds.ticket);
   if (tile >= p.tiles) return;
   const int32_t row = threadIdx.x / G::LPR * R;
@@ -379,11 +391,11 @@ __global__ __launch_bounds__(kScanThreads) void scan_backward_kernel(ScanParams 
   RawVec<E, VEC> x[R], g[R];
   RawVec<O, VEC> dh[R], before[R];                                      // before: h_{t-1}
   with_flag(base >= 1, [&](auto full) {
-    fetch_rows<-1, full.value>(gs, token, dl, left - 1, g);
-    fetch_rows<-1, full.value>(dhs, token, dl, left - 1, dh);
-    if (TIED) fetch_rows<-1, full.value>(xs, token, dl, left - 1, x);
+    fetch_rows<-1, full.value, G::STREAM>(gs, token, dl, left - 1, g);
+    fetch_rows<-1, full.value, G::STREAM>(dhs, token, dl, left - 1, dh);
+    if (TIED) fetch_rows<-1, full.value, G::STREAM>(xs, token, dl, left - 1, x);
     // token - 1 of the tensor; where there is none (the first token of all), that one
-    fetch_rows<-1, full.value>(hs, base >= 1 ? token : token - 1, dl, left - 1, before);
+    fetch_rows<-1, full.value, G::STREAM>(hs, base >= 1 ? token : token - 1, dl, left - 1, before);
   });
   const bool marked = mark_sequences(p, base, lds.mark);
   const uint32_t out = dxs.offset(max(token, 0), dl);
@@ -424,8 +436,8 @@ __global__ __launch_bounds__(kScanThreads) void scan_backward_kernel(ScanParams 
         dg[i] = c[i] * (TIED ? hp[i] - element(x[r], i) : hp[i]);
       }
       if (owner && valid) {
-        store<VEC>(dxs.at(out, -r), dx);
-        store<VEC>(dgs.at(out, -r), dg);
+        store<VEC, G::STREAM>(dxs.at(out, -r), dx);
+        store<VEC, G::STREAM>(dgs.at(out, -r), dg);
         if (start > 0 && p.d_initial_state != nullptr) {
           store<VEC>(p.d_initial_state + static_cast<int64_t>(start - 1) * p.D + dl, c);
         }
@@ -473,9 +485,14 @@ int run(ScanParams p, bool tied, bool backward, void* workspace, hipStream_t str
 // window of 4 against one of 16: 4096 channels (64 blocks) 193 and 227 us,
 // 2048 109 and 122, 1024 77 and 68, 512 65 and 44, 64 57 and 36.
 constexpr int32_t kNarrowBlocks = 24;
-using Vector = Geometry<4, 16, 8, 4>;         // rows of at least one 4-element vector
-using VectorNarrow = Geometry<4, 16, 8, 16>;  // the same, of fewer than kNarrowBlocks blocks
-using Scalar = Geometry<1, 64, 32, 16>;       // rows of up to three elements
+using Vector = Geometry<4, 16, 8, 4, false>;         // rows of at least one 4-element vector
+// The same from kStreamBytes on, if every row is whole 128-byte lines.  At
+// 1.6 GB (65536 x 4096 forward) past the caches 364 us against 388, at 101 MB
+// (4096 x 4096) 32 and 29; with lines that two rows share (32768 x 4093) 344
+// and 269.
+using VectorStream = Geometry<4, 16, 8, 4, true>;
+using VectorNarrow = Geometry<4, 16, 8, 16, false>;  // of fewer than kNarrowBlocks blocks
+using Scalar = Geometry<1, 64, 32, 16, false>;       // rows of up to three elements
 
 template <typename G>
 int run_types(const ScanArgs& a, bool backward, const ScanParams& p, hipStream_t stream) {
@@ -509,6 +526,14 @@ int launch_either(const ScanArgs& a, bool backward, hipStream_t stream) {
   p.d_initial_state = static_cast<float*>(a.d_initial_state.ptr);
   if (a.D < Vector::VEC) return run_types<Scalar>(a, backward, p, stream);
   if (a.D < kNarrowBlocks * kScanChannels) return run_types<VectorNarrow>(a, backward, p, stream);
+  const int64_t e = a.dtype == KDA_BF16 ? 2 : 4, eh = a.h_format == KDA_BF16 ? 2 : 4;
+  const bool reads_x = !backward || a.tied != 0;
+  const int64_t element = backward ? (a.tied != 0 ? 4 : 3) * e + 2 * eh : 2 * e + eh;
+  // whole 128-byte lines in every row of every tensor
+  const bool lines = a.D % 64 == 0 && a.g.stride % 64 == 0 && (!reads_x || a.x.stride % 64 == 0);
+  if (lines && static_cast<int64_t>(p.T) * p.D * element >= kStreamBytes) {
+    return run_types<VectorStream>(a, backward, p, stream);
+  }
   return run_types<Vector>(a, backward, p, stream);
 }
 

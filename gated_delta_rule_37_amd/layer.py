@@ -196,8 +196,11 @@ def _scratch(size, device, stream):
     that stream."""
     if size == 0:
         return _NULL
-    with torch.cuda.stream(stream):   # None: stay on the current one
+    if stream is None:
         ws = torch.empty(size, dtype=torch.uint8, device=device)
+    else:
+        with torch.cuda.stream(stream):
+            ws = torch.empty(size, dtype=torch.uint8, device=device)
     return (ws.data_ptr(), size)
 
 

@@ -368,6 +368,99 @@ def test_steps_continue_a_forward():
         assert (state[n] - ref).abs().max() <= 1e-4 * ref.abs().max()
 
 
+# ------------------------------------------------------------- beyond 32 bits
+
+
+def test_step_in_a_long_pool():
+    """A pool of more than 2^31 elements: the last slots' addresses need 64 bits."""
+    H, n = 32, 4200                          # 2.2e9 elements, 8.8 GB
+    state = torch.empty(n, H, 128, 128, device=DEV)
+    slots = torch.tensor([n - 1, 0, n - 2, n], dtype=torch.int32)
+    x = _step_inputs(4, H, seed=3, slow=True)
+    init = _randn(3, H, 128, 128, seed=4)
+    for i, at in enumerate((n - 1, 0, n - 2)):
+        state[at] = _d(init[i])
+    o = layer.step(*(_d(t) for t in x.values()), state, _d(slots))
+    want_o, want, eo, ep = lr.step(*(t.double() for t in x.values()), init.double(), torch.tensor([0, 1, 2, 3]),
+                                   torch.zeros(4, H, 128).double())
+    lr.assert_close(o[:3], want_o[:3], eo[:3], "o")
+    lr.assert_close(state[[n - 1, 0, n - 2]], want, ep, "state")
+
+
+def test_scan_of_many_elements():
+    """More than 2^31 elements of x, g and h: the last sequence's rows."""
+    T, D, last = (1 << 20) + 300, 2056, 300
+    cu = [0, 1 << 20, T]
+    x = torch.zeros(T, D, dtype=BF, device=DEV)
+    g = torch.zeros(T, D, dtype=BF, device=DEV)
+    xl, gl, h0l, _ = _scan_case([0, last], D, BF, True, True, False, seed=6, slow=True)
+    x[-last:], g[-last:] = _d(xl), _d(gl)
+    x[0] = 1.0                               # the first sequence carries it to its end: g = 0
+    h0 = torch.zeros(2, D, device=DEV)
+    h0[1] = _d(h0l[0])
+    got = layer.scan_forward(kda.Plan(cu, 1), x, g, initial_state=h0)
+    h, final = lr.scan(xl.double(), gl.double(), [0, last], _w(h0l), False)
+    eh, ef = lr.scan_bound(xl.double(), gl.double(), [0, last], _w(h0l), False)
+    lr.assert_close(got["h"][-last:], h, eh, "h")
+    lr.assert_close(got["final_state"][1:], final, ef, "final_state")
+    assert (got["final_state"][0] == 1).all() and (got["h"][(1 << 20) - 1] == 1).all()
+    back = layer.scan_backward(kda.Plan(cu, 1), None, g, got["h"], x, initial_state=h0)
+    args = (xl.double(), gl.double(), got["h"][-last:].cpu().double(), [0, last], _w(h0l), False, xl.double(), None)
+    want, bounds = lr.scan_backward(*args), lr.scan_backward_bounds(*args)
+    for n in ("dx", "dg"):
+        lr.assert_close(back[n][-last:], want[n], bounds[n], n)
+    lr.assert_close(back["dh0"][1:], want["dh0"], bounds["dh0"], "dh0")
+    assert (back["dx"][0] == 1).all() and (back["dh0"][0] == 1).all()
+
+
+def test_rows_beyond_32_bits():
+    """The row-wise operators behind 2^31 elements of one tensor."""
+    T, H = 270000, 64                        # 2.2e9 elements of 128-channel heads
+    tail = 5
+    z = torch.zeros(T, H, 128, dtype=BF, device=DEV)
+    zl, b = _randn(tail, H, 128, seed=1, dtype=BF), torch.zeros(T, H, dtype=BF, device=DEV)
+    z[-tail:] = _d(zl)
+    a_log = torch.zeros(H, device=DEV)
+    got = layer.prepare_inputs(z, z, z, b, a_log)
+    w = zl.double()
+    zero = torch.zeros(tail, H).double()
+    want = lr.prepare(w, w, w, zero, torch.zeros(H).double(), None, 1.0, 1e-6)
+    bounds = lr.prepare_bounds(want, w, torch.zeros(H).double(), None)
+    for n in ("q", "k", "g"):
+        lr.assert_close(got[n][-tail:], want[n], bounds[n] + 1e-6 * want[n].abs(), n)
+    del got
+    weight = torch.ones(128, device=DEV)
+    y = layer.output_norm(z, weight, gate=z, residual=z)
+    args = dict(o=w, weight=torch.ones(128).double(), gate=w, kind="sigmoid", res_scale=None, residual=w, eps=1e-6)
+    lr.assert_close(y[-tail:], lr.output_norm(**args), lr.output_norm_bound(**args), "y")
+
+
+@pytest.mark.parametrize("D", [1472, 1536, 1540, 8192])
+def test_scan_widths(D):
+    """Both sides of the window's and the cached accesses' rules (8192 channels
+    of 8192 tokens are past the caches)."""
+    cu = [0, 100, 8192 if D == 8192 else 700]
+    x, g, h0, dev = _scan_case(cu, 64, BF, True, True, False, seed=D, slow=True)
+    T = cu[-1]
+    dx, dg_, dh0 = (torch.zeros(*s, D, dtype=t, device=DEV) for s, t in (((T,), BF), ((T,), BF), ((2,), F32)))
+    at = torch.cat([torch.arange(0, 32), torch.arange(D - 32, D)])     # the first and last channels carry the case
+    dx[:, at], dg_[:, at], dh0[:, at] = dev[0], dev[1], _d(h0)
+    got = layer.scan_forward(kda.Plan(cu, 1), dx, dg_, initial_state=dh0, tied=True, h_dtype=F32)
+    h, final = lr.scan(x.double(), g.double(), cu, _w(h0), True)
+    eh, ef = lr.scan_bound(x.double(), g.double(), cu, _w(h0), True)
+    lr.assert_close(got["h"][:, at], h, eh, "h")
+    lr.assert_close(got["final_state"][:, at], final, ef, "final_state")
+    assert not got["h"][:, 32:D - 32].any()
+    dh = torch.zeros(T, D, device=DEV)
+    part = _randn(T, 64, seed=2)
+    dh[:, at] = _d(part)
+    back = layer.scan_backward(kda.Plan(cu, 1), dx, dg_, got["h"], dh, initial_state=dh0, tied=True)
+    args = (x.double(), g.double(), got["h"][:, at].cpu().double(), cu, _w(h0), True, part.double(), None)
+    want, bounds = lr.scan_backward(*args), lr.scan_backward_bounds(*args)
+    for n in ("dx", "dg", "dh0"):
+        lr.assert_close(back[n][:, at], want[n], bounds[n], n)
+
+
 # ------------------------------------------------------------- together
 
 
