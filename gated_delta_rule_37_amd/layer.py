@@ -124,7 +124,7 @@ def _call(name, device, args, stream):
         fn = _functions[name] = getattr(kda.lib(), name)
     index = device.index
     raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         status = fn(*args, raw)
     else:
         with torch.cuda.device(index):
