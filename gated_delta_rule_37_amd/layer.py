@@ -35,7 +35,7 @@ final_state::
     y = layer.output_norm(o, weight, gate=z, activation="sigmoid")
 
 Every call enqueues on ``stream`` (default: the current stream of its tensors'
-device) and returns without waiting.  A tensor on another device than the rest
+device) and returns without waiting; what it allocates belongs to that stream.  A tensor on another device than the rest
 raises ValueError.
 """
 from __future__ import annotations
@@ -156,8 +156,8 @@ def prepare_inputs(q_raw, k_raw, gate_raw, beta_raw, a_log, dt_bias=None, q_scal
     T, H, K, dev, args = _raw(q_raw, k_raw, gate_raw, beta_raw, a_log, dt_bias, q_scale, eps)
     bf = torch.bfloat16
     if out is None:
-        out = {n: torch.empty(T, H, K, dtype=bf, device=dev) for n in ("q", "k", "g")}
-        out["beta"] = torch.empty(T, H, dtype=bf, device=dev)
+        out = {n: _empty(stream, dev, bf, T, H, K) for n in ("q", "k", "g")}
+        out["beta"] = _empty(stream, dev, bf, T, H)
         for t in out.values():
             args += _made(t)
     else:
@@ -179,10 +179,10 @@ def prepare_inputs_backward(q_raw, k_raw, gate_raw, beta_raw, a_log, dt_bias, dq
     for n, t in (("dq", dq), ("dk", dk), ("dg", dg)):
         args += _buf(t, f32, (T, H, K), n, dev)
     args += _buf(dbeta, f32, (T, H), "dbeta", dev)
-    out = {n: torch.empty(T, H, K, dtype=dt, device=dev) for n in ("dq_raw", "dk_raw", "dgate_raw")}
-    out["dbeta_raw"] = torch.empty(T, H, dtype=dt, device=dev)
-    out["da_log"] = torch.empty(H, dtype=f32, device=dev)
-    out["ddt_bias"] = None if dt_bias is None else torch.empty(H, K, dtype=f32, device=dev)
+    out = {n: _empty(stream, dev, dt, T, H, K) for n in ("dq_raw", "dk_raw", "dgate_raw")}
+    out["dbeta_raw"] = _empty(stream, dev, dt, T, H)
+    out["da_log"] = _empty(stream, dev, f32, H)
+    out["ddt_bias"] = None if dt_bias is None else _empty(stream, dev, f32, H, K)
     for n in ("dq_raw", "dk_raw", "dgate_raw", "dbeta_raw", "da_log", "ddt_bias"):
         args += _made(out[n])
     args += _scratch(kda.lib().kda_prepare_inputs_backward_workspace_bytes(T, H, K), dev, stream)
@@ -190,18 +190,18 @@ def prepare_inputs_backward(q_raw, k_raw, gate_raw, beta_raw, a_log, dt_bias, dq
     return out
 
 
-def _scratch(size, device, stream):
-    """A workspace of ``size`` bytes for one call.  It is allocated on the call's
-    stream, so that torch's allocator hands the memory on only to later work of
-    that stream."""
-    if size == 0:
-        return _NULL
+def _empty(stream, device, dtype, *shape):
+    """Uninitialised memory of the call's stream: torch's allocator hands it on,
+    once it is free, only to later work of that stream."""
     if stream is None:
-        ws = torch.empty(size, dtype=torch.uint8, device=device)
-    else:
-        with torch.cuda.stream(stream):
-            ws = torch.empty(size, dtype=torch.uint8, device=device)
-    return (ws.data_ptr(), size)
+        return torch.empty(*shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, dtype=dtype, device=device)
+
+
+def _scratch(size, device, stream):
+    """A workspace of ``size`` bytes for one call."""
+    return _NULL if size == 0 else (_empty(stream, device, torch.uint8, size).data_ptr(), size)
 
 
 def _norm(o, weight, gate, activation, res_scale, dtype):
@@ -236,7 +236,7 @@ def output_norm(o, weight, gate=None, activation="sigmoid", res_scale=None, resi
     if dtype not in DTYPES:
         raise TypeError(f"dtype: expected one of {list(DTYPES)}, got {dtype}")
     if out is None:
-        out = torch.empty(T, H, V, dtype=dtype, device=dev)
+        out = _empty(stream, dev, dtype, T, H, V)
     args = [T, H, V, *_buf(o, o.dtype, (T, H, V), "o", dev), _dtype(o, "o"), *gated, *weights,
             *_buf(residual, dtype, (T, H, V), "residual", dev), DTYPES[dtype], float(eps),
             *_buf(out, dtype, (T, H, V), "out", dev)]
@@ -255,22 +255,22 @@ def output_norm_backward(dy, o, weight, gate=None, activation="sigmoid", res_sca
     if d_o_dtype not in DTYPES:
         raise TypeError(f"d_o_dtype: expected one of {list(DTYPES)}, got {d_o_dtype}")
     f32 = torch.float32
-    out = dict(d_o=torch.empty(T, H, V, dtype=d_o_dtype, device=dev),
-               d_gate=None if gate is None else torch.empty(T, H, V, dtype=dtype, device=dev),
-               d_weight=torch.empty(V, dtype=f32, device=dev),
-               d_res_scale=None if res_scale is None else torch.empty(H, V, dtype=f32, device=dev))
+    out = dict(d_o=_empty(stream, dev, d_o_dtype, T, H, V),
+               d_gate=None if gate is None else _empty(stream, dev, dtype, T, H, V),
+               d_weight=_empty(stream, dev, f32, V),
+               d_res_scale=None if res_scale is None else _empty(stream, dev, f32, H, V))
     args = [T, H, V, *_buf(dy, dtype, (T, H, V), "dy", dev), *_buf(o, o.dtype, (T, H, V), "o", dev), _dtype(o, "o"),
             *gated, *weights, _dtype(dy, "dy"), float(eps), *_made(out["d_o"]),
             DTYPES[d_o_dtype], *_made(out["d_gate"]),
-            *_made(out["d_weight"]),
-            *_made(out["d_res_scale"]),
+            *_made(out["d_weight"]), *_made(out["d_res_scale"]),
             *_scratch(kda.lib().kda_output_norm_backward_workspace_bytes(T, H, V), dev, stream)]
     _call("kda_output_norm_backward", dev, args, stream)
     return out
 
 
 def scan_segments(cu_seqlens, D: int) -> int:
-    """The segment count for a plan that only the scan uses."""
+    """The segment count for a plan that only the scan uses: the scan cuts the
+    tokens into tiles by itself, whatever the plan's segments are, so one."""
     return 1
 
 
@@ -293,8 +293,8 @@ def scan_forward(plan: kda.Plan, x, g, initial_state=None, tied=False, h_dtype=N
     final_state), h in ``h_dtype`` (default: x's), final_state fp32."""
     T, D, dev, args = _scan(plan, x, g, initial_state, tied)
     if out is None:
-        out = dict(h=torch.empty(T, D, dtype=g.dtype if h_dtype is None else h_dtype, device=dev),
-                   final_state=torch.empty(plan.N, D, dtype=torch.float32, device=dev))
+        out = dict(h=_empty(stream, dev, g.dtype if h_dtype is None else h_dtype, T, D),
+                   final_state=_empty(stream, dev, torch.float32, plan.N, D))
     h = out["h"]
     args += [*_buf(h, h.dtype, (T, D), "h", dev), _dtype(h, "h"),
              *_buf(out["final_state"], torch.float32, (plan.N, D), "final_state", dev),
@@ -312,8 +312,8 @@ def scan_backward(plan: kda.Plan, x, g, h, dh, d_final=None, initial_state=None,
     T, D, dev, args = _scan(plan, x if tied else None, g, initial_state, tied)
     f32 = torch.float32
     want = initial_state is not None if want_dh0 is None else want_dh0
-    out = dict(dx=torch.empty(T, D, dtype=g.dtype, device=dev), dg=torch.empty(T, D, dtype=g.dtype, device=dev),
-               dh0=torch.empty(plan.N, D, dtype=f32, device=dev) if want else None)
+    out = dict(dx=_empty(stream, dev, g.dtype, T, D), dg=_empty(stream, dev, g.dtype, T, D),
+               dh0=_empty(stream, dev, f32, plan.N, D) if want else None)
     args += [*_buf(h, h.dtype, (T, D), "h", dev), *_buf(dh, h.dtype, (T, D), "dh", dev), _dtype(h, "h"),
              *_buf(d_final, f32, (plan.N, D), "d_final", dev), *_made(out["dx"]),
              *_made(out["dg"]), *_made(out["dh0"]),
@@ -340,7 +340,7 @@ def scan_step(x, g, state, slots=None, state_out=None, h=None, tied=False, strea
     B, D = x.shape
     dt, dev = x.dtype, x.device
     if h is None:
-        h = torch.empty(B, D, dtype=dt, device=dev)
+        h = _empty(stream, dev, dt, B, D)
     n, slots, pool = _pool(B, state, slots, state_out, (D,), dev)
     args = [B, D, _dtype(x, "x"), *_buf(x, dt, (B, D), "x", dev), *_buf(g, dt, (B, D), "g", dev), int(bool(tied)),
             *slots, n, *pool, *_buf(h, dt, (B, D), "h", dev)]
@@ -360,7 +360,7 @@ def step(q, k, v, g, beta, state, slots=None, state_out=None, o=None, o_dtype=to
     V = v.shape[2]
     bf, dev = torch.bfloat16, k.device
     if o is None:
-        o = torch.empty(B, H, V, dtype=o_dtype, device=dev)
+        o = _empty(stream, dev, o_dtype, B, H, V)
     n, slots, pool = _pool(B, state, slots, state_out, (H, K, V), dev)
     bound = float("-inf") if gate_lower_bound is None else float(gate_lower_bound)
     args = [B, H, K, V, *kda._heads(H, heads), *_buf(q, bf, (B, H, K), "q", dev), *_buf(k, bf, (B, H, K), "k", dev),

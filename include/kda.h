@@ -529,6 +529,7 @@ size_t kda_prepare_inputs_backward_workspace_bytes(int32_t T, int32_t H, int32_t
  *   weight    [V]; res_scale [H, V] or NULL (one); residual [T, H, V] dtype or
  *             NULL (zero)
  *   y         [T, H, V] dtype; it may be the residual itself, in place
+ * mean_v o^2 has to stay finite in FP32; a row of zeros gives the residual.
  */
 int kda_output_norm(int32_t T, int32_t H, int32_t V, const void* o, size_t o_bytes, int32_t o_format,
                     const void* gate, size_t gate_bytes, int64_t gate_stride, int32_t activation,
@@ -567,8 +568,9 @@ size_t kda_output_norm_backward_workspace_bytes(int32_t T, int32_t H, int32_t V)
  *   tied           0 or 1
  *   initial_state  [N, D] FP32 or NULL (zero)
  *   h              [T, D] in h_format; final_state [N, D] FP32
- * Only the plan's sequences count: its segments and pieces change nothing.  An
- * infinity or NaN stays in its own sequence.
+ * Only the plan's sequences count: its segments and pieces change nothing.
+ * States have to stay finite in FP32; an infinity or NaN stays in its own
+ * sequence, and there a decay of exactly 0 may or may not end it.
  * Workspace: kda_scan_workspace_bytes(plan, D) bytes, NULL where that is 0 (at
  * most 128 tokens).  Its contents are not needed afterwards.  Two calls that
  * may run at the same time need a workspace each: sharing one gives undefined

@@ -631,3 +631,37 @@ def test_other_stream():
     stream.synchronize()
     for n in ref:
         assert torch.equal(out[n], ref[n])
+
+
+def test_two_streams_at_once():
+    """Calls that run at the same time, each with its own workspace: scans of
+    many tiles, backward sums, steps; every result as when run alone."""
+    cu, D = [0, 20000], 512
+    plan = kda.Plan(cu, 1)
+    plan.device_blob(DEV)
+    sets, ref = [], []
+    for i in range(2):
+        _, _, h0, dev = _scan_case(cu, D, BF, True, True, False, seed=20 + i, slow=True)
+        raw, a_log, dt_bias = _prepare_inputs(300, 8, BF, True, seed=30 + i)
+        grads = [_d(_randn(300, 8, 128, seed=40 + i)) for _ in range(3)] + [_d(_randn(300, 8, seed=41 + i))]
+        sets.append((dev, _d(h0), [_d(t) for t in raw.values()], _d(a_log), _d(dt_bias), grads))
+
+    def work(s, stream=None):
+        dev, h0, raw, a_log, dt_bias, grads = s
+        f = layer.scan_forward(plan, *dev, initial_state=h0, tied=True, stream=stream)
+        b = layer.scan_backward(plan, *dev, f["h"], dev[0], initial_state=h0, tied=True, stream=stream)
+        r = layer.prepare_inputs_backward(*raw, a_log, dt_bias, *grads, stream=stream)
+        return [*f.values(), *b.values(), *r.values()]
+
+    for s in sets:
+        ref.append(work(s))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        got = [work(s, st) for s, st in zip(sets, streams)]
+        for st in streams:
+            st.synchronize()
+        for a, b in zip(got, ref):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
