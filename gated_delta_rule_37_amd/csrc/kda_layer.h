@@ -79,7 +79,6 @@ constexpr int kRowThreads = 256;        // row-wise kernels
 constexpr int64_t kStreamBytes = int64_t(256) << 20;   // the last-level cache: larger calls go past it
 constexpr int kPrepareGroups = 16;      // 16-lane groups of 8 channels a workgroup
 constexpr int kPrepareBwdBlocks = 512;  // backward grid at most: two workgroups a CU
-constexpr int kNormBwdBlocks = 512;
 
 struct PrepareBwdLayout {
   RowGrid grid;
@@ -87,20 +86,20 @@ struct PrepareBwdLayout {
 };
 PrepareBwdLayout prepare_bwd_layout(int32_t T, int32_t H);
 
-// The norm's lane group for rows of V channels: `lanes` threads a row,
-// `vec` elements at a time, `nv` times.
+// The norm's lane group for rows of V channels: `lanes` threads a row, each
+// with `vectors` vectors of 8 channels.
 struct NormShape {
-  int32_t lanes, vec, nv;
+  int32_t lanes, vectors;
 };
-NormShape norm_shape(int32_t V, bool vector_rows);
+NormShape norm_shape(int32_t V);
+int32_t norm_threads(const NormShape& shape);   // a workgroup's
 
 struct NormBwdLayout {
   RowGrid grid;
   size_t weight, scale, total;   // byte offsets: [blocks][V] and [P][H][V] FP32
 };
-NormBwdLayout norm_bwd_layout(int32_t T, int32_t H, int32_t V, const NormShape& shape);
-size_t norm_bwd_workspace(int32_t T, int32_t H, int32_t V);
-bool norm_vector_rows(const NormArgs& a);
+NormBwdLayout norm_bwd_layout(int32_t T, int32_t H, int32_t V);
+bool norm_whole_rows(const NormArgs& a);   // rows of whole, aligned 16-byte vectors
 
 // The scan's tiles: kScanTile tokens of kScanChannels channels, one workgroup
 // each.  More than one token tile need words of workspace in which tiles leave

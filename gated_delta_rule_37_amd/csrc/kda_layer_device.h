@@ -20,6 +20,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // writes them whole; aligned ones cost nothing extra).
 typedef u32x2 u32x2_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
 // One aligned vector; STREAM: past the caches, which pays where a call's
 // tensors are larger than the 256 MB last-level cache (kStreamBytes) and costs
@@ -107,6 +108,35 @@ __device__ __forceinline__ void load(const fp32_t* p, float (&x)[VEC]) {
   }
 }
 
+// Eight elements at any address.
+__device__ __forceinline__ void load8_any(const bf16_t* p, float (&x)[8]) {
+  const u32x4 w = *reinterpret_cast<const u32x4_any*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8_any(const fp32_t* p, float (&x)[8]) {
+  const f32x4 a = *reinterpret_cast<const f32x4_any*>(p), b = *reinterpret_cast<const f32x4_any*>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = a[i];
+    x[4 + i] = b[i];
+  }
+}
+__device__ __forceinline__ void store8_any(bf16_t* p, const float (&x)[8]) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+  *reinterpret_cast<u32x4_any*>(p) = w;
+}
+__device__ __forceinline__ void store8_any(fp32_t* p, const float (&x)[8]) {
+  const f32x4 a = {x[0], x[1], x[2], x[3]}, b = {x[4], x[5], x[6], x[7]};
+  *reinterpret_cast<f32x4_any*>(p) = a;
+  *reinterpret_cast<f32x4_any*>(p + 4) = b;
+}
+
 // The same, rounded to nearest even for bf16.
 template <int VEC, bool STREAM = false>
 __device__ __forceinline__ void store(bf16_t* p, const float (&x)[VEC]) {
@@ -158,11 +188,13 @@ __device__ __forceinline__ float sum16(float x) {
   x += row_rotate<1>(x);
   return x;
 }
-__device__ __forceinline__ float sum64(float x) {
+__device__ __forceinline__ float sum32(float x) {
   x = sum16(x);
-  x += __shfl_xor(x, 16);
-  x += __shfl_xor(x, 32);
-  return x;
+  return x + __shfl_xor(x, 16);
+}
+__device__ __forceinline__ float sum64(float x) {
+  x = sum32(x);
+  return x + __shfl_xor(x, 32);
 }
 
 // Sum of the rows first, first + 16, ... below `rows` of one column of a

@@ -92,23 +92,33 @@ PrepareBwdLayout prepare_bwd_layout(int32_t T, int32_t H) {
   return L;
 }
 
-NormShape norm_shape(int32_t V, bool vector_rows) {
-  if (vector_rows) {
-    if (V <= 128) return {16, 8, 1};
-    if (V <= 512) return {64, 8, 1};
-    if (V <= 2048) return {256, 8, 1};
-    if (V <= 4096) return {256, 8, 2};
-    return {256, 8, 4};
-  }
-  if (V <= 256) return {64, 4, 1};
-  if (V <= 1024) return {256, 4, 1};
-  if (V <= 2048) return {256, 4, 2};
-  return {256, 4, 8};
+// A row's last vectors leave lanes idle, so a row takes the smallest group that
+// holds it; up to 1024 channels it stays inside a wave, where its sum needs no
+// barrier.  Forward, bf16 o and residual, 268 MB in rows of V: V = 128 72 us (64
+// lanes: 194), 256 70 (64 lanes: 110), 512 71 (256 lanes: 205), 1024 70 (256
+// lanes: 117), 2048 73 (64 lanes of four vectors: 106), 4096 72, 8192 74 (256
+// lanes of four vectors: 109).
+NormShape norm_shape(int32_t V) {
+  if (V <= 128) return {16, 1};
+  if (V <= 256) return {32, 1};
+  if (V <= 512) return {64, 1};
+  if (V <= 1024) return {64, 2};
+  if (V <= 2048) return {256, 1};
+  if (V <= 4096) return {256, 2};
+  return {512, 2};
 }
+// Backward: as many workgroups as the CUs hold at once, three a CU of 256
+// threads (164 registers with two vectors) and one of 512; each leaves partial
+// sums, and more of them wait.  65536 rows of 1024: 768 workgroups 114 us, 512
+// 142, 1024 154; 32768 x 32 heads of 128: 347, 1024 357; rows of 8192: 256
+// workgroups 161, 512 166.
+int32_t norm_bwd_blocks(const NormShape& s) { return s.lanes == 512 ? 256 : 768; }
+int32_t norm_threads(const NormShape& s) { return s.lanes > kRowThreads ? s.lanes : kRowThreads; }
 
-NormBwdLayout norm_bwd_layout(int32_t T, int32_t H, int32_t V, const NormShape& shape) {
+NormBwdLayout norm_bwd_layout(int32_t T, int32_t H, int32_t V) {
+  const NormShape shape = norm_shape(V);
   NormBwdLayout L;
-  L.grid = row_grid(T, H, kRowThreads / shape.lanes, kNormBwdBlocks);
+  L.grid = row_grid(T, H, norm_threads(shape) / shape.lanes, norm_bwd_blocks(shape));
   const size_t v = static_cast<size_t>(V) * sizeof(float);
   L.weight = 0;
   L.scale = up256(static_cast<size_t>(L.grid.blocks) * v);
@@ -116,15 +126,7 @@ NormBwdLayout norm_bwd_layout(int32_t T, int32_t H, int32_t V, const NormShape& 
   return L;
 }
 
-// For whichever of the shapes a call's strides lead to.
-size_t norm_bwd_workspace(int32_t T, int32_t H, int32_t V) {
-  const size_t scalar = norm_bwd_layout(T, H, V, norm_shape(V, false)).total;
-  if (V % 8 != 0) return scalar;
-  const size_t vector = norm_bwd_layout(T, H, V, norm_shape(V, true)).total;
-  return scalar > vector ? scalar : vector;
-}
-
-bool norm_vector_rows(const NormArgs& a) {
+bool norm_whole_rows(const NormArgs& a) {
   return a.V % 8 == 0 && (a.gate.ptr == nullptr || a.gate.stride * static_cast<int64_t>(size_of(a.dtype)) % 16 == 0);
 }
 
@@ -207,7 +209,7 @@ int check_norm(const NormArgs& a, bool backward) {
                       {a.d_weight.ptr, a.d_weight.bytes, V * 4, !backward},
                       {a.d_res_scale.ptr, a.d_res_scale.bytes, row * 4, true}});
   if (st != KDA_OK) return st;
-  return backward ? check_workspace(a.workspace, norm_bwd_workspace(a.T, a.H, a.V)) : KDA_OK;
+  return backward ? check_workspace(a.workspace, norm_bwd_layout(a.T, a.H, a.V).total) : KDA_OK;
 }
 
 int check_scan(const ScanArgs& a, bool backward) {

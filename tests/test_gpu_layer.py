@@ -90,7 +90,8 @@ def test_prepare_inputs_backward(T, H, dtype, bias, strided):
 
 NORM_SHAPES = [(1, 1, 128), (37, 5, 128), (9, 3, 40), (5, 2, 1), (4, 3, 7), (3, 1, 512), (3, 2, 513), (2, 1, 1000),
                (3, 1, 2048), (2, 1, 2049), (2, 1, 2056), (2, 1, 4104), (2, 1, 8192), (1, 1, 8191), (1300, 17, 128),
-               (700, 1, 264)]
+               (700, 1, 264), (5, 3, 129), (4, 1, 200), (900, 1, 256), (3, 1, 1024), (2, 1, 1025), (2, 1, 4096), (2, 1, 4097),
+               (1100, 1, 777), (2, 2, 9)]
 
 
 def _norm_case(T, H, V, o_dtype, dtype, kind, scaled, strided, seed):
