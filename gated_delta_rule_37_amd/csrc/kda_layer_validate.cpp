@@ -107,12 +107,15 @@ NormShape norm_shape(int32_t V) {
   if (V <= 4096) return {256, 2};
   return {512, 2};
 }
-// Backward: as many workgroups as the CUs hold at once, three a CU of 256
-// threads (164 registers with two vectors) and one of 512; each leaves partial
-// sums, and more of them wait.  65536 rows of 1024: 768 workgroups 114 us, 512
-// 142, 1024 154; 32768 x 32 heads of 128: 347, 1024 357; rows of 8192: 256
-// workgroups 161, 512 166.
-int32_t norm_bwd_blocks(const NormShape& s) { return s.lanes == 512 ? 256 : 768; }
+// Backward: each workgroup leaves partial sums, so only as many as run at once.
+// Two vectors (156-174 registers): three workgroups a CU of 256 threads and one
+// of 512.  65536 rows of 1024: 768 workgroups 114 us, 512 142, 1024 154; rows of
+// 8192: 256 workgroups 161, 512 166.  One vector (85-92 registers): four a CU
+// for the sake of most shapes, bf16 rows of 128, 256, 512 and 2048: 1024
+// workgroups 111, 110, 111 and 113 us, 768 114, 114, 114 and 121; 1024 x 4 heads
+// 17.4 against 18.5.  FP32 o in many heads is better with 768: 32768 x 32 346
+// against 356, 8191 x 16 49.2 against 50.1.
+int32_t norm_bwd_blocks(const NormShape& s) { return s.vectors == 1 ? 1024 : s.lanes == 512 ? 256 : 768; }
 int32_t norm_threads(const NormShape& s) { return s.lanes > kRowThreads ? s.lanes : kRowThreads; }
 
 NormBwdLayout norm_bwd_layout(int32_t T, int32_t H, int32_t V) {
