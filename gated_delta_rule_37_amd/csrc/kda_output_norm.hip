@@ -218,17 +218,18 @@ __global__ __launch_bounds__(kThreads<LANES>) void norm_backward_kernel(NormPara
     store_row(sh, static_cast<G*>(p.d_o) + row, o);
     if (p.gate != nullptr) store_row(sh, static_cast<E*>(p.d_gate) + row, z);
   }
-  // ds: this group's sum of m; dw: the workgroup's sum of s m
+  // ds: this group's sum of m; dw: the workgroup's sum of s m, of an idle group
+  // zeros whatever s is
   if (active && p.res_scale != nullptr) store_row(sh, p.scale_part + (token * p.H + head) * p.V, m);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m[j][i] *= s[j][i];
+    for (int i = 0; i < 8; ++i) m[j][i] = active ? m[j][i] * s[j][i] : 0.f;
   }
   if constexpr (kGroups == 1) {
     store_row(sh, p.weight_part + static_cast<int64_t>(blockIdx.x) * p.V, m);
   } else {
-    store_row(sh, &part[group][0], m);   // zeros from an idle group
+    store_row(sh, &part[group][0], m);
     __syncthreads();
     for (int32_t v = threadIdx.x; v < p.V; v += kThreads<LANES>) {
       float sum = 0.f;

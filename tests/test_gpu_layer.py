@@ -151,6 +151,22 @@ def test_output_norm_backward(T, H, V, o_dtype, dtype, kind, scaled, strided):
                 lr.assert_close(t, want[n], bounds[n], n)
 
 
+@pytest.mark.parametrize("V", [8, 128, 250, 512, 1000, 2048, 4104])
+def test_output_norm_backward_infinite_scale(V):
+    """An infinite residual scale reaches its own channel's sums alone, and as
+    the formula has it: lanes without a row add nothing, not 0 inf."""
+    T, H = 5, 3
+    o, dy = _randn(T, H, V, seed=1).abs() + 0.5, _randn(T, H, V, seed=2).abs() + 0.5
+    weight, s = torch.ones(V), torch.ones(H, V)
+    s[0, 3] = float("inf")
+    got = layer.output_norm_backward(_d(dy), _d(o), _d(weight), res_scale=_d(s), activation="none")
+    d_weight, d_scale = got["d_weight"].cpu(), got["d_res_scale"].cpu()
+    others = torch.arange(V) != 3
+    assert d_weight[3] == float("inf")
+    assert d_weight[others].isfinite().all() and d_scale.isfinite().all()
+    assert got["d_o"].cpu()[:, 1:].isfinite().all()
+
+
 # ------------------------------------------------------------- per-channel scan
 
 # cu_seqlens, segments, channels, dtype, h's dtype, tied, initial states, strided
