@@ -98,7 +98,8 @@ struct NormBwdLayout {
   RowGrid grid;
   size_t weight, scale, total;   // byte offsets: [blocks][V] and [P][H][V] FP32
 };
-NormBwdLayout norm_bwd_layout(int32_t T, int32_t H, int32_t V);
+NormBwdLayout norm_bwd_layout(int32_t T, int32_t H, int32_t V, int32_t o_format);
+size_t norm_bwd_workspace(int32_t T, int32_t H, int32_t V);
 bool norm_whole_rows(const NormArgs& a);   // rows of whole, aligned 16-byte vectors
 
 // The scan's tiles: kScanTile tokens of kScanChannels channels, one workgroup

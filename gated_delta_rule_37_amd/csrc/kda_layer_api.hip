@@ -143,7 +143,7 @@ int kda_output_norm_backward(int32_t T, int32_t H, int32_t V, const void* dy, si
 
 size_t kda_output_norm_backward_workspace_bytes(int32_t T, int32_t H, int32_t V) {
   if (T <= 0 || H <= 0 || H > 65535 || V <= 0 || V > 8192 || static_cast<int64_t>(H) * V > (1 << 24)) return 0;
-  return kda::norm_bwd_layout(T, H, V).total;
+  return kda::norm_bwd_workspace(T, H, V);
 }
 
 int kda_scan_forward(const kda_plan* plan, const int32_t* plan_dev, size_t plan_dev_bytes, int32_t D, int32_t dtype,

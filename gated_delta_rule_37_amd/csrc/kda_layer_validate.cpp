@@ -107,27 +107,33 @@ NormShape norm_shape(int32_t V) {
   if (V <= 4096) return {256, 2};
   return {512, 2};
 }
-// Backward: each workgroup leaves partial sums, so only as many as run at once.
-// Two vectors (156-174 registers): three workgroups a CU of 256 threads and one
-// of 512.  65536 rows of 1024: 768 workgroups 114 us, 512 142, 1024 154; rows of
-// 8192: 256 workgroups 161, 512 166.  One vector (85-92 registers): four a CU
-// for the sake of most shapes, bf16 rows of 128, 256, 512 and 2048: 1024
-// workgroups 111, 110, 111 and 113 us, 768 114, 114, 114 and 121; 1024 x 4 heads
-// 17.4 against 18.5.  FP32 o in many heads is better with 768: 32768 x 32 346
-// against 356, 8191 x 16 49.2 against 50.1.
-int32_t norm_bwd_blocks(const NormShape& s) { return s.vectors == 1 ? 1024 : s.lanes == 512 ? 256 : 768; }
+// Backward: each workgroup leaves partial sums, so only as many as run at once
+// and have enough in flight.  Two vectors a lane (156-174 registers): three
+// workgroups a CU of 256 threads and one of 512; with 65536 rows of 1024 bf16
+// channels 768 workgroups 114 us, 512 142, 1024 154, with rows of 8192 256
+// workgroups 161, 512 166.  One vector (85-92 registers): four of bf16 o (2^26
+// channels in rows of 128, 256, 512 and 2048: 1024 workgroups 111, 110, 111 and
+// 113 us, 768 114, 114, 114 and 121), three of fp32 o, whose loads are twice as
+// many (with a gate: 768 workgroups 176, 177, 176 and 183 us, 1024 180, 180, 180
+// and 183, 512 187 to 198).
+int32_t norm_bwd_blocks(const NormShape& s, int32_t o_format) {
+  if (s.vectors == 1 && o_format == KDA_BF16) return 1024;
+  return s.lanes == 512 ? 256 : 768;
+}
 int32_t norm_threads(const NormShape& s) { return s.lanes > kRowThreads ? s.lanes : kRowThreads; }
 
-NormBwdLayout norm_bwd_layout(int32_t T, int32_t H, int32_t V) {
+NormBwdLayout norm_bwd_layout(int32_t T, int32_t H, int32_t V, int32_t o_format) {
   const NormShape shape = norm_shape(V);
   NormBwdLayout L;
-  L.grid = row_grid(T, H, norm_threads(shape) / shape.lanes, norm_bwd_blocks(shape));
+  L.grid = row_grid(T, H, norm_threads(shape) / shape.lanes, norm_bwd_blocks(shape, o_format));
   const size_t v = static_cast<size_t>(V) * sizeof(float);
   L.weight = 0;
   L.scale = up256(static_cast<size_t>(L.grid.blocks) * v);
   L.total = L.scale + up256(static_cast<size_t>(L.grid.lanes) * static_cast<size_t>(H) * v);
   return L;
 }
+// Of either format of o: bf16 has the more workgroups.
+size_t norm_bwd_workspace(int32_t T, int32_t H, int32_t V) { return norm_bwd_layout(T, H, V, KDA_BF16).total; }
 
 bool norm_whole_rows(const NormArgs& a) {
   return a.V % 8 == 0 && (a.gate.ptr == nullptr || a.gate.stride * static_cast<int64_t>(size_of(a.dtype)) % 16 == 0);
@@ -212,7 +218,7 @@ int check_norm(const NormArgs& a, bool backward) {
                       {a.d_weight.ptr, a.d_weight.bytes, V * 4, !backward},
                       {a.d_res_scale.ptr, a.d_res_scale.bytes, row * 4, true}});
   if (st != KDA_OK) return st;
-  return backward ? check_workspace(a.workspace, norm_bwd_layout(a.T, a.H, a.V).total) : KDA_OK;
+  return backward ? check_workspace(a.workspace, norm_bwd_workspace(a.T, a.H, a.V)) : KDA_OK;
 }
 
 int check_scan(const ScanArgs& a, bool backward) {

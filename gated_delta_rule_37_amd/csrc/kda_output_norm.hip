@@ -350,7 +350,7 @@ int launch_norm(const NormArgs& a, hipStream_t stream) {
 int launch_norm_backward(const NormArgs& a, hipStream_t stream) {
   const NormShape shape = norm_shape(a.V);
   const bool whole = norm_whole_rows(a);
-  const NormBwdLayout L = norm_bwd_layout(a.T, a.H, a.V);
+  const NormBwdLayout L = norm_bwd_layout(a.T, a.H, a.V, a.o_format);
   NormParams p = params_of(a, L.grid);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace.ptr);
   p.weight_part = reinterpret_cast<float*>(ws + L.weight);

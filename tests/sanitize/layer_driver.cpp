@@ -59,7 +59,7 @@ int norm(bool backward, int32_t T, int32_t H, int32_t V, int32_t dtype, int32_t 
   } else {
     a.dy = rows(n * e);
     a.d_o = dst(n * 4), a.d_gate = dst(n * e), a.d_weight = dst(size_t(V) * 4), a.d_res_scale = dst(row * 4);
-    a.workspace = dst(kda::norm_bwd_layout(T, H, V).total);
+    a.workspace = dst(kda::norm_bwd_workspace(T, H, V));
   }
   return kda::check_norm(a, backward);
 }
