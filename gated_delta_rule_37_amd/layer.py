@@ -185,7 +185,8 @@ def prepare_inputs_backward(q_raw, k_raw, gate_raw, beta_raw, a_log, dt_bias, dq
     out["ddt_bias"] = None if dt_bias is None else _empty(stream, dev, f32, H, K)
     for n in ("dq_raw", "dk_raw", "dgate_raw", "dbeta_raw", "da_log", "ddt_bias"):
         args += _made(out[n])
-    args += _scratch(kda.lib().kda_prepare_inputs_backward_workspace_bytes(T, H, K), dev, stream)
+    workspace = _scratch(kda.lib().kda_prepare_inputs_backward_workspace_bytes(T, H, K), dev, stream)
+    args += _made(workspace)
     _call("kda_prepare_inputs_backward", dev, args, stream)
     return out
 
@@ -200,8 +201,10 @@ def _empty(stream, device, dtype, *shape):
 
 
 def _scratch(size, device, stream):
-    """A workspace of ``size`` bytes for one call."""
-    return _NULL if size == 0 else (_empty(stream, device, torch.uint8, size).data_ptr(), size)
+    """A workspace of ``size`` bytes for one call, or None.  The caller keeps it
+    until the C call has returned: only what is enqueued is in stream order, and
+    another thread may allocate on the same stream while the call runs."""
+    return None if size == 0 else _empty(stream, device, torch.uint8, size)
 
 
 def _norm(o, weight, gate, activation, res_scale, dtype):
@@ -259,11 +262,11 @@ def output_norm_backward(dy, o, weight, gate=None, activation="sigmoid", res_sca
                d_gate=None if gate is None else _empty(stream, dev, dtype, T, H, V),
                d_weight=_empty(stream, dev, f32, V),
                d_res_scale=None if res_scale is None else _empty(stream, dev, f32, H, V))
+    workspace = _scratch(kda.lib().kda_output_norm_backward_workspace_bytes(T, H, V), dev, stream)
     args = [T, H, V, *_buf(dy, dtype, (T, H, V), "dy", dev), *_buf(o, o.dtype, (T, H, V), "o", dev), _dtype(o, "o"),
             *gated, *weights, _dtype(dy, "dy"), float(eps), *_made(out["d_o"]),
             DTYPES[d_o_dtype], *_made(out["d_gate"]),
-            *_made(out["d_weight"]), *_made(out["d_res_scale"]),
-            *_scratch(kda.lib().kda_output_norm_backward_workspace_bytes(T, H, V), dev, stream)]
+            *_made(out["d_weight"]), *_made(out["d_res_scale"]), *_made(workspace)]
     _call("kda_output_norm_backward", dev, args, stream)
     return out
 
@@ -296,9 +299,10 @@ def scan_forward(plan: kda.Plan, x, g, initial_state=None, tied=False, h_dtype=N
         out = dict(h=_empty(stream, dev, g.dtype if h_dtype is None else h_dtype, T, D),
                    final_state=_empty(stream, dev, torch.float32, plan.N, D))
     h = out["h"]
+    workspace = _scratch(kda.lib().kda_scan_workspace_bytes(plan.handle, D), dev, stream)
     args += [*_buf(h, h.dtype, (T, D), "h", dev), _dtype(h, "h"),
              *_buf(out["final_state"], torch.float32, (plan.N, D), "final_state", dev),
-             *_scratch(kda.lib().kda_scan_workspace_bytes(plan.handle, D), dev, stream)]
+             *_made(workspace)]
     _call("kda_scan_forward", dev, args, stream)
     return out
 
@@ -314,10 +318,10 @@ def scan_backward(plan: kda.Plan, x, g, h, dh, d_final=None, initial_state=None,
     want = initial_state is not None if want_dh0 is None else want_dh0
     out = dict(dx=_empty(stream, dev, g.dtype, T, D), dg=_empty(stream, dev, g.dtype, T, D),
                dh0=_empty(stream, dev, f32, plan.N, D) if want else None)
+    workspace = _scratch(kda.lib().kda_scan_workspace_bytes(plan.handle, D), dev, stream)
     args += [*_buf(h, h.dtype, (T, D), "h", dev), *_buf(dh, h.dtype, (T, D), "dh", dev), _dtype(h, "h"),
              *_buf(d_final, f32, (plan.N, D), "d_final", dev), *_made(out["dx"]),
-             *_made(out["dg"]), *_made(out["dh0"]),
-             *_scratch(kda.lib().kda_scan_workspace_bytes(plan.handle, D), dev, stream)]
+             *_made(out["dg"]), *_made(out["dh0"]), *_made(workspace)]
     _call("kda_scan_backward", dev, args, stream)
     return out
 
