@@ -115,6 +115,10 @@ struct ScanLayout {
   size_t tickets, maps, states, total;
 };
 ScanLayout scan_layout(int32_t T, int32_t D);
+// Whether a ticket names one of a channel block's tiles.  The words of a
+// workspace that another call overwrites can hold anything, and a ticket is
+// turned into addresses: one with the top bit set must not pass as negative.
+constexpr bool is_tile(uint32_t ticket, int32_t tiles) { return ticket < static_cast<uint32_t>(tiles); }
 
 int check_prepare(const PrepareArgs& a, bool backward);
 int check_norm(const NormArgs& a, bool backward);

@@ -87,13 +87,13 @@ __device__ __forceinline__ int32_t column_of(const ScanParams& p) {
 // The next tile of this workgroup's channel block.  Tickets are handed out in
 // the order of the tiles, so every tile before this one belongs to a workgroup
 // that already runs, and the oldest of them waits for nothing: all waits end.
-__device__ __forceinline__ int32_t take_ticket(const ScanParams& p, int32_t column, uint32_t* box) {
-  if (p.tiles == 1) return 0;
+__device__ __forceinline__ uint32_t take_ticket(const ScanParams& p, int32_t column, uint32_t* box) {
+  if (p.tiles == 1) return 0u;
   if (threadIdx.x == 0) {
     *box = __hip_atomic_fetch_add(p.tickets + column * 32, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
   }
   __syncthreads();
-  return __builtin_amdgcn_readfirstlane(static_cast<int32_t>(*box));
+  return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int32_t>(*box)));
 }
 
 __device__ __forceinline__ int64_t word_of(const ScanParams& p, int32_t tile, int32_t column) {
@@ -105,7 +105,8 @@ __device__ __forceinline__ int64_t word_of(const ScanParams& p, int32_t tile, in
 // them has its state and those after it their maps, then applies those maps in
 // order: exactly what each of these tiles does itself, so the result does not
 // depend on which states were there.  Polls are bounded, so that a workspace
-// that another call overwrites gives NaN instead of a hang.
+// that another call overwrites gives wrong values, NaN or rows that stay
+// unwritten (a ticket given twice or passed over), but no hang.
 constexpr int kMaxPolls = 1 << 20;   // seconds; a wait takes microseconds
 template <int LOOK>
 __device__ __forceinline__ float look_back(const ScanParams& p, int32_t tile, int32_t column) {
@@ -321,8 +322,9 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(ScanParams p) {
   constexpr int VEC = G::VEC, R = G::R;
   __shared__ __align__(16) TileLds<G> lds;
   const int32_t column = column_of(p);
-  const int32_t tile = take_ticket(p, column, &lds.ticket);
-  if (tile >= p.tiles) return;
+  const uint32_t ticket = take_ticket(p, column, &lds.ticket);
+  if (!is_tile(ticket, p.tiles)) return;
+  const int32_t tile = static_cast<int32_t>(ticket);
   const int32_t row = threadIdx.x / G::LPR * R;                                // first token in the tile
   const int32_t d = column * kScanChannels + (threadIdx.x % G::LPR) * VEC;
   const bool owner = d < p.D;
@@ -391,8 +393,9 @@ __global__ __launch_bounds__(kScanThreads) void scan_backward_kernel(ScanParams 
   constexpr int VEC = G::VEC, R = G::R;
   __shared__ __align__(16) TileLds<G> lds;
   const int32_t column = column_of(p);
-  const int32_t tile = take_ticket(p, column, &lds.ticket);
-  if (tile >= p.tiles) return;
+  const uint32_t ticket = take_ticket(p, column, &lds.ticket);
+  if (!is_tile(ticket, p.tiles)) return;
+  const int32_t tile = static_cast<int32_t>(ticket);
   const int32_t row = threadIdx.x / G::LPR * R;
   const int32_t d = column * kScanChannels + (threadIdx.x % G::LPR) * VEC;
   const bool owner = d < p.D;

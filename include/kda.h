@@ -574,7 +574,7 @@ size_t kda_output_norm_backward_workspace_bytes(int32_t T, int32_t H, int32_t V)
  * Workspace: kda_scan_workspace_bytes(plan, D) bytes, NULL where that is 0 (at
  * most 128 tokens).  Its contents are not needed afterwards.  Two calls that
  * may run at the same time need a workspace each: sharing one gives undefined
- * results (wrong values or NaN).
+ * results (wrong values, NaN or rows that stay unwritten).
  */
 int kda_scan_forward(const kda_plan* plan, const int32_t* plan_dev, size_t plan_dev_bytes, int32_t D, int32_t dtype,
                      const void* x, size_t x_bytes, int64_t x_stride, const void* g, size_t g_bytes, int64_t g_stride,
