@@ -65,6 +65,9 @@ static_assert(kScanTile < kScanThreads, "a thread for each token boundary of a t
 // The map (A, B) of h; a constant map (A = 0, as a sequence's start gives) is B
 // whatever h is, so that an infinity or NaN stays in its own sequence.
 __device__ __forceinline__ float apply(float A, float B, float h) { return A == 0.f ? B : __fmaf_rn(A, h, B); }
+// The decay of a run that ends with one of decay a: 0 from a constant map on,
+// where the product would keep a NaN or infinity of the sequence before.
+__device__ __forceinline__ float decay_after(float A, float a) { return a == 0.f ? 0.f : A * a; }
 
 // ------------------------------------------------ the tiles' maps and states
 // Words that other workgroups wait for carry their own readiness: all ones
@@ -209,7 +212,7 @@ __device__ __forceinline__ void tile_states(const ScanParams& p, int32_t tile, i
       for (int i = 0; i < kGroups; ++i) {
         const float ga = lds.map[i][0][lane];
         b = apply(ga, lds.map[i][1][lane], b);
-        a *= ga;
+        a = decay_after(a, ga);
       }
       const int64_t w = word_of(p, tile, column) + lane;
       if (tile > 0) {
@@ -311,7 +314,7 @@ __device__ __forceinline__ void step_map(int r, int32_t mark, bool valid, const 
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
     B[i] = r == 0 ? b[i] : PLAIN ? a[i] * B[i] + b[i] : apply(a[i], b[i], B[i]);
-    A[i] = r == 0 ? a[i] : A[i] * a[i];
+    A[i] = r == 0 ? a[i] : PLAIN ? A[i] * a[i] : decay_after(A[i], a[i]);
     // row by row: composing all rows at the end would keep their maps in registers
     if (!PLAIN) asm volatile("" : "+v"(A[i]), "+v"(B[i]));
   }

@@ -1,0 +1,84 @@
+"""The operators around the recurrence at the edges of their domains, on the
+GPU: gates that are not finite, rows of large values, saturated gates, and the
+precision of their exponentials.  Each bound counts units of EPS = 2^-24, half
+a step of FP32: an exponential is off by at most 4 (the hardware's 2^x is within
+2, its correction adds a rounding), a reciprocal by 2, a product or sum by 1."""
+import pytest
+import torch
+
+from gated_delta_rule_37_amd import kda, layer
+import layer_reference as lr
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _randn(*shape, seed, dtype=F32, scale=1.0):
+    return (torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * scale).to(dtype)
+
+
+def _uniform(lo, hi, *shape, seed):
+    return lo + (hi - lo) * torch.rand(*shape, generator=torch.Generator().manual_seed(seed))
+
+
+def _d(t):
+    return None if t is None else t.to(DEV)
+
+
+# ------------------------------------------------------------- gates that are not finite
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("D,dtype", [(72, F32), (13, BF), (2, F32), (1600, BF)])
+def test_scan_keeps_sequences_apart_from_bad_gates(D, dtype, bad):
+    """A gate that is not a number stays in its own sequence in both directions,
+    at a sequence's first token, inside it and at its last; the others give the
+    same bits as without it."""
+    cu, T, N = [0, 100, 101, 400, 900, 905, 1300], 1300, 6
+    x, dh = (_d(_randn(T, D, seed=s, dtype=dtype)) for s in (1, 2))
+    g = _d((-0.01 * _randn(T, D, seed=3).abs()).to(dtype))
+    h0, d_final = _d(_randn(N, D, seed=4)), _d(_randn(N, D, seed=5))
+    plan = kda.Plan(cu, 1)
+
+    def both(gates, h):
+        f = layer.scan_forward(plan, x, gates, initial_state=h0, tied=True)
+        b = layer.scan_backward(plan, x, gates, h if h is not None else f["h"], dh, d_final=d_final,
+                                initial_state=h0, tied=True)
+        return f, b
+
+    f, b = both(g, None)
+    for places in ((cu[1], cu[3]), (cu[3] + 250,), (cu[2] - 1, cu[4] - 1)):
+        g2 = g.clone()
+        g2[list(places)] = bad
+        hit = {n for n in range(N) for t in places if cu[n] <= t < cu[n + 1]}
+        f2, b2 = both(g2, f["h"])
+        for n in sorted(set(range(N)) - hit):
+            rows = slice(cu[n], cu[n + 1])
+            assert torch.equal(f2["h"][rows], f["h"][rows]), (places, n)
+            assert torch.equal(f2["final_state"][n], f["final_state"][n]), (places, n)
+            assert all(torch.equal(b2[k][rows], b[k][rows]) for k in ("dx", "dg")), (places, n)
+            assert torch.equal(b2["dh0"][n], b["dh0"][n]), (places, n)
+        if bad != bad:
+            assert all(f2["final_state"][n].isnan().all() and b2["dh0"][n].isnan().all() for n in hit)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_inputs_stay_as_they_were(dtype):
+    """The scan's backward, called twice on one set of inputs, writes into none
+    of them and gives the same bits; h, dh in FP32, as the recurrence keeps them."""
+    cu, T, D, N = [0, 40, 300], 300, 70, 2
+    x, g = _d(_randn(T, D, seed=1, dtype=dtype)), _d((-_randn(T, D, seed=2).abs()).to(dtype))
+    h0, d_final, dh = _d(_randn(N, D, seed=3)), _d(_randn(N, D, seed=4)), _d(_randn(T, D, seed=5))
+    plan = kda.Plan(cu, 1)
+    h = layer.scan_forward(plan, x, g, initial_state=h0, h_dtype=F32)["h"]
+    ins = [x, g, h, dh, d_final, h0]
+    kept = [t.clone() for t in ins]
+    runs = [layer.scan_backward(plan, x, g, h, dh, d_final=d_final, initial_state=h0) for _ in range(2)]
+    assert all(torch.equal(a, b) for a, b in zip(ins, kept))
+    assert all(torch.equal(runs[0][n], runs[1][n]) for n in runs[0])
+    args = (x.cpu().double(), g.cpu().double(), h.cpu().double(), cu, h0.cpu().double(), False, dh.cpu().double(),
+            d_final.cpu().double())
+    want, bounds = lr.scan_backward(*args), lr.scan_backward_bounds(*args)
+    for n, t in runs[1].items():
+        lr.assert_close(t, want[n], bounds[n], n)
