@@ -149,9 +149,9 @@ __global__ __launch_bounds__(kThreads<LANES>) void norm_kernel(NormParams p) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += o[j][i] * o[j][i];
+      for (int i = 0; i < 8; ++i) sum += (o[j][i] * inv) * o[j][i];   // the sum without 1 / V could overflow
     }
-    const float r = rsqrtf(group_sum<LANES>(sum, scratch) * inv + p.eps);
+    const float r = rsqrtf(group_sum<LANES>(sum, scratch) + p.eps);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
@@ -199,12 +199,13 @@ __global__ __launch_bounds__(kThreads<LANES>) void norm_backward_kernel(NormPara
         if (p.activation != KDA_ACT_NONE) act_and_slope(p.activation, z[j][i], a, slope);
         z[j][i] = dy[j][i] * s[j][i] * w[j][i] * slope;   // d_z / n
         dy[j][i] *= a;                                    // dy act(z)
-        sum += o[j][i] * o[j][i];
-        dot += dy[j][i] * s[j][i] * w[j][i] * o[j][i];    // sum of dn o
+        const float share = o[j][i] * inv;                // as in the forward
+        sum += share * o[j][i];
+        dot += dy[j][i] * s[j][i] * w[j][i] * share;      // mean of dn o
       }
     }
-    const float r = rsqrtf(group_sum<LANES>(sum, scratch) * inv + p.eps);
-    const float c = group_sum<LANES>(dot, scratch) * r * inv;   // mean(dn n)
+    const float r = rsqrtf(group_sum<LANES>(sum, scratch) + p.eps);
+    const float c = group_sum<LANES>(dot, scratch) * r;   // mean(dn n)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll

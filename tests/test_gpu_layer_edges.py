@@ -82,3 +82,27 @@ def test_inputs_stay_as_they_were(dtype):
     want, bounds = lr.scan_backward(*args), lr.scan_backward_bounds(*args)
     for n, t in runs[1].items():
         lr.assert_close(t, want[n], bounds[n], n)
+
+
+# ------------------------------------------------------------- large values
+
+
+@pytest.mark.parametrize("V", [128, 520, 1000, 2048, 8191, 8192])
+@pytest.mark.parametrize("o_dtype", [F32, BF])
+def test_output_norm_of_large_values(V, o_dtype):
+    """Rows whose mean of squares is finite in FP32 (about 2.5e37) and whose sum
+    of squares is not."""
+    T, H = 3, 2
+    x = dict(o=_randn(T, H, V, seed=V, dtype=o_dtype, scale=5e18), weight=1 + 0.5 * _randn(V, seed=1),
+             gate=_randn(T, H, V, seed=2), res_scale=_randn(H, V, seed=3))
+    residual, dy = _randn(T, H, V, seed=4), _randn(T, H, V, seed=5)
+    dev, w = {n: _d(t) for n, t in x.items()}, {n: t.double() for n, t in x.items()}
+    assert (w["o"] ** 2).mean(-1).max() < torch.finfo(F32).max
+    got = layer.output_norm(**dev, activation="silu", residual=_d(residual))
+    args = dict(**w, kind="silu", eps=1e-6)
+    lr.assert_close(got, lr.output_norm(**args, residual=residual.double()),
+                    lr.output_norm_bound(**args, residual=residual.double()), "y")
+    grads = layer.output_norm_backward(_d(dy), **dev, activation="silu")
+    want, bounds = lr.output_norm_backward(dy.double(), **args), lr.output_norm_backward_bounds(dy.double(), **args)
+    for n, t in grads.items():
+        lr.assert_close(t, want[n], bounds[n], n)
