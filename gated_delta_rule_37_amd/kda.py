@@ -26,6 +26,7 @@ library can refuse an undersized buffer before it launches anything.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -202,18 +203,30 @@ class Plan:
             self.bounds = self.blob[4:4 + self.S + 1].copy()
             self.segment_live = self.blob[4 + self.S + 1 + 3 * self.S:4 + self.S + 1 + 4 * self.S].copy()
         self._dev = {}
+        self._readers = {}    # device -> the streams that its copy is recorded on
 
     @property
     def handle(self):
         return self._h
 
-    def device_blob(self, device) -> torch.Tensor:
-        """The caller-owned device copy of the blob (cached per device)."""
+    def device_blob(self, device, stream=None) -> torch.Tensor:
+        """The caller-owned device copy of the blob (cached per device), for work
+        on ``stream`` (default: the device's current stream).  When the plan is
+        dropped, its memory waits for the work enqueued until then on every
+        stream that it was asked for.  The first call for a device copies from
+        the host, so it has to come before a capture, and a captured graph needs
+        the plan for as long as it is replayed."""
         device = torch.device(device)
         t = self._dev.get(device)
         if t is None:
             t = torch.from_numpy(self.blob.copy()).to(device)
             self._dev[device] = t
+        if device.type == "cuda":
+            raw = _raw_stream(device) if stream is None else stream.cuda_stream
+            seen = self._readers.setdefault(device, set())
+            if raw not in seen:
+                t.record_stream(torch.cuda.current_stream(device) if stream is None else stream)
+                seen.add(raw)
         return t
 
     def summary_bytes(self, H: int, K: int = 128, V: int = 128) -> int:
@@ -234,6 +247,12 @@ class Plan:
             pass
 
 
+def _raw_stream(device) -> int:
+    """The handle of the device's current stream."""
+    index = torch.cuda.current_device() if device.index is None else device.index
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _buf(t: torch.Tensor, dtype, shape, name: str):
     """(address, size in bytes) of a device tensor, after checking its dtype,
     shape and layout; None stands for an absent optional tensor."""
@@ -248,6 +267,12 @@ def _buf(t: torch.Tensor, dtype, shape, name: str):
     if t.device.type != "cuda":
         raise ValueError(f"{name}: must be a device tensor")
     return (t.data_ptr(), t.numel() * t.element_size())
+
+
+def _allocating_on(stream):
+    """A context in which what torch allocates belongs to ``stream`` (None: to the
+    current one): once it is free, only later work of that stream is given it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _stream(t: torch.Tensor, stream):
@@ -390,10 +415,14 @@ def backward(plan: Plan, q, k, v, g, beta, d_o, d_final=None, initial_state=None
     V = v.shape[2]
     dev = q.device
     f32 = dict(dtype=torch.float32, device=dev)
+    ws_bytes = int(lib().kda_backward_workspace_bytes(plan.handle, H, K, V))
     make = (lambda *shape: torch.empty(*shape, **f32)) if sentinel is None else (
         lambda *shape: torch.full(shape, float(sentinel), **f32))
-    out = dict(dq=make(T, H, K), dk=make(T, H, K), dv=make(T, H, V), dg=make(T, H, K), dbeta=make(T, H),
-               dh0=make(plan.N, H, K, V) if want_dh0 else None)
+    with _allocating_on(stream):
+        out = dict(dq=make(T, H, K), dk=make(T, H, K), dv=make(T, H, V), dg=make(T, H, K), dbeta=make(T, H),
+                   dh0=make(plan.N, H, K, V) if want_dh0 else None)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    blob = plan.device_blob(dev, stream)
     ins = _flat([
         _buf(q, torch.bfloat16, (T, H, K), "q"), _buf(k, torch.bfloat16, (T, H, K), "k"),
         _buf(v, torch.bfloat16, (T, H, V), "v"), _buf(g, torch.bfloat16, (T, H, K), "g"),
@@ -407,17 +436,15 @@ def backward(plan: Plan, q, k, v, g, beta, d_o, d_final=None, initial_state=None
         _buf(out["dv"], torch.float32, None, "dv"), _buf(out["dg"], torch.float32, None, "dg"),
         _buf(out["dbeta"], torch.float32, None, "dbeta"), _buf(out["dh0"], torch.float32, None, "dh0"),
     ])
-    ws_bytes = int(lib().kda_backward_workspace_bytes(plan.handle, H, K, V))
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     if saved is None:
-        st = lib().kda_backward(plan.handle, *_plan_dev(plan, plan.device_blob(dev)), *ins, H, K, V,
+        st = lib().kda_backward(plan.handle, *_plan_dev(plan, blob), *ins, H, K, V,
                                 *_heads(H, heads), *grads, *_buf(ws, torch.uint8, None, "workspace"),
                                 _stream(q, stream))
         _check(st, "kda_backward")
         return out
     kept = _flat([_buf(saved[0], torch.float32, (plan.S, H, K, V), "transitions"),
                   _buf(saved[1], torch.float32, (plan.S, H, K, V), "carry_in")])
-    st = lib().kda_backward_from_forward(plan.handle, *_plan_dev(plan, plan.device_blob(dev)), *ins, H, K, V,
+    st = lib().kda_backward_from_forward(plan.handle, *_plan_dev(plan, blob), *ins, H, K, V,
                                          *_heads(H, heads), *kept, *grads,
                                          *_buf(ws, torch.uint8, None, "workspace"), _stream(q, stream))
     _check(st, "kda_backward_from_forward")
@@ -509,8 +536,9 @@ def forward(plan: Plan, q, k, v, g, beta, out=None, stream=None, groups=1, event
     T, H, K = q.shape
     V = v.shape[2]
     if out is None:
-        out = alloc_outputs(plan, H, K, V, q.device, o_dtype)
-    pd = plan.device_blob(q.device)
+        with _allocating_on(stream):
+            out = alloc_outputs(plan, H, K, V, q.device, o_dtype)
+    pd = plan.device_blob(q.device, stream)
     main = torch.cuda.current_stream(q.device) if stream is None else stream
     runs = head_groups(H, groups)
 

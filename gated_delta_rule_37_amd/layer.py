@@ -35,8 +35,10 @@ final_state::
     y = layer.output_norm(o, weight, gate=z, activation="sigmoid")
 
 Every call enqueues on ``stream`` (default: the current stream of its tensors'
-device) and returns without waiting; what it allocates belongs to that stream.  A tensor on another device than the rest
-raises ValueError.
+device) and returns without waiting; what it allocates belongs to that stream,
+and a plan's device copy waits for it (``Plan.device_blob``, which a capture of
+a scan needs called before).  A tensor on another device than the rest raises
+ValueError.
 """
 from __future__ import annotations
 
@@ -192,11 +194,10 @@ def prepare_inputs_backward(q_raw, k_raw, gate_raw, beta_raw, a_log, dt_bias, dq
 
 
 def _empty(stream, device, dtype, *shape):
-    """Uninitialised memory of the call's stream: torch's allocator hands it on,
-    once it is free, only to later work of that stream."""
+    """Uninitialised memory of the call's stream."""
     if stream is None:
         return torch.empty(*shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
+    with kda._allocating_on(stream):
         return torch.empty(*shape, dtype=dtype, device=device)
 
 
@@ -277,12 +278,12 @@ def scan_segments(cu_seqlens, D: int) -> int:
     return 1
 
 
-def _scan(plan, x, g, initial_state, tied):
+def _scan(plan, x, g, initial_state, tied, stream):
     T, D = g.shape
     if T != plan.T:
         raise ValueError(f"inputs hold {T} tokens, the plan {plan.T}")
     dt, dev = g.dtype, g.device
-    blob = plan.device_blob(dev)
+    blob = plan.device_blob(dev, stream)
     args = [plan.handle, *_buf(blob, torch.int32, (len(plan.blob),), "plan_dev", dev), D, _dtype(g, "g"),
             *_rows(x, dt, (T, D), "x", dev), *_rows(g, dt, (T, D), "g", dev), int(bool(tied)),
             *_buf(initial_state, torch.float32, (plan.N, D), "initial_state", dev)]
@@ -294,7 +295,7 @@ def scan_forward(plan: kda.Plan, x, g, initial_state=None, tied=False, h_dtype=N
     when ``tied``, for x and g [T, D] (bf16 or fp32), every sequence of the plan
     from its ``initial_state`` [N, D] (default: zero).  Returns dict(h,
     final_state), h in ``h_dtype`` (default: x's), final_state fp32."""
-    T, D, dev, args = _scan(plan, x, g, initial_state, tied)
+    T, D, dev, args = _scan(plan, x, g, initial_state, tied, stream)
     if out is None:
         out = dict(h=_empty(stream, dev, g.dtype if h_dtype is None else h_dtype, T, D),
                    final_state=_empty(stream, dev, torch.float32, plan.N, D))
@@ -313,7 +314,7 @@ def scan_backward(plan: kda.Plan, x, g, h, dh, d_final=None, initial_state=None,
     ``d_final`` [N, D] (default: zero) as dict(dx, dg, dh0).  ``h`` is what the
     forward wrote; x is only read when ``tied``.  dh0 (fp32) is None unless
     ``want_dh0`` (default: whether there are initial states)."""
-    T, D, dev, args = _scan(plan, x if tied else None, g, initial_state, tied)
+    T, D, dev, args = _scan(plan, x if tied else None, g, initial_state, tied, stream)
     f32 = torch.float32
     want = initial_state is not None if want_dh0 is None else want_dh0
     out = dict(dx=_empty(stream, dev, g.dtype, T, D), dg=_empty(stream, dev, g.dtype, T, D),

@@ -51,3 +51,47 @@ def test_workspace_outlives_the_call(name, monkeypatch):
     assert seen == [name]
     gc.collect()
     assert made[0][0]() is None, "the workspace is kept after the call"
+
+
+class _Copy:
+    """Stands for a plan's device copy; remembers the streams it waits for."""
+
+    def __init__(self):
+        self.recorded = []
+
+    def record_stream(self, stream):
+        self.recorded.append(stream)
+
+
+def test_plan_copy_waits_for_its_readers(monkeypatch):
+    """Dropping a plan may not hand its device copy on while a stream that it
+    was asked for still reads it: each is recorded, once."""
+    device, plan = torch.device("cuda:0"), kda.Plan([0, 5], 1)
+    t = plan._dev[device] = _Copy()
+    current = [7]
+    monkeypatch.setattr(kda, "_raw_stream", lambda d: current[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: ("current", current[0]))
+
+    class Side:
+        cuda_stream = 9
+
+    for _ in range(2):
+        assert plan.device_blob(device) is t
+        assert plan.device_blob(device, Side) is t
+    current[0] = 11
+    plan.device_blob(device)
+    assert t.recorded == [("current", 7), Side, ("current", 11)]
+
+
+def test_scans_ask_for_the_plan_on_their_stream(monkeypatch):
+    """Both directions name the call's stream when they ask for the plan's copy."""
+    T, D = 10, 8
+    x, plan, asked = torch.zeros(T, D), kda.Plan([0, T], 1), []
+    blob = torch.from_numpy(plan.blob.copy())
+    monkeypatch.setattr(kda.Plan, "device_blob", lambda self, device, stream=None: asked.append(stream) or blob)
+    monkeypatch.setattr(layer, "_empty", lambda stream, device, dtype, *shape: torch.empty(*shape, dtype=dtype))
+    monkeypatch.setattr(layer, "_call", lambda *a: None)
+    layer.scan_forward(plan, x, x, stream="side")
+    layer.scan_backward(plan, x, x, x, x, stream="side")
+    layer.scan_forward(plan, x, x)
+    assert asked == ["side", "side", None]
