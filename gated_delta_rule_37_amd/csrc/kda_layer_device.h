@@ -255,8 +255,8 @@ __device__ __forceinline__ float element(const RawVec<bf16_t, 4>& r, int i) {
 }
 __device__ __forceinline__ float element(const RawVec<fp32_t, 4>& r, int i) { return r.a[i]; }
 
-// 1 - e^g for g <= 0, given a = e^g.  The difference cancels near 0; above
-// -1/4 the Taylor sum to g^6 / 6! replaces it, exact to 2^-24 relative.
+// 1 - e^g, given a = e^g.  The difference cancels near 0; for |g| < 1/4 the
+// Taylor sum to g^6 / 6! replaces it, exact to 2^-24 relative.
 __device__ __forceinline__ float one_minus_exp(float g, float a) {
   float s = 1.f / 720.f;
   s = s * g + 1.f / 120.f;
@@ -266,7 +266,7 @@ __device__ __forceinline__ float one_minus_exp(float g, float a) {
   s = s * g + 1.f;
   float near = -g * s;
   asm("" : "+v"(near));   // both sides and a select: cheaper than branching around the sum
-  return g > -0.25f ? near : 1.f - a;
+  return fabsf(g) < 0.25f ? near : 1.f - a;
 }
 
 // e^x by the hardware's 2^x: relative error about 1 + |x| units of 2^-24,

@@ -106,3 +106,22 @@ def test_output_norm_of_large_values(V, o_dtype):
     want, bounds = lr.output_norm_backward(dy.double(), **args), lr.output_norm_backward_bounds(dy.double(), **args)
     for n, t in grads.items():
         lr.assert_close(t, want[n], bounds[n], n)
+
+
+# ------------------------------------------------------------- 1 - e^g on both sides of zero
+
+
+@pytest.mark.parametrize("one_token", [False, True])
+def test_tied_input_of_any_gate(one_token):
+    """h = (1 - e^g) x from zero.  Near zero a series, 8 EPS of the value; else a
+    difference, 4 EPS of e^g and |g| for its argument's rounding, and its own."""
+    g = torch.cat([torch.linspace(-3, 3, 193), torch.tensor([0.0, -0.25, 0.25, 1e-6, -1e-6, 1e-30, -1e-30, 5.0])])
+    x, D = torch.ones_like(g), g.numel()
+    if one_token:
+        got = layer.scan_step(_d(x[None]), _d(g[None]), torch.zeros(1, D, device=DEV), tied=True)
+    else:
+        got = layer.scan_forward(kda.Plan([0, 1], 1), _d(x[None]), _d(g[None]), tied=True)["h"]
+    w = g.double()
+    want = -torch.expm1(w)
+    slack = torch.where(w.abs() < 0.25, 8 * want.abs(), 2 * want.abs() + torch.exp(w) * (4 + w.abs()))
+    lr.assert_close(got[0], want, lr.EPS * slack, "h")
