@@ -273,6 +273,16 @@ __device__ __forceinline__ float one_minus_exp(float g, float a) {
 // results below 2^-126 are 0.
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
+// sigmoid(z) and sigmoid(-z) = 1 - sigmoid(z), from e^-|z|: each to a few units
+// of its own value however small it is, so that a gradient of a saturated gate,
+// up * down, is not the 0 that 1 - up rounds to from z = 17 on.
+struct Sigmoids {
+  float up, down;
+};
+__device__ __forceinline__ Sigmoids sigmoids(float z) {
+  const float t = fast_exp(-fabsf(z)), large = __builtin_amdgcn_rcpf(1.f + t), small = t * large;
+  return z < 0.f ? Sigmoids{small, large} : Sigmoids{large, small};
+}
 __device__ __forceinline__ float sigmoidf(float z) { return __builtin_amdgcn_rcpf(1.f + fast_exp(-z)); }
 
 }  // namespace kda

@@ -60,10 +60,10 @@ __device__ __forceinline__ float act(int32_t activation, float z) {
   return activation == KDA_ACT_SILU ? z * s : s;
 }
 __device__ __forceinline__ void act_and_slope(int32_t activation, float z, float& a, float& slope) {
-  const float s = sigmoidf(z);
+  const Sigmoids s = sigmoids(z);
   const bool silu = activation == KDA_ACT_SILU;
-  a = silu ? z * s : s;
-  slope = silu ? s * (1.f + z * (1.f - s)) : s * (1.f - s);
+  a = silu ? z * s.up : s.up;
+  slope = s.up * (silu ? 1.f + z * s.down : s.down);
 }
 
 // One lane's share of a row: vectors j LANES + lane of j = 0..NV-1.  WHOLE:

@@ -155,8 +155,8 @@ __global__ __launch_bounds__(kRowThreads) void prepare_backward_kernel(PreparePa
     store<8>(static_cast<E*>(p.k) + at, dk);
     store<8>(static_cast<E*>(p.g) + at, dg);
     if (w.lane == 0) {
-      const float s = sigmoidf(b[0]);
-      b[0] = db * s * (1.f - s);
+      const Sigmoids s = sigmoids(b[0]);
+      b[0] = db * s.up * s.down;
       store<1>(static_cast<E*>(p.beta) + row, b);
     }
   }

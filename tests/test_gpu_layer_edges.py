@@ -108,6 +108,41 @@ def test_output_norm_of_large_values(V, o_dtype):
         lr.assert_close(t, want[n], bounds[n], n)
 
 
+# ------------------------------------------------------------- saturated gates
+
+
+def _both_signs(lo, hi, *shape, seed):
+    z = _uniform(lo, hi, *shape, seed=seed)
+    return torch.where(_randn(*shape, seed=seed + 1) < 0, -z, z)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "silu"])
+def test_output_norm_backward_of_saturated_gates(kind):
+    """The slope of a saturated gate keeps its relative precision: sigmoid(z)
+    sigmoid(-z), not s (1 - s).  The norm's and the products' 64 EPS and 4 |z|
+    of the exponential; silu's 1 + z sigmoid(-z) has no cancellation there."""
+    T, H, V = 5, 2, 128
+    z = _both_signs(8.0, 80.0, T, H, V, seed=1)
+    o, dy, weight = _randn(T, H, V, seed=3), _randn(T, H, V, seed=4), 1 + 0.5 * _randn(V, seed=5)
+    got = layer.output_norm_backward(_d(dy), _d(o), _d(weight), gate=_d(z), activation=kind)["d_gate"]
+    zw, ow = z.double(), o.double()
+    up, down = lr.sigmoid(zw), lr.sigmoid(-zw)
+    slope = up * down if kind == "sigmoid" else up * (1 + zw * down)
+    n = ow / torch.sqrt((ow * ow).mean(-1, keepdim=True) + 1e-6)
+    want = dy.double() * weight.double() * n * slope
+    lr.assert_close(got, want, lr.EPS * want.abs() * (64 + 4 * zw.abs()), "d_gate")
+
+
+def test_prepare_backward_of_saturated_beta():
+    """dbeta sigmoid(b) sigmoid(-b), 24 EPS and 4 |b| of the exponential."""
+    T, H = 40, 8
+    b, dbeta = _both_signs(8.0, 80.0, T, H, seed=1), _randn(T, H, seed=3)
+    rows = _d(_randn(T, H, 128, seed=4))
+    got = layer.prepare_inputs_backward(rows, rows, rows, _d(b), _d(torch.zeros(H)), None, rows, rows, rows, _d(dbeta))
+    want = dbeta.double() * lr.sigmoid(b.double()) * lr.sigmoid(-b.double())
+    lr.assert_close(got["dbeta_raw"], want, lr.EPS * want.abs() * (24 + 4 * b.double().abs()), "dbeta_raw")
+
+
 # ------------------------------------------------------------- 1 - e^g on both sides of zero
 
 
