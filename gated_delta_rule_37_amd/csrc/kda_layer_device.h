@@ -213,6 +213,8 @@ __device__ __forceinline__ float column_sum(const float* p, int64_t row, int32_t
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eLow = 1.92596299e-08f;   // log2(e) - kLog2e
+constexpr float kLn2 = 0.6931471805599453f;
 
 // Raw storage of VEC elements, so that a load can stay in flight unconverted.
 template <typename E, int VEC>
@@ -269,9 +271,18 @@ __device__ __forceinline__ float one_minus_exp(float g, float a) {
   return fabsf(g) < 0.25f ? near : 1.f - a;
 }
 
-// e^x by the hardware's 2^x: relative error about 1 + |x| units of 2^-24,
-// results below 2^-126 are 0.
+// e^x by the hardware's 2^p, p = x log2(e); results below 2^-126 are 0.  p is
+// rounded, to half a unit of up to 2^7, so the relative error is about 1 + |x|
+// units of 2^-24: for results that are stored in bf16.
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+// The same for fp32 results, to at most 4 units (2^p itself 2): what p lost, and
+// log2(e) itself, is worked in to first order.  Where 2^p is 0, infinite or NaN
+// there is nothing to correct.
+__device__ __forceinline__ float exact_exp(float x) {
+  const float p = x * kLog2e, e = __builtin_amdgcn_exp2f(p);
+  const float lost = __fmaf_rn(x, kLog2e, -p) + x * kLog2eLow;
+  return fabsf(p) < 128.f ? __fmaf_rn(e, lost * kLn2, e) : e;
+}
 
 // sigmoid(z) and sigmoid(-z) = 1 - sigmoid(z), from e^-|z|: each to a few units
 // of its own value however small it is, so that a gradient of a saturated gate,
@@ -280,10 +291,10 @@ struct Sigmoids {
   float up, down;
 };
 __device__ __forceinline__ Sigmoids sigmoids(float z) {
-  const float t = fast_exp(-fabsf(z)), large = __builtin_amdgcn_rcpf(1.f + t), small = t * large;
+  const float t = exact_exp(-fabsf(z)), large = __builtin_amdgcn_rcpf(1.f + t), small = t * large;
   return z < 0.f ? Sigmoids{small, large} : Sigmoids{large, small};
 }
-__device__ __forceinline__ float sigmoidf(float z) { return __builtin_amdgcn_rcpf(1.f + fast_exp(-z)); }
+__device__ __forceinline__ float sigmoidf(float z) { return __builtin_amdgcn_rcpf(1.f + exact_exp(-z)); }
 
 }  // namespace kda
 

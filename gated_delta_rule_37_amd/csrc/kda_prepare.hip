@@ -36,9 +36,12 @@ struct PrepareParams {
 
 // softplus(z) = max(z, 0) + log1p(t), t = e^-|z|, with log1p(t) =
 // 2 atanh(s), s = t / (2 + t) <= 1/3: the odd series to s^15 leaves 2^-26, and
-// no branch or cancellation loses relative precision where t is small.
+// no branch or cancellation loses relative precision where t is small.  EXACT:
+// for a result in fp32 (the forward's is rounded to bf16: 316 us against 318 at
+// 32768 x 32 heads).
+template <bool EXACT>
 __device__ __forceinline__ float softplusf(float z) {
-  const float t = fast_exp(-fabsf(z)), s = t * __builtin_amdgcn_rcpf(2.f + t), w = s * s;
+  const float t = EXACT ? exact_exp(-fabsf(z)) : fast_exp(-fabsf(z)), s = t * __builtin_amdgcn_rcpf(2.f + t), w = s * s;
   float a = 1.f / 15.f;
   a = a * w + 1.f / 13.f;
   a = a * w + 1.f / 11.f;
@@ -72,7 +75,7 @@ __global__ __launch_bounds__(kRowThreads) void prepare_kernel(PrepareParams p) {
   if (!w.active) return;
   const int32_t c0 = w.lane * 8;
   const int64_t col = static_cast<int64_t>(w.head) * 128 + c0;
-  const float rate = -fast_exp(p.a_log[w.head]);
+  const float rate = -exact_exp(p.a_log[w.head]);
   float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (p.dt_bias != nullptr) load<8>(p.dt_bias + col, bias);
   for (int64_t t = w.token; t < p.T; t += p.lanes) {
@@ -93,7 +96,7 @@ __global__ __launch_bounds__(kRowThreads) void prepare_kernel(PrepareParams p) {
     for (int i = 0; i < 8; ++i) {
       q[i] *= rq;
       k[i] *= rk;
-      z[i] = rate * softplusf(z[i] + bias[i]);
+      z[i] = rate * softplusf<false>(z[i] + bias[i]);
     }
     const int64_t row = t * p.H + w.head, out = row * 128 + c0;
     store<8, STREAM>(static_cast<bf16_t*>(p.q) + out, q);
@@ -112,7 +115,7 @@ __global__ __launch_bounds__(kRowThreads) void prepare_backward_kernel(PreparePa
   if (!w.active) return;
   const int32_t c0 = w.lane * 8;
   const int64_t col = static_cast<int64_t>(w.head) * 128 + c0;
-  const float rate = -fast_exp(p.a_log[w.head]);
+  const float rate = -exact_exp(p.a_log[w.head]);
   float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (p.dt_bias != nullptr) load<8>(p.dt_bias + col, bias);
   float sum_bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -147,7 +150,7 @@ __global__ __launch_bounds__(kRowThreads) void prepare_backward_kernel(PreparePa
       dq[i] = p.q_scale * rq * (dq[i] - (q[i] * rq) * pq);
       dk[i] = rk * (dk[i] - (k[i] * rk) * pk);
       const float v = z[i] + bias[i];
-      sum_decay += dg[i] * rate * softplusf(v);
+      sum_decay += dg[i] * rate * softplusf<true>(v);
       dg[i] = dg[i] * rate * sigmoidf(v);
       sum_bias[i] += dg[i];
     }

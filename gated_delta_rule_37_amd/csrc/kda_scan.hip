@@ -77,6 +77,17 @@ __device__ __forceinline__ float decay_after(float A, float a) { return a == 0.f
 constexpr uint32_t kEmpty = 0xffffffffu;
 __device__ __forceinline__ uint32_t float_bits(float x) { return x != x ? 0x7fc00000u : __float_as_uint(x); }
 
+// The decay e^g of the scan over gates of type E and states stored as O.  In bf16
+// throughout the hardware's exponential has to do, in both directions: 65536 x
+// 4096 forward 292 us, with the exact one in both walks 320 (backward 235 and
+// 238).  Gates near 0, which remember, lose nothing there, and a gate far below
+// 0 scales what is left of the state by 1 + |g| units of 2^-24.
+template <typename E, typename O>
+__device__ __forceinline__ float decay_of(float g) {
+  constexpr bool kBf16 = sizeof(E) == 2 && sizeof(O) == 2;
+  return kBf16 ? fast_exp(g) : exact_exp(g);
+}
+
 // This workgroup's channel block; each block gets as many workgroups as there
 // are tiles.  Workgroups go round the 8 XCDs in launch order: without the shift
 // from round to round, an XCD would keep the same blocks where their number is
@@ -355,7 +366,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(ScanParams p) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         const float gi = element(g[r], i);
-        a[i] = fast_exp(gi);
+        a[i] = decay_of<E, O>(gi);
         v[i] = TIED ? one_minus_exp(gi, a[i]) * element(x[r], i) : element(x[r], i);
         if (kKeep) u[r][i] = v[i];
       }
@@ -373,7 +384,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(ScanParams p) {
       }
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float gi = element(g[r], i), a = fast_exp(gi);
+        const float gi = element(g[r], i), a = decay_of<E, O>(gi);
         float v = kKeep ? u[r][i] : element(x[r], i);
         if (TIED && !kKeep) v *= one_minus_exp(gi, a);
         h[i] = a * h[i] + v;
@@ -426,7 +437,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_backward_kernel(ScanParams 
       float a[VEC], v[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        a[i] = fast_exp(element(g[r], i));
+        a[i] = decay_of<E, O>(element(g[r], i));
         v[i] = a[i] * element(dh[r], i);
       }
       // a sequence's last token: c = a (dh + d_final)
@@ -450,7 +461,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_backward_kernel(ScanParams 
       }
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float gi = element(g[r], i), a = fast_exp(gi), l = element(dh[r], i) + c[i];
+        const float gi = element(g[r], i), a = decay_of<E, O>(gi), l = element(dh[r], i) + c[i];
         dx[i] = TIED ? one_minus_exp(gi, a) * l : l;
         c[i] = a * l;
         dg[i] = c[i] * (TIED ? hp[i] - element(x[r], i) : hp[i]);

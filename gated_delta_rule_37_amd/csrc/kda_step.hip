@@ -89,7 +89,7 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(StepParams p) {
       if (p.gate_floor_on) g = fmaxf(g, p.gate_floor);
       key[0][threadIdx.x] = bf2f(p.k[c]);
       key[1][threadIdx.x] = bf2f(p.q[c]);
-      key[2][threadIdx.x] = fast_exp(g);
+      key[2][threadIdx.x] = exact_exp(g);
     }
     const float beta = bf2f(p.beta[bh]);
     float v[4];
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(kScanStepThreads) void scan_step_kernel(ScanStepPar
       load<VEC>(static_cast<const E*>(p.g) + row, g);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float a = fast_exp(g[i]);
+        const float a = exact_exp(g[i]);
         h[i] = a * h[i] + (p.tied ? one_minus_exp(g[i], a) : 1.f) * x[i];
       }
       store<VEC>(static_cast<E*>(p.h) + row, h);

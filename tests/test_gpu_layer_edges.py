@@ -160,3 +160,69 @@ def test_tied_input_of_any_gate(one_token):
     want = -torch.expm1(w)
     slack = torch.where(w.abs() < 0.25, 8 * want.abs(), 2 * want.abs() + torch.exp(w) * (4 + w.abs()))
     lr.assert_close(got[0], want, lr.EPS * slack, "h")
+
+
+# ------------------------------------------------------------- precision of the exponentials
+
+
+def test_prepare_backward_keeps_fp32_precision():
+    """dgate = -dg e^a sigmoid(z): the rate 4 EPS, the sigmoid 10 (exponential 4,
+    its weight in 1 + t 2, that sum 1, reciprocal 2, product 1), two products:
+    16.  da: the softplus 16, rate and products 6, 128 terms in 8 + 4 additions
+    and 2 of the partial sums: 36 of the terms' magnitudes."""
+    T, H = 6, 5
+    z, dg = _uniform(-80.0, 20.0, T, H, 128, seed=1), _randn(T, H, 128, seed=2)
+    a_log = _uniform(-6.0, 6.0, H, seed=3)
+    one = torch.ones(T, H, 128)
+    got = layer.prepare_inputs_backward(_d(one), _d(one), _d(z), _d(torch.zeros(T, H)), _d(a_log), None, _d(one), _d(one),
+                                        _d(dg), _d(torch.zeros(T, H)))
+    rate, w = -torch.exp(a_log.double())[:, None], z.double()
+    want = dg.double() * rate * lr.sigmoid(w)
+    lr.assert_close(got["dgate_raw"], want, 16 * lr.EPS * want.abs(), "dgate_raw")
+    terms = dg.double() * rate * lr.softplus(w)
+    lr.assert_close(got["da_log"], terms.sum((0, 2)), 40 * lr.EPS * terms.abs().sum((0, 2)), "da_log")
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "silu"])
+def test_output_norm_keeps_fp32_precision(kind):
+    """Rows of 8 channels, one lane's: 8 terms' additions and the mean's scaling
+    give at most 10 EPS of the mean square, 5 of the root, 2 of the reciprocal
+    root, 4 products, the gate's 10 and its product: 22."""
+    T, H, V = 300, 2, 8
+    z, o = _uniform(-80.0, 20.0, T, H, V, seed=1), _randn(T, H, V, seed=2)
+    weight = 1 + 0.5 * _randn(V, seed=3)
+    got = layer.output_norm(_d(o), _d(weight), gate=_d(z), activation=kind)
+    args = dict(o=o.double(), weight=weight.double(), gate=z.double(), kind=kind, res_scale=None, residual=None, eps=1e-6)
+    want = lr.output_norm(**args)
+    lr.assert_close(got, want, 22 * lr.EPS * want.abs(), "y")
+
+
+@pytest.mark.parametrize("D", [512, 3])
+def test_decays_keep_fp32_precision(D):
+    """One token from a state, no input: h = e^g h0, 4 EPS of the exponential, a
+    product and a sum; the gradient dg = e^g dh h0 one product more."""
+    N = 1024 if D == 3 else 64
+    g, h0, dh = _uniform(-80.0, 0.0, N, D, seed=1), _randn(N, D, seed=2), _randn(N, D, seed=3)
+    zero, plan = torch.zeros(N, D, device=DEV), kda.Plan(list(range(N + 1)), 1)
+    a = torch.exp(g.double())
+    want = a * h0.double()
+    got = layer.scan_forward(plan, zero, _d(g), initial_state=_d(h0))
+    for n in ("h", "final_state"):
+        lr.assert_close(got[n], want, 6 * lr.EPS * want.abs(), n)
+    pool = _d(h0).clone()
+    lr.assert_close(layer.scan_step(zero, _d(g), pool), want, 6 * lr.EPS * want.abs(), "step h")
+    lr.assert_close(pool, want, 6 * lr.EPS * want.abs(), "step state")
+    back = layer.scan_backward(plan, None, _d(g), got["h"], _d(dh), initial_state=_d(h0))
+    lr.assert_close(back["dg"], dh.double() * want, 8 * lr.EPS * (dh.double() * want).abs(), "dg")
+    lr.assert_close(back["dh0"], dh.double() * a, 6 * lr.EPS * (dh.double() * a).abs(), "dh0")
+
+
+def test_step_decay_keeps_fp32_precision():
+    """kda_step with k = 0: S = Diag(e^g) S, 4 EPS and a product."""
+    B, H = 6, 3
+    g, state = _uniform(-80.0, 0.0, B, H, 128, seed=1).to(BF), _randn(B, H, 128, 128, seed=2)
+    zero = torch.zeros(B, H, 128, dtype=BF, device=DEV)
+    pool = _d(state).clone()
+    layer.step(zero, zero, zero, _d(g), torch.zeros(B, H, dtype=BF, device=DEV), pool)
+    want = torch.exp(g.double())[..., None] * state.double()
+    lr.assert_close(pool, want, 6 * lr.EPS * want.abs(), "state")
