@@ -226,3 +226,30 @@ def test_step_decay_keeps_fp32_precision():
     layer.step(zero, zero, zero, _d(g), torch.zeros(B, H, dtype=BF, device=DEV), pool)
     want = torch.exp(g.double())[..., None] * state.double()
     lr.assert_close(pool, want, 6 * lr.EPS * want.abs(), "state")
+
+
+# ------------------------------------------------------------- single tokens, slot by slot
+
+
+@pytest.mark.parametrize("D,dtype,tied", [(8, BF, True), (13, F32, False), (300, F32, True)])
+def test_scan_step_slot_by_slot(D, dtype, tied):
+    """As many roundings as the element's own slot has tokens, of its own
+    magnitudes: 24 EPS a token of |state| + sum |x|.  Unused rows count nowhere."""
+    B, n = 300, 400
+    slots = torch.randperm(n, generator=torch.Generator().manual_seed(B))[:B].to(torch.int32)
+    slots[::17] = -1
+    slots[5] = slots[B - 1]
+    x, g = _randn(B, D, seed=1, dtype=dtype), (-_randn(B, D, seed=2).abs()).to(dtype)
+    state, h0 = _randn(n, D, seed=3), torch.full((B, D), -7.0).to(dtype)
+    pool = _d(state).clone()
+    h = layer.scan_step(_d(x), _d(g), pool, _d(slots), h=_d(h0), tied=tied)
+    want_h, want = lr.scan_step(x.double(), g.double(), state.double(), slots, h0.double(), tied)
+    used = (slots >= 0) & (slots < n)
+    tokens = torch.bincount(slots[used].long(), minlength=n).double()
+    assert tokens.max() == 2
+    mag = state.double().abs().index_add(0, slots[used].long(), x.double()[used].abs())
+    slack = 24 * lr.EPS * tokens[:, None] * mag
+    lr.assert_close(pool, want, slack, "state")
+    row_slack = torch.zeros(B, D).double()
+    row_slack[used] = slack[slots[used].long()]
+    lr.assert_close(h, want_h, row_slack, "h")
