@@ -253,3 +253,32 @@ def test_scan_step_slot_by_slot(D, dtype, tied):
     row_slack = torch.zeros(B, D).double()
     row_slack[used] = slack[slots[used].long()]
     lr.assert_close(h, want_h, row_slack, "h")
+
+
+# ------------------------------------------------------------- sequences and tiles
+
+
+@pytest.mark.parametrize("D,dtype,h_dtype", [(70, F32, F32), (2, BF, F32), (1600, BF, BF)])
+@pytest.mark.parametrize("cu,S", [
+    ([0, 128], 1), ([0, 128, 256], 1), ([0, 127, 128, 129, 384], 1), ([0, 1, 256, 257], 2),   # at a tile's edge
+    (list(range(0, 601)), 1), ([0, 5] + list(range(6, 700, 2)), 1),                          # more than 256 sequences
+    ([0, 500, 3000], 300)])                                                                   # more than 256 segments
+def test_scan_boundaries(cu, S, D, dtype, h_dtype):
+    """Tokens that are whole tiles, sequences that begin where a tile does, and
+    more fragments of the plan than a workgroup has threads."""
+    T, N = cu[-1], len(cu) - 1
+    at = slice(0, D) if D < 100 else torch.cat([torch.arange(0, 16), torch.arange(D - 16, D)])   # the channels looked at
+    x, g = _randn(T, D, seed=1, dtype=dtype), (-0.05 * _randn(T, D, seed=2).abs()).to(dtype)
+    h0, d_final, dh = _randn(N, D, seed=3), _randn(N, D, seed=4), _randn(T, D, seed=5, dtype=h_dtype)
+    plan = kda.Plan(cu, S)
+    got = layer.scan_forward(plan, _d(x), _d(g), initial_state=_d(h0), tied=True, h_dtype=h_dtype)
+    w = [t[:, at].double() for t in (x, g)]
+    want, final = lr.scan(*w, cu, h0[:, at].double(), True)
+    eh, ef = lr.scan_bound(*w, cu, h0[:, at].double(), True)
+    lr.assert_close(got["h"][:, at], want, eh, "h")
+    lr.assert_close(got["final_state"][:, at], final, ef, "final_state")
+    back = layer.scan_backward(plan, _d(x), _d(g), got["h"], _d(dh), d_final=_d(d_final), initial_state=_d(h0), tied=True)
+    args = (*w, got["h"].cpu()[:, at].double(), cu, h0[:, at].double(), True, dh[:, at].double(), d_final[:, at].double())
+    want, bounds = lr.scan_backward(*args), lr.scan_backward_bounds(*args)
+    for n, t in back.items():
+        lr.assert_close(t[:, at], want[n], bounds[n], n)

@@ -1,5 +1,7 @@
 """Memory of calls on another stream than the current one, on the GPU: what a
 call allocates and a plan's device copy are not handed on while it runs."""
+import threading
+
 import pytest
 import torch
 
@@ -74,3 +76,43 @@ def test_forward_and_backward_allocate_on_their_stream(busy):
         assert torch.equal(f[n], want_f[n]), n
     for n in want_b:
         assert torch.equal(b[n], want_b[n]), n
+
+
+def test_two_threads_on_one_stream():
+    """Calls of two threads at once on the shared default stream: each keeps its
+    own workspace and outputs, and gives the bits that it gives alone."""
+    T, D, H = 3000, 200, 4
+    plan = kda.Plan([0, 1000, T], 1)
+    plan.device_blob(DEV)
+
+    def inputs(seed):
+        gen = torch.Generator().manual_seed(seed)
+        x, rows = torch.randn(T, D, generator=gen).to(DEV), torch.randn(300, H, 128, generator=gen).to(DEV)
+        return x, -x.abs(), rows, rows[:, :, 0].contiguous(), rows[0, :, 0].contiguous()
+
+    def work(x, g, rows, b, a_log):
+        f = layer.scan_forward(plan, x, g, tied=True)
+        s = layer.scan_backward(plan, x, g, f["h"], x, tied=True, want_dh0=True)
+        n = layer.output_norm_backward(rows, rows, rows[0, 0].contiguous(), gate=rows)
+        p = layer.prepare_inputs_backward(rows, rows, rows, b, a_log, None, rows, rows, rows, b)
+        return [t for d in (f, s, n, p) for t in d.values() if t is not None]
+
+    sets = [inputs(s) for s in (1, 2)]
+    want = [work(*s) for s in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def run(i):
+        for _ in range(20):
+            got[i].append(work(*sets[i]))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 20
+        for outs in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want[i]))
