@@ -108,14 +108,14 @@ NormShape norm_shape(int32_t V) {
   return {512, 2};
 }
 // Backward: each workgroup leaves partial sums, so only as many as run at once
-// and have enough in flight.  Two vectors a lane (156-174 registers): three
+// and have enough in flight.  Two vectors a lane (154-178 registers): three
 // workgroups a CU of 256 threads and one of 512; with 65536 rows of 1024 bf16
 // channels 768 workgroups 114 us, 512 142, 1024 154, with rows of 8192 256
 // workgroups 161, 512 166.  One vector (85-92 registers): four of bf16 o (2^26
-// channels in rows of 128, 256, 512 and 2048: 1024 workgroups 111, 110, 111 and
-// 113 us, 768 114, 114, 114 and 121), three of fp32 o, whose loads are twice as
-// many (with a gate: 768 workgroups 176, 177, 176 and 183 us, 1024 180, 180, 180
-// and 183, 512 187 to 198).
+// channels in rows of 128, 256, 512 and 2048: 1024 workgroups 109, 110, 111 and
+// 113 us, 768 111, 114, 115 and 122), three of fp32 o, whose loads are twice as
+// many (with a gate: 768 workgroups 181, 178, 179 and 182 us, 1024 183, 181, 181
+// and 186, 512 191 to 206).
 int32_t norm_bwd_blocks(const NormShape& s, int32_t o_format) {
   if (s.vectors == 1 && o_format == KDA_BF16) return 1024;
   return s.lanes == 512 ? 256 : 768;

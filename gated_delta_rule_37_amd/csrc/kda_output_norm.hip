@@ -13,8 +13,8 @@
 // once, HBM bandwidth is the bound.  Rows whose width or stride is not a
 // multiple of 16 bytes take the same vectors at any address, and what is left
 // of the row one by one.  fp32 o, gate and y in bf16, 65536 x 32 heads of
-// 128 forward 380 us, 5.7 TB/s; 8191 x 16 backward with every term 40 us, 5.8
-// TB/s (part of it from the last-level cache), and 6 us for the sums over the
+// 128 forward 378 us, 5.7 TB/s; 8191 x 16 backward with every term 42 us, 5.6
+// TB/s (part of it from the last-level cache), and 5 us for the sums over the
 // rows (a large copy: 5.2 TB/s).
 #include "kda_layer.h"
 #include "kda_layer_device.h"

@@ -15,8 +15,12 @@
 // map, gets the state before its tile from the maps of the tiles before it
 // (look_back), publishes the state behind it, and only then walks its tokens
 // from that state and writes.  Each element is read and written once, so HBM
-// bandwidth is the bound: 65536 x 4096 bf16 forward (tied) 292-310 us, 5.2-5.5
-// TB/s, 32768 x 4096 backward 234-242 us, 5.6 TB/s (a large copy: 5.2).
+// bandwidth is the bound where there are many channel blocks of whole 128-byte
+// lines: 65536 x 4096 bf16 forward (tied) 292-310 us, 5.2-5.5 TB/s, 32768 x 4096
+// backward 234-242 us, 5.6 TB/s (a large copy: 5.2).  Few blocks are bound by the
+// chain of look-backs (32768 x 64 forward 36 us, backward 38, 0.3 and 0.7 TB/s),
+// rows whose lines two blocks share likely by fetching them twice (32768 x 4093
+// 237 and 480 us, 3.4 TB/s).
 //
 // What was measured on the way, 65536 x 4096 forward: a thread walking a channel
 // alone 31.6 ms; a workgroup owning 16 channels and walking the whole sequence

@@ -20,7 +20,10 @@ namespace kda {
 namespace {
 
 // The rows of the batch that name one slot, in order.  The workgroups of the
-// first such row work for all of them; the others have nothing to do.
+// first such row work for all of them; the others have nothing to do.  Each
+// workgroup reads the whole list, so that cost grows with the square of the
+// rows: nothing up to 1024 of them, 65536 rows of 8 channels 1450 us against 32
+// without slots.
 struct SlotRows {
   const int32_t* slots;   // null: row b is slot b
   int32_t B, num_slots;

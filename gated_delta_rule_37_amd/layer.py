@@ -12,7 +12,8 @@ formula).  Entry points mirror the C names:
   ``kda_output_norm_backward``): the norm of o with its gate, residual and scale
 * :func:`scan_forward`, :func:`scan_backward` (``kda_scan_forward``,
   ``kda_scan_backward``): h_t = exp(g_t) h_{t-1} + u_t per channel over packed
-  sequences; :func:`scan_segments` picks the plan's segment count for it
+  sequences; any plan serves, and one that only they use needs one segment
+  (:func:`scan_segments`)
 * :func:`scan_step` (``kda_scan_step``) and :func:`step` (``kda_step``): single
   tokens over a pool of states
 
