@@ -219,8 +219,8 @@ class Plan:
         device = torch.device(device)
         t = self._dev.get(device)
         if t is None:
-            t = torch.from_numpy(self.blob.copy()).to(device)
-            self._dev[device] = t
+            # one copy, whichever thread comes first: its readers are recorded on it
+            t = self._dev.setdefault(device, torch.from_numpy(self.blob.copy()).to(device))
         if device.type == "cuda":
             raw = _raw_stream(device) if stream is None else stream.cuda_stream
             seen = self._readers.setdefault(device, set())
@@ -410,7 +410,7 @@ def backward(plan: Plan, q, k, v, g, beta, d_o, d_final=None, initial_state=None
     buffers are filled with ``sentinel`` first when it is given.  ``saved`` =
     (transitions, carry_in) as the forward wrote them (no gate lower bound)
     calls ``kda_backward_from_forward``, which reads them instead of
-    recomputing them."""
+    recomputing them.  What the call allocates belongs to ``stream``."""
     T, H, K = k.shape
     V = v.shape[2]
     dev = q.device
@@ -522,7 +522,7 @@ def forward(plan: Plan, q, k, v, g, beta, out=None, stream=None, groups=1, event
     """The whole segmented forward: summaries, compose, carry.  Returns ``out``.
     Sequence n starts from ``initial_state[n]`` ([N, H, K, V] FP32) when given,
     else from zero.  ``o_dtype`` (used when ``out`` is None) is float32 or
-    bfloat16.
+    bfloat16.  Buffers that the call allocates belong to ``stream``.
 
     With ``groups`` > 1 the heads are cut into that many groups.  Summaries and
     carry launches of every group run in order on ``stream``; each group's

@@ -13,7 +13,7 @@ DEV = "cuda:0"
 
 @pytest.fixture(scope="module")
 def busy():
-    """Keeps a stream busy for some milliseconds with scans of its own."""
+    """Keeps a stream busy for some 40 ms with scans of its own."""
     T, D = 32768, 4096
     plan = kda.Plan([0, T], 1)
     x, g = torch.zeros(T, D, dtype=torch.bfloat16, device=DEV), torch.zeros(T, D, dtype=torch.bfloat16, device=DEV)
@@ -22,7 +22,7 @@ def busy():
     torch.cuda.synchronize()
 
     def run(stream):
-        for _ in range(60):
+        for _ in range(200):
             layer.scan_forward(plan, x, g, out=out, stream=stream)
     return run
 
@@ -62,13 +62,19 @@ def test_forward_and_backward_allocate_on_their_stream(busy):
         return f, kda.backward(plan, *ins, d_o, want_dh0=True, stream=stream)
 
     want_f, want_b = work(None)
-    torch.cuda.synchronize()
+    sizes = [t.numel() * t.element_size() for t in want_f.values()] + [
+        int(kda.lib().kda_backward_workspace_bytes(plan.handle, H, 128, 128))]
+
+    def others():
+        return [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(2)]
+
     side = torch.cuda.Stream()
+    work(side)                      # both streams' pools hold what follows
+    others()
+    torch.cuda.synchronize()
     busy(side)
     f, b = work(side)
-    sizes = [t.numel() * t.element_size() for t in f.values()] + [
-        int(kda.lib().kda_backward_workspace_bytes(plan.handle, H, 128, 128))]
-    new = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(2)]
+    new = others()
     assert not side.query()
     side.synchronize()
     assert len(new) == 2 * len(sizes)

@@ -95,3 +95,25 @@ def test_scans_ask_for_the_plan_on_their_stream(monkeypatch):
     layer.scan_backward(plan, x, x, x, x, stream="side")
     layer.scan_forward(plan, x, x)
     assert asked == ["side", "side", None]
+
+
+def test_one_plan_copy_for_all_threads(monkeypatch):
+    """A copy that another thread has made meanwhile is the one that is used, so
+    that the readers are recorded on the copy that the plan keeps."""
+    device, plan, first = torch.device("cuda:0"), kda.Plan([0, 5], 1), _Copy()
+
+    class Blob:
+        def copy(self):
+            return self
+
+    class Host:
+        def to(self, d):
+            plan._dev[d] = first     # the other thread was faster
+            return _Copy()
+
+    plan.blob = Blob()
+    monkeypatch.setattr(torch, "from_numpy", lambda a: Host())
+    monkeypatch.setattr(kda, "_raw_stream", lambda d: 7)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: "current")
+    assert plan.device_blob(device) is first
+    assert first.recorded == ["current"]
