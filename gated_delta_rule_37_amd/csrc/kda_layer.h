@@ -1,6 +1,6 @@
 // Parameter blocks, host checks and launchers of the operators around the
-// recurrence (input preparation, output norm, per-channel scan, single-token
-// steps).  A launcher takes arguments that have passed its check and returns
+// recurrence (input preparation, norms and rotation of queries and keys, output
+// norm, per-channel scan, linear attention, single-token steps).  A launcher takes arguments that have passed its check and returns
 // a kda_status.
 #ifndef KDA_LAYER_H_
 #define KDA_LAYER_H_
@@ -65,6 +65,22 @@ struct StepArgs {
   Dst state_out, o;
 };
 
+struct RotateArgs {
+  int32_t T, Hq, Hk, D, R, dtype, interleaved, d_format;
+  Rows q_raw, k_raw;
+  Rows positions, inv_freq, q_weight, k_weight;   // int32; FP32; stride unused
+  float q_scale, eps;
+  Dst q, k;                                       // backward: gradients of the raw rows
+  Rows dq, dk;                                    // backward only, d_format
+  Dst dq_weight, dk_weight, workspace;
+};
+
+struct LinearStepArgs {
+  int32_t B, H, Hq, Hk, Hv, K, V, g_dtype, o_format, num_slots;
+  Rows q, k, v, g, slots, state;   // g.stride: H, or 0 for one g [H]
+  Dst state_out, o;
+};
+
 // Partial sums over tokens (the backward passes of the row-wise operators).
 // A group of lanes takes rows (t, h) of one head: rows r, r + P H, r + 2 P H,
 // ... for the P "lanes" of tokens; every group leaves one partial row.
@@ -78,6 +94,7 @@ RowGrid row_grid(int64_t T, int64_t H, int32_t groups_per_block, int32_t max_blo
 constexpr int kRowThreads = 256;        // row-wise kernels
 constexpr int64_t kStreamBytes = int64_t(256) << 20;   // the last-level cache: larger calls go past it
 constexpr int kPrepareGroups = 16;      // 16-lane groups of 8 channels a workgroup
+constexpr int kRotateBwdBlocks = 768;   // norms and rotation, backward grid at most: three workgroups a CU
 constexpr int kPrepareBwdBlocks = 512;  // backward grid at most: two workgroups a CU
 
 struct PrepareBwdLayout {
@@ -120,7 +137,18 @@ ScanLayout scan_layout(int32_t T, int32_t D);
 // turned into addresses: one with the top bit set must not pass as negative.
 constexpr bool is_tile(uint32_t ticket, int32_t tiles) { return ticket < static_cast<uint32_t>(tiles); }
 
+// Work of the norms and rotation: `tiles` of `tokens` tokens, forward each by
+// row_blocks workgroups, backward by `blocks` workgroups in all.
+struct RotateGrid {
+  int32_t tokens, tiles, row_blocks, blocks;
+};
+RotateGrid rotate_grid(const RotateArgs& a, bool backward);
+size_t rotate_bwd_workspace(int32_t T, int32_t D);
+bool rotate_whole_rows(const RotateArgs& a);   // pairs of whole, aligned 16-byte vectors
+
 int check_prepare(const PrepareArgs& a, bool backward);
+int check_rotate(const RotateArgs& a, bool backward);
+int check_linear_step(const LinearStepArgs& a);
 int check_norm(const NormArgs& a, bool backward);
 int check_scan(const ScanArgs& a, bool backward);
 int check_scan_step(const ScanStepArgs& a);
@@ -136,6 +164,9 @@ int finish_launch();
 
 int launch_prepare(const PrepareArgs& a, hipStream_t stream);
 int launch_prepare_backward(const PrepareArgs& a, hipStream_t stream);
+int launch_rotate(const RotateArgs& a, hipStream_t stream);
+int launch_rotate_backward(const RotateArgs& a, hipStream_t stream);
+int launch_linear_step(const LinearStepArgs& a, hipStream_t stream);
 int launch_norm(const NormArgs& a, hipStream_t stream);
 int launch_norm_backward(const NormArgs& a, hipStream_t stream);
 int launch_scan(const ScanArgs& a, hipStream_t stream);

@@ -86,6 +86,79 @@ size_t kda_prepare_inputs_backward_workspace_bytes(int32_t T, int32_t H, int32_t
   return kda::prepare_bwd_layout(T, H).total;
 }
 
+int kda_qk_norm_rotate(int32_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t R, int32_t dtype, int32_t interleaved,
+                       const void* q_raw, size_t q_raw_bytes, int64_t q_raw_stride,
+                       const void* k_raw, size_t k_raw_bytes, int64_t k_raw_stride,
+                       const int32_t* positions, size_t positions_bytes,
+                       const float* inv_freq, size_t inv_freq_bytes,
+                       const float* q_weight, size_t q_weight_bytes, const float* k_weight, size_t k_weight_bytes,
+                       float q_scale, float eps, void* q, size_t q_bytes, void* k, size_t k_bytes,
+                       hipStream_t stream) {
+  kda::RotateArgs a{};
+  a.T = T;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.D = D;
+  a.R = R;
+  a.dtype = dtype;
+  a.interleaved = interleaved;
+  a.q_raw = {q_raw, q_raw_bytes, q_raw_stride};
+  a.k_raw = {k_raw, k_raw_bytes, k_raw_stride};
+  a.positions = {positions, positions_bytes, 0};
+  a.inv_freq = {inv_freq, inv_freq_bytes, 0};
+  a.q_weight = {q_weight, q_weight_bytes, 0};
+  a.k_weight = {k_weight, k_weight_bytes, 0};
+  a.q_scale = q_scale;
+  a.eps = eps;
+  a.q = {q, q_bytes};
+  a.k = {k, k_bytes};
+  const int st = kda::check_rotate(a, false);
+  return st != KDA_OK ? st : kda::launch_rotate(a, stream);
+}
+
+int kda_qk_norm_rotate_backward(int32_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t R, int32_t dtype, int32_t interleaved,
+                                const void* q_raw, size_t q_raw_bytes, int64_t q_raw_stride,
+                                const void* k_raw, size_t k_raw_bytes, int64_t k_raw_stride,
+                                const int32_t* positions, size_t positions_bytes,
+                                const float* inv_freq, size_t inv_freq_bytes,
+                                const float* q_weight, size_t q_weight_bytes, const float* k_weight, size_t k_weight_bytes,
+                                float q_scale, float eps,
+                                const void* dq, size_t dq_bytes, const void* dk, size_t dk_bytes, int32_t d_format,
+                                void* dq_raw, size_t dq_raw_bytes, void* dk_raw, size_t dk_raw_bytes,
+                                float* dq_weight, size_t dq_weight_bytes, float* dk_weight, size_t dk_weight_bytes,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  kda::RotateArgs a{};
+  a.T = T;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.D = D;
+  a.R = R;
+  a.dtype = dtype;
+  a.interleaved = interleaved;
+  a.q_raw = {q_raw, q_raw_bytes, q_raw_stride};
+  a.k_raw = {k_raw, k_raw_bytes, k_raw_stride};
+  a.positions = {positions, positions_bytes, 0};
+  a.inv_freq = {inv_freq, inv_freq_bytes, 0};
+  a.q_weight = {q_weight, q_weight_bytes, 0};
+  a.k_weight = {k_weight, k_weight_bytes, 0};
+  a.q_scale = q_scale;
+  a.eps = eps;
+  a.dq = {dq, dq_bytes, 0};
+  a.dk = {dk, dk_bytes, 0};
+  a.d_format = d_format;
+  a.q = {dq_raw, dq_raw_bytes};
+  a.k = {dk_raw, dk_raw_bytes};
+  a.dq_weight = {dq_weight, dq_weight_bytes};
+  a.dk_weight = {dk_weight, dk_weight_bytes};
+  a.workspace = {workspace, workspace_bytes};
+  const int st = kda::check_rotate(a, true);
+  return st != KDA_OK ? st : kda::launch_rotate_backward(a, stream);
+}
+
+size_t kda_qk_norm_rotate_backward_workspace_bytes(int32_t T, int32_t D) {
+  return T <= 0 || D <= 0 || D > 256 ? 0 : kda::rotate_bwd_workspace(T, D);
+}
+
 int kda_output_norm(int32_t T, int32_t H, int32_t V, const void* o, size_t o_bytes, int32_t o_format,
                     const void* gate, size_t gate_bytes, int64_t gate_stride, int32_t activation,
                     const float* weight, size_t weight_bytes, const float* res_scale, size_t res_scale_bytes,
@@ -250,6 +323,35 @@ int kda_step(int32_t B, int32_t H, int32_t K, int32_t V, int32_t head_begin, int
   a.o = {o, o_bytes};
   const int st = kda::check_step(a);
   return st != KDA_OK ? st : kda::launch_step(a, stream);
+}
+
+int kda_linear_step(int32_t B, int32_t H, int32_t Hq, int32_t Hk, int32_t Hv, int32_t K, int32_t V,
+                    const uint16_t* q, size_t q_bytes, const uint16_t* k, size_t k_bytes,
+                    const uint16_t* v, size_t v_bytes, const void* g, size_t g_bytes, int64_t g_stride,
+                    int32_t g_dtype, const int32_t* slots, size_t slots_bytes, int32_t num_slots,
+                    const float* state, size_t state_bytes, float* state_out, size_t state_out_bytes,
+                    void* o, size_t o_bytes, int32_t o_format, hipStream_t stream) {
+  kda::LinearStepArgs a{};
+  a.B = B;
+  a.H = H;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.Hv = Hv;
+  a.K = K;
+  a.V = V;
+  a.g_dtype = g_dtype;
+  a.o_format = o_format;
+  a.num_slots = num_slots;
+  a.q = {q, q_bytes, 0};
+  a.k = {k, k_bytes, 0};
+  a.v = {v, v_bytes, 0};
+  a.g = {g, g_bytes, g_stride};
+  a.slots = {slots, slots_bytes, 0};
+  a.state = {state, state_bytes, 0};
+  a.state_out = {state_out, state_out_bytes};
+  a.o = {o, o_bytes};
+  const int st = kda::check_linear_step(a);
+  return st != KDA_OK ? st : kda::launch_linear_step(a, stream);
 }
 
 }  // extern "C"

@@ -19,6 +19,8 @@ constexpr int32_t kMaxChannels = 1 << 20;
 constexpr int32_t kMaxNormWidth = 8192;
 constexpr int64_t kMaxNormRow = 1 << 24;   // H * V: the column sums' grid
 constexpr int32_t kMaxHeads = 65535;
+constexpr int32_t kMaxRotateWidth = 256;
+constexpr int32_t kMaxLinearWidth = 128;
 constexpr int64_t kMaxStride = (int64_t(1) << 31) - 1;   // 2^30 rows of it stay inside 64-bit byte counts
 
 bool known_type(int32_t t) { return t == KDA_FP32 || t == KDA_BF16; }
@@ -52,6 +54,13 @@ int check_workspace(const Dst& ws, size_t need) {
   if (ws.ptr == nullptr) return KDA_ERR_INVALID_ARG;
   if (!aligned16(ws.ptr)) return KDA_ERR_MISALIGNED;
   return ws.bytes < need ? KDA_ERR_WORKSPACE_TOO_SMALL : KDA_OK;
+}
+
+// Linear attention's heads and widths: q, k and v heads that H is a multiple of.
+int check_linear_heads(int32_t H, int32_t Hq, int32_t Hk, int32_t Hv, int32_t K, int32_t V) {
+  if (H <= 0 || Hq <= 0 || Hk <= 0 || Hv <= 0 || K <= 0 || V <= 0) return KDA_ERR_INVALID_ARG;
+  if (H > kMaxHeads || K > kMaxLinearWidth || V > kMaxLinearWidth || K % 8 != 0 || V % 8 != 0) return KDA_ERR_UNSUPPORTED;
+  return H % Hq != 0 || H % Hk != 0 || H % Hv != 0 ? KDA_ERR_INVALID_ARG : KDA_OK;
 }
 
 // A batch of single tokens over state slots.
@@ -187,6 +196,59 @@ int check_prepare(const PrepareArgs& a, bool backward) {
   return backward ? check_workspace(a.workspace, prepare_bwd_layout(a.T, a.H).total) : KDA_OK;
 }
 
+// Four tokens of one workgroup share the launch's fixed cost once there are
+// enough of them.
+RotateGrid rotate_grid(const RotateArgs& a, bool backward) {
+  RotateGrid g;
+  g.tokens = a.T >= 4096 ? 4 : a.T >= 2048 ? 2 : 1;
+  g.tiles = static_cast<int32_t>((static_cast<int64_t>(a.T) + g.tokens - 1) / g.tokens);
+  const int64_t rows = static_cast<int64_t>(g.tokens) * (static_cast<int64_t>(a.Hq) + a.Hk);
+  // a row takes at most 16 lanes: one round of rows a workgroup where tokens are few
+  g.row_blocks = g.tiles >= 256 ? 1 : static_cast<int32_t>((rows + 15) / 16);
+  g.blocks = backward ? (g.tiles < kRotateBwdBlocks ? g.tiles : kRotateBwdBlocks) : 0;
+  return g;
+}
+size_t rotate_bwd_workspace(int32_t T, int32_t D) {
+  const int32_t blocks = T < kRotateBwdBlocks ? T : kRotateBwdBlocks;
+  return up256(static_cast<size_t>(blocks) * 2 * static_cast<size_t>(D) * sizeof(float));
+}
+
+bool rotate_whole_rows(const RotateArgs& a) {
+  const int64_t e = static_cast<int64_t>(size_of(a.dtype));
+  return a.D % 16 == 0 && (a.interleaved != 0 || a.R % 16 == 0) && a.q_raw.stride * e % 16 == 0 && a.k_raw.stride * e % 16 == 0;
+}
+
+int check_rotate(const RotateArgs& a, bool backward) {
+  if (a.T <= 0 || a.Hq <= 0 || a.Hk <= 0 || a.D <= 0) return KDA_ERR_INVALID_ARG;
+  if (a.D > kMaxRotateWidth || a.D % 8 != 0 || a.Hq > kMaxHeads || a.Hk > kMaxHeads || a.T > kMaxTokens) return KDA_ERR_UNSUPPORTED;
+  if (a.R < 0 || a.R > a.D || a.R % 2 != 0 || (a.interleaved != 0 && a.interleaved != 1)) return KDA_ERR_INVALID_ARG;
+  if (!known_type(a.dtype) || (backward && !known_type(a.d_format))) return KDA_ERR_INVALID_ARG;
+  if (!std::isfinite(a.q_scale) || !(a.eps > 0.f) || !std::isfinite(a.eps)) return KDA_ERR_INVALID_ARG;
+  const size_t e = size_of(a.dtype), D = static_cast<size_t>(a.D), q_row = static_cast<size_t>(a.Hq) * D,
+               k_row = static_cast<size_t>(a.Hk) * D, T = static_cast<size_t>(a.T), d = backward ? size_of(a.d_format) : 0;
+  int st = first_error({check_stride(a.q_raw, static_cast<int64_t>(q_row)), check_stride(a.k_raw, static_cast<int64_t>(k_row))});
+  if (st != KDA_OK) return st;
+  if (backward && ((a.q_weight.ptr == nullptr) != (a.dq_weight.ptr == nullptr) ||
+                   (a.k_weight.ptr == nullptr) != (a.dk_weight.ptr == nullptr))) {
+    return KDA_ERR_INVALID_ARG;
+  }
+  st = check_buffers({{a.q_raw.ptr, a.q_raw.bytes, rows_need(a.q_raw, a.T, q_row, e), false},
+                      {a.k_raw.ptr, a.k_raw.bytes, rows_need(a.k_raw, a.T, k_row, e), false},
+                      {a.positions.ptr, a.positions.bytes, a.R > 0 ? T * 4 : 0, a.R == 0},
+                      {a.inv_freq.ptr, a.inv_freq.bytes, static_cast<size_t>(a.R) * 2, a.R == 0},
+                      {a.q_weight.ptr, a.q_weight.bytes, D * 4, true},
+                      {a.k_weight.ptr, a.k_weight.bytes, D * 4, true},
+                      {a.dq.ptr, a.dq.bytes, T * q_row * d, !backward},
+                      {a.dk.ptr, a.dk.bytes, T * k_row * d, !backward},
+                      {a.q.ptr, a.q.bytes, T * q_row * e, false},
+                      {a.k.ptr, a.k.bytes, T * k_row * e, false},
+                      {a.dq_weight.ptr, a.dq_weight.bytes, D * 4, true},
+                      {a.dk_weight.ptr, a.dk_weight.bytes, D * 4, true}});
+  if (st != KDA_OK) return st;
+  const bool sums = backward && (a.dq_weight.ptr != nullptr || a.dk_weight.ptr != nullptr);
+  return sums ? check_workspace(a.workspace, rotate_bwd_workspace(a.T, a.D)) : KDA_OK;
+}
+
 int check_norm(const NormArgs& a, bool backward) {
   if (a.T <= 0 || a.H <= 0 || a.V <= 0) return KDA_ERR_INVALID_ARG;
   if (a.V > kMaxNormWidth || a.H > kMaxHeads || a.T > kMaxTokens) return KDA_ERR_UNSUPPORTED;
@@ -286,6 +348,26 @@ int check_step(const StepArgs& a) {
                       {a.state.ptr, a.state.bytes, pool, false},
                       {a.state_out.ptr, a.state_out.bytes, pool, false},
                       {a.o.ptr, a.o.bytes, n * size_of(a.o_format), false}});
+  return st != KDA_OK ? st : check_pool(a.state, a.state_out, pool);
+}
+
+int check_linear_step(const LinearStepArgs& a) {
+  int st = check_linear_heads(a.H, a.Hq, a.Hk, a.Hv, a.K, a.V);
+  if (st != KDA_OK) return st;
+  st = check_slots(a.B, a.slots, a.num_slots);
+  if (st != KDA_OK) return st;
+  if (!known_type(a.g_dtype) || !known_type(a.o_format)) return KDA_ERR_INVALID_ARG;
+  if (a.g.ptr != nullptr && a.g.stride != 0 && a.g.stride != a.H) return KDA_ERR_INVALID_ARG;
+  const size_t B = static_cast<size_t>(a.B), H = static_cast<size_t>(a.H), K = static_cast<size_t>(a.K),
+               V = static_cast<size_t>(a.V), pool = static_cast<size_t>(a.num_slots) * H * K * V * 4;
+  st = check_buffers({{a.q.ptr, a.q.bytes, B * static_cast<size_t>(a.Hq) * K * 2, false},
+                      {a.k.ptr, a.k.bytes, B * static_cast<size_t>(a.Hk) * K * 2, false},
+                      {a.v.ptr, a.v.bytes, B * static_cast<size_t>(a.Hv) * V * 2, false},
+                      {a.g.ptr, a.g.bytes, (a.g.stride == 0 ? H : B * H) * size_of(a.g_dtype), false},
+                      {a.slots.ptr, a.slots.bytes, B * 4, true},
+                      {a.state.ptr, a.state.bytes, pool, false},
+                      {a.state_out.ptr, a.state_out.bytes, pool, false},
+                      {a.o.ptr, a.o.bytes, B * H * V * size_of(a.o_format), false}});
   return st != KDA_OK ? st : check_pool(a.state, a.state_out, pool);
 }
 

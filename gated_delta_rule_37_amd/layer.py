@@ -194,6 +194,66 @@ def prepare_inputs_backward(q_raw, k_raw, gate_raw, beta_raw, a_log, dt_bias, dq
     return out
 
 
+def _rotate(q_raw, k_raw, positions, inv_freq, q_weight, k_weight, q_scale, eps, interleaved):
+    """The two inputs' shapes, the device and the arguments that both directions
+    of the norms and rotation share."""
+    T, Hq, D = q_raw.shape
+    Hk, dt, dev, f32 = k_raw.shape[1], q_raw.dtype, q_raw.device, torch.float32
+    pairs = 0 if inv_freq is None else inv_freq.shape[0]
+    if pairs and positions is None:
+        raise ValueError("positions: needed with inv_freq")
+    args = [T, Hq, Hk, D, 2 * pairs, _dtype(q_raw, "q_raw"), int(bool(interleaved)),
+            *_rows(q_raw, dt, (T, Hq, D), "q_raw", dev), *_rows(k_raw, dt, (T, Hk, D), "k_raw", dev),
+            *_buf(positions, torch.int32, (T,), "positions", dev), *_buf(inv_freq, f32, (pairs,), "inv_freq", dev),
+            *_buf(q_weight, f32, (D,), "q_weight", dev), *_buf(k_weight, f32, (D,), "k_weight", dev),
+            float(q_scale), float(eps)]
+    return (T, Hq, D), (T, Hk, D), dev, args
+
+
+def qk_norm_rotate(q_raw, k_raw, positions=None, inv_freq=None, q_weight=None, k_weight=None, q_scale=1.0, eps=1e-6,
+                   interleaved=False, out=None, stream=None):
+    """``kda_qk_norm_rotate``: q_raw [T, Hq, D] and k_raw [T, Hk, D] (bf16 or
+    fp32; rows may be slices of a wider projection) divided by their root mean
+    square per head, times their weight [D] (q also times ``q_scale``), then their
+    first 2 len(inv_freq) channels turned by positions (int32 [T]) times
+    ``inv_freq`` (fp32): channels (i, i + len(inv_freq)) are a pair, or
+    (2 i, 2 i + 1) when ``interleaved``.  Without inv_freq nothing turns.  Returns
+    dict(q, k) in the inputs' dtype; ``out`` gives the buffers, which may be
+    dense inputs themselves."""
+    q_shape, k_shape, dev, args = _rotate(q_raw, k_raw, positions, inv_freq, q_weight, k_weight, q_scale, eps,
+                                          interleaved)
+    dt = q_raw.dtype
+    if out is None:
+        out = dict(q=_empty(stream, dev, dt, *q_shape), k=_empty(stream, dev, dt, *k_shape))
+        args += [*_made(out["q"]), *_made(out["k"])]
+    else:
+        args += [*_buf(out["q"], dt, q_shape, "q", dev), *_buf(out["k"], dt, k_shape, "k", dev)]
+    _call("kda_qk_norm_rotate", dev, args, stream)
+    return out
+
+
+def qk_norm_rotate_backward(q_raw, k_raw, positions, inv_freq, q_weight, k_weight, dq, dk, q_scale=1.0, eps=1e-6,
+                            interleaved=False, stream=None):
+    """``kda_qk_norm_rotate_backward``: from the gradients of q and k (bf16 or fp32,
+    both the same) those of the raw inputs (their dtype) and of the weights (fp32,
+    None without them): dict(dq_raw, dk_raw, dq_weight, dk_weight)."""
+    q_shape, k_shape, dev, args = _rotate(q_raw, k_raw, positions, inv_freq, q_weight, k_weight, q_scale, eps,
+                                          interleaved)
+    dt, D, f32 = q_raw.dtype, q_shape[2], torch.float32
+    args += [*_buf(dq, dq.dtype, q_shape, "dq", dev), *_buf(dk, dq.dtype, k_shape, "dk", dev), _dtype(dq, "dq")]
+    out = dict(dq_raw=_empty(stream, dev, dt, *q_shape), dk_raw=_empty(stream, dev, dt, *k_shape),
+               dq_weight=None if q_weight is None else _empty(stream, dev, f32, D),
+               dk_weight=None if k_weight is None else _empty(stream, dev, f32, D))
+    for t in out.values():
+        args += _made(t)
+    weights = q_weight is not None or k_weight is not None
+    size = kda.lib().kda_qk_norm_rotate_backward_workspace_bytes(q_shape[0], D) if weights else 0
+    workspace = _scratch(size, dev, stream)
+    args += _made(workspace)
+    _call("kda_qk_norm_rotate_backward", dev, args, stream)
+    return out
+
+
 def _empty(stream, device, dtype, *shape):
     """Uninitialised memory of the call's stream."""
     if stream is None:
@@ -373,4 +433,32 @@ def step(q, k, v, g, beta, state, slots=None, state_out=None, o=None, o_dtype=to
             *_buf(v, bf, (B, H, V), "v", dev), *_buf(g, bf, (B, H, K), "g", dev), *_buf(beta, bf, (B, H), "beta", dev),
             bound, *slots, n, *pool, *_buf(o, o.dtype, (B, H, V), "o", dev), _dtype(o, "o")]
     _call("kda_step", dev, args, stream)
+    return o
+
+
+def _linear_heads(q, k, v, g):
+    """H, Hq, Hk, Hv, K, V: as many states as the most heads of q, k, v and g."""
+    Hq, K = q.shape[1:]
+    Hk, (Hv, V) = k.shape[1], v.shape[1:]
+    return max(Hq, Hk, Hv, g.shape[-1]), Hq, Hk, Hv, K, V
+
+
+def linear_step(q, k, v, g, state, slots=None, state_out=None, o=None, o_dtype=torch.bfloat16, stream=None):
+    """``kda_linear_step``: the next token of B sequences, q [B, Hq, K], k [B, Hk, K]
+    and v [B, Hv, V] bf16, g [B, H] or [H] (fp32 or bf16), whose states lie in the
+    slots ``slots`` (int32 [B], default: slot b) of ``state`` [num_slots, H, K, V]
+    fp32, updated in place unless ``state_out`` is given.  A slot outside the pool
+    marks an unused row.  Returns o [B, H, V] in ``o_dtype`` (``o``: the buffer to
+    write)."""
+    B = q.shape[0]
+    H, Hq, Hk, Hv, K, V = _linear_heads(q, k, v, g)
+    bf, dev = torch.bfloat16, q.device
+    if o is None:
+        o = _empty(stream, dev, o_dtype, B, H, V)
+    n, slots, pool = _pool(B, state, slots, state_out, (H, K, V), dev)
+    fixed = g.dim() == 1
+    args = [B, H, Hq, Hk, Hv, K, V, *_buf(q, bf, (B, Hq, K), "q", dev), *_buf(k, bf, (B, Hk, K), "k", dev),
+            *_buf(v, bf, (B, Hv, V), "v", dev), *_buf(g, g.dtype, (H,) if fixed else (B, H), "g", dev),
+            0 if fixed else H, _dtype(g, "g"), *slots, n, *pool, *_buf(o, o.dtype, (B, H, V), "o", dev), _dtype(o, "o")]
+    _call("kda_linear_step", dev, args, stream)
     return o

@@ -519,6 +519,58 @@ int kda_prepare_inputs_backward(int32_t T, int32_t H, int32_t K, int32_t dtype,
 size_t kda_prepare_inputs_backward_workspace_bytes(int32_t T, int32_t H, int32_t K);
 
 /*
+ * kda_qk_norm_rotate -- the norms of queries and keys for each head and their
+ * rotation by position, in one pass.  Per token t and head, over its D channels
+ * c of x = q_raw or k_raw:
+ *     n = weight * x / sqrt(mean_c x^2 + eps),  q also times q_scale
+ * then the first R channels turn in pairs (a, b) by the angle
+ * positions[t] * inv_freq[i], i < R / 2:
+ *     (a, b) -> (a cos - b sin, a sin + b cos)
+ * where pair i is channels (i, i + R / 2), or (2 i, 2 i + 1) when interleaved;
+ * the channels from R on stay as the norm left them.
+ *   q_raw          [T, Hq, D] dtype, k_raw [T, Hk, D] dtype, each with its own
+ *                  token stride; D a multiple of 8, at most 256
+ *                  (KDA_ERR_UNSUPPORTED)
+ *   R              even, 0 <= R <= D; interleaved 0 or 1
+ *   positions      [T] int32, any values; inv_freq [R / 2].  Both may be NULL
+ *                  where R is 0.  Angles are taken in FP64: to 1e-9 at
+ *                  positions up to 2^23, whatever the frequency up to 1.
+ *   q_weight, k_weight  [D] or NULL (one)
+ *   q, k           dtype, dense; each may be its dense raw input itself, in
+ *                  place
+ * mean_c x^2 has to stay finite in FP32; a row of zeros stays zero.
+ */
+int kda_qk_norm_rotate(int32_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t R, int32_t dtype, int32_t interleaved,
+                       const void* q_raw, size_t q_raw_bytes, int64_t q_raw_stride,
+                       const void* k_raw, size_t k_raw_bytes, int64_t k_raw_stride,
+                       const int32_t* positions, size_t positions_bytes,
+                       const float* inv_freq, size_t inv_freq_bytes,
+                       const float* q_weight, size_t q_weight_bytes, const float* k_weight, size_t k_weight_bytes,
+                       float q_scale, float eps, void* q, size_t q_bytes, void* k, size_t k_bytes,
+                       hipStream_t stream);
+
+/*
+ * kda_qk_norm_rotate_backward -- gradients of kda_qk_norm_rotate for the
+ * cotangents dq [T, Hq, D] and dk [T, Hk, D], dense, in d_format (kda_dtype):
+ *   dq_raw, dk_raw          [T, heads, D] dtype, dense
+ *   dq_weight, dk_weight    [D]; NULL exactly when the weight is NULL
+ * Workspace: kda_qk_norm_rotate_backward_workspace_bytes(T, D) bytes, not read
+ * where both weights are NULL.
+ */
+int kda_qk_norm_rotate_backward(int32_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t R, int32_t dtype,
+                                int32_t interleaved, const void* q_raw, size_t q_raw_bytes, int64_t q_raw_stride,
+                                const void* k_raw, size_t k_raw_bytes, int64_t k_raw_stride,
+                                const int32_t* positions, size_t positions_bytes,
+                                const float* inv_freq, size_t inv_freq_bytes,
+                                const float* q_weight, size_t q_weight_bytes,
+                                const float* k_weight, size_t k_weight_bytes, float q_scale, float eps,
+                                const void* dq, size_t dq_bytes, const void* dk, size_t dk_bytes, int32_t d_format,
+                                void* dq_raw, size_t dq_raw_bytes, void* dk_raw, size_t dk_raw_bytes,
+                                float* dq_weight, size_t dq_weight_bytes, float* dk_weight, size_t dk_weight_bytes,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t kda_qk_norm_rotate_backward_workspace_bytes(int32_t T, int32_t D);
+
+/*
  * kda_output_norm -- the norm after the recurrence with its gate and residual
  * scale, per (token, head) row over V channels (any V up to 8192; H = 1 gives
  * a norm over whole rows):
@@ -608,7 +660,8 @@ int kda_scan_backward(const kda_plan* plan, const int32_t* plan_dev, size_t plan
 size_t kda_scan_workspace_bytes(const kda_plan* plan, int32_t D);
 
 /*
- * Single tokens over a pool of states (kda_scan_step, kda_step).  Row b of the
+ * Single tokens over a pool of states (kda_scan_step, kda_step,
+ * kda_linear_step).  Row b of the
  * batch is the next token of the sequence whose state lies in slot slots[b] of
  * the pool; slots NULL means slot b.
  *   - A slot outside [0, num_slots) marks an unused row: its output row and
@@ -649,6 +702,26 @@ int kda_step(int32_t B, int32_t H, int32_t K, int32_t V, int32_t head_begin, int
              const int32_t* slots, size_t slots_bytes, int32_t num_slots,
              const float* state, size_t state_bytes, float* state_out, size_t state_out_bytes,
              void* o, size_t o_bytes, int32_t o_format, hipStream_t stream);
+
+/*
+ * kda_linear_step -- single tokens of linear attention with a decay for each
+ * head, over a pool of states as kda_step's:
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t
+ *   q        [B, Hq, K], k [B, Hk, K], v [B, Hv, V] bf16, dense; H is a
+ *            multiple of Hq, Hk and Hv (KDA_ERR_INVALID_ARG), and head h reads
+ *            q head h / (H / Hq), k head h / (H / Hk), v head h / (H / Hv)
+ *   K, V     multiples of 8, at most 128 (KDA_ERR_UNSUPPORTED)
+ *   g        g_dtype, [B, H] with g_stride H, or [H] for every row with
+ *            g_stride 0; g <= 0, finite or -inf (exp(-inf) = 0)
+ *   state, state_out  [num_slots, H, K, V] FP32
+ *   o        [B, H, V] in o_format
+ */
+int kda_linear_step(int32_t B, int32_t H, int32_t Hq, int32_t Hk, int32_t Hv, int32_t K, int32_t V,
+                    const uint16_t* q, size_t q_bytes, const uint16_t* k, size_t k_bytes,
+                    const uint16_t* v, size_t v_bytes, const void* g, size_t g_bytes, int64_t g_stride,
+                    int32_t g_dtype, const int32_t* slots, size_t slots_bytes, int32_t num_slots,
+                    const float* state, size_t state_bytes, float* state_out, size_t state_out_bytes,
+                    void* o, size_t o_bytes, int32_t o_format, hipStream_t stream);
 
 /* Human-readable name of a kda_status value. */
 const char* kda_status_string(int status);
