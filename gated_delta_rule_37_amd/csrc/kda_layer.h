@@ -81,6 +81,17 @@ struct LinearStepArgs {
   Dst state_out, o;
 };
 
+struct LinearArgs {
+  const kda_plan* plan;
+  Rows plan_dev;
+  int32_t H, Hq, Hk, Hv, K, V, g_dtype, o_format;   // backward: o_format is the gradients'
+  Rows q, k, v, g;                                  // g.stride 0: one g [H]
+  Rows initial_state;
+  Dst o, final_state, workspace;                    // forward
+  Rows d_o, d_final;                                // backward
+  Dst dq, dk, dv, dg, d_initial_state;
+};
+
 // Partial sums over tokens (the backward passes of the row-wise operators).
 // A group of lanes takes rows (t, h) of one head: rows r, r + P H, r + 2 P H,
 // ... for the P "lanes" of tokens; every group leaves one partial row.
@@ -146,8 +157,25 @@ RotateGrid rotate_grid(const RotateArgs& a, bool backward);
 size_t rotate_bwd_workspace(int32_t T, int32_t D);
 bool rotate_whole_rows(const RotateArgs& a);   // pairs of whole, aligned 16-byte vectors
 
+// Linear attention's workspace (byte offsets): the pieces' states and decays
+// where a sequence is cut, [P][H][K][V] and [P][H] FP32.
+struct LinearLayout {
+  size_t states, decays, total;
+};
+LinearLayout linear_layout(const kda_plan* plan, int32_t H, int32_t K, int32_t V);
+// Backward: also the states' cotangents, the gates' gradient [T][H], what each
+// chunk's queries take from before it [ceil(T / 64) + F][H] (chunk c of fragment f
+// in slot floor(begin_f / 64) + f + c; then the 64 ranges' sums of a shared
+// gate), what passes each fragment's end [F][H], and one gradient of every head
+// [T][H][max(K, V)] where heads are shared.
+struct LinearBwdLayout {
+  size_t states, cotangents, decays, gates, rho, anchor, heads, total;
+};
+LinearBwdLayout linear_bwd_layout(const LinearArgs& a);
+
 int check_prepare(const PrepareArgs& a, bool backward);
 int check_rotate(const RotateArgs& a, bool backward);
+int check_linear(const LinearArgs& a, bool backward);
 int check_linear_step(const LinearStepArgs& a);
 int check_norm(const NormArgs& a, bool backward);
 int check_scan(const ScanArgs& a, bool backward);
@@ -166,6 +194,8 @@ int launch_prepare(const PrepareArgs& a, hipStream_t stream);
 int launch_prepare_backward(const PrepareArgs& a, hipStream_t stream);
 int launch_rotate(const RotateArgs& a, hipStream_t stream);
 int launch_rotate_backward(const RotateArgs& a, hipStream_t stream);
+int launch_linear(const LinearArgs& a, hipStream_t stream);
+int launch_linear_backward(const LinearArgs& a, hipStream_t stream);
 int launch_linear_step(const LinearStepArgs& a, hipStream_t stream);
 int launch_norm(const NormArgs& a, hipStream_t stream);
 int launch_norm_backward(const NormArgs& a, hipStream_t stream);

@@ -325,6 +325,93 @@ int kda_step(int32_t B, int32_t H, int32_t K, int32_t V, int32_t head_begin, int
   return st != KDA_OK ? st : kda::launch_step(a, stream);
 }
 
+int kda_linear_forward(const kda_plan* plan, const int32_t* plan_dev, size_t plan_dev_bytes, int32_t H, int32_t Hq,
+                       int32_t Hk, int32_t Hv, int32_t K, int32_t V, const uint16_t* q, size_t q_bytes, int64_t q_stride,
+                       const uint16_t* k, size_t k_bytes, int64_t k_stride, const uint16_t* v, size_t v_bytes, int64_t v_stride,
+                       const void* g, size_t g_bytes, int64_t g_stride, int32_t g_dtype,
+                       const float* initial_state, size_t initial_state_bytes,
+                       void* o, size_t o_bytes, int32_t o_format, float* final_state, size_t final_state_bytes,
+                       void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  kda::LinearArgs a{};
+  a.plan = plan;
+  a.plan_dev = {plan_dev, plan_dev_bytes, 0};
+  a.H = H;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.Hv = Hv;
+  a.K = K;
+  a.V = V;
+  a.g_dtype = g_dtype;
+  a.q = {q, q_bytes, q_stride};
+  a.k = {k, k_bytes, k_stride};
+  a.v = {v, v_bytes, v_stride};
+  a.g = {g, g_bytes, g_stride};
+  a.initial_state = {initial_state, initial_state_bytes, 0};
+  a.o_format = o_format;
+  a.o = {o, o_bytes};
+  a.final_state = {final_state, final_state_bytes};
+  a.workspace = {workspace, workspace_bytes};
+  const int st = kda::check_linear(a, false);
+  return st != KDA_OK ? st : kda::launch_linear(a, stream);
+}
+
+int kda_linear_backward(const kda_plan* plan, const int32_t* plan_dev, size_t plan_dev_bytes, int32_t H, int32_t Hq,
+                        int32_t Hk, int32_t Hv, int32_t K, int32_t V, const uint16_t* q, size_t q_bytes, int64_t q_stride,
+                        const uint16_t* k, size_t k_bytes, int64_t k_stride, const uint16_t* v, size_t v_bytes, int64_t v_stride,
+                        const void* g, size_t g_bytes, int64_t g_stride, int32_t g_dtype,
+                        const float* initial_state, size_t initial_state_bytes,
+                        const uint16_t* d_o, size_t d_o_bytes, const float* d_final, size_t d_final_bytes,
+                        void* dq, size_t dq_bytes, void* dk, size_t dk_bytes, void* dv, size_t dv_bytes,
+                        int32_t grad_format, void* dg, size_t dg_bytes,
+                        float* d_initial_state, size_t d_initial_state_bytes,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  kda::LinearArgs a{};
+  a.plan = plan;
+  a.plan_dev = {plan_dev, plan_dev_bytes, 0};
+  a.H = H;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.Hv = Hv;
+  a.K = K;
+  a.V = V;
+  a.g_dtype = g_dtype;
+  a.q = {q, q_bytes, q_stride};
+  a.k = {k, k_bytes, k_stride};
+  a.v = {v, v_bytes, v_stride};
+  a.g = {g, g_bytes, g_stride};
+  a.initial_state = {initial_state, initial_state_bytes, 0};
+  a.o_format = grad_format;
+  a.d_o = {d_o, d_o_bytes, 0};
+  a.d_final = {d_final, d_final_bytes, 0};
+  a.dq = {dq, dq_bytes};
+  a.dk = {dk, dk_bytes};
+  a.dv = {dv, dv_bytes};
+  a.dg = {dg, dg_bytes};
+  a.d_initial_state = {d_initial_state, d_initial_state_bytes};
+  a.workspace = {workspace, workspace_bytes};
+  const int st = kda::check_linear(a, true);
+  return st != KDA_OK ? st : kda::launch_linear_backward(a, stream);
+}
+
+size_t kda_linear_workspace_bytes(const kda_plan* plan, int32_t H, int32_t K, int32_t V) {
+  return plan == nullptr || H <= 0 || H > 65535 || K <= 0 || K > 128 || V <= 0 || V > 128
+             ? 0 : kda::linear_layout(plan, H, K, V).total;
+}
+
+size_t kda_linear_backward_workspace_bytes(const kda_plan* plan, int32_t H, int32_t Hq, int32_t Hk, int32_t Hv, int32_t K,
+                                           int32_t V) {
+  if (plan == nullptr || H <= 0 || H > 65535 || K <= 0 || K > 128 || V <= 0 || V > 128) return 0;
+  kda::LinearArgs a{};
+  a.plan = plan;
+  a.H = H;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.Hv = Hv;
+  a.K = K;
+  a.V = V;
+  return kda::linear_bwd_layout(a).total;
+}
+
 int kda_linear_step(int32_t B, int32_t H, int32_t Hq, int32_t Hk, int32_t Hv, int32_t K, int32_t V,
                     const uint16_t* q, size_t q_bytes, const uint16_t* k, size_t k_bytes,
                     const uint16_t* v, size_t v_bytes, const void* g, size_t g_bytes, int64_t g_stride,

@@ -351,6 +351,68 @@ int check_step(const StepArgs& a) {
   return st != KDA_OK ? st : check_pool(a.state, a.state_out, pool);
 }
 
+LinearLayout linear_layout(const kda_plan* plan, int32_t H, int32_t K, int32_t V) {
+  LinearLayout L{};
+  if (plan->F == plan->N) return L;   // no sequence is cut
+  const size_t cells = static_cast<size_t>(plan->P) * static_cast<size_t>(H);
+  L.states = 0;
+  L.decays = up256(cells * static_cast<size_t>(K) * static_cast<size_t>(V) * sizeof(float));
+  L.total = L.decays + up256(cells * sizeof(float));
+  return L;
+}
+
+LinearBwdLayout linear_bwd_layout(const LinearArgs& a) {
+  const LinearLayout F = linear_layout(a.plan, a.H, a.K, a.V);
+  const size_t H = static_cast<size_t>(a.H), T = static_cast<size_t>(a.plan->T), frags = static_cast<size_t>(a.plan->F),
+               slots = (T + 63) / 64 + frags, width = static_cast<size_t>(a.K > a.V ? a.K : a.V);
+  const bool shared = a.Hq != a.H || a.Hk != a.H || a.Hv != a.H;
+  LinearBwdLayout L{};
+  L.states = 0;
+  L.cotangents = F.decays;
+  L.decays = 2 * F.decays;
+  L.gates = F.total + F.decays;
+  L.rho = L.gates + up256(T * H * sizeof(float));
+  L.anchor = L.rho + up256((slots > 64 ? slots : 64) * H * sizeof(float));
+  L.heads = L.anchor + up256(frags * H * sizeof(float));
+  L.total = L.heads + (shared ? up256(T * H * width * sizeof(float)) : 0);
+  return L;
+}
+
+int check_linear(const LinearArgs& a, bool backward) {
+  if (a.plan == nullptr || a.plan_dev.ptr == nullptr) return KDA_ERR_INVALID_ARG;
+  int st = check_linear_heads(a.H, a.Hq, a.Hk, a.Hv, a.K, a.V);
+  if (st != KDA_OK) return st;
+  if (!known_type(a.g_dtype) || !known_type(a.o_format)) return KDA_ERR_INVALID_ARG;
+  const int32_t T = a.plan->T;
+  const size_t H = static_cast<size_t>(a.H), K = static_cast<size_t>(a.K), V = static_cast<size_t>(a.V), tokens = static_cast<size_t>(T),
+               q_row = static_cast<size_t>(a.Hq) * K, k_row = static_cast<size_t>(a.Hk) * K, v_row = static_cast<size_t>(a.Hv) * V,
+               state = static_cast<size_t>(a.plan->N) * H * K * V * 4, e = size_of(a.o_format), eg = size_of(a.g_dtype);
+  const bool fixed = a.g.stride == 0;
+  st = first_error({check_stride(a.q, static_cast<int64_t>(q_row)), check_stride(a.k, static_cast<int64_t>(k_row)),
+                    check_stride(a.v, static_cast<int64_t>(v_row)), fixed ? KDA_OK : check_stride(a.g, a.H)});
+  if (st != KDA_OK) return st;
+  st = check_buffers({{a.plan_dev.ptr, a.plan_dev.bytes, a.plan->blob.size() * sizeof(int32_t), false},
+                      {a.q.ptr, a.q.bytes, rows_need(a.q, T, q_row, 2), false},
+                      {a.k.ptr, a.k.bytes, rows_need(a.k, T, k_row, 2), false},
+                      {a.v.ptr, a.v.bytes, rows_need(a.v, T, v_row, 2), false},
+                      {a.g.ptr, a.g.bytes, fixed ? H * eg : rows_need(a.g, T, H, eg), false},
+                      {a.initial_state.ptr, a.initial_state.bytes, state, true},
+                      {a.o.ptr, a.o.bytes, tokens * H * V * e, backward},
+                      {a.final_state.ptr, a.final_state.bytes, state, backward},
+                      {a.d_o.ptr, a.d_o.bytes, tokens * H * V * 2, !backward},
+                      {a.d_final.ptr, a.d_final.bytes, state, true},
+                      {a.dq.ptr, a.dq.bytes, tokens * q_row * e, !backward},
+                      {a.dk.ptr, a.dk.bytes, tokens * k_row * e, !backward},
+                      {a.dv.ptr, a.dv.bytes, tokens * v_row * e, !backward},
+                      {a.dg.ptr, a.dg.bytes, (fixed ? H : tokens * H) * eg, !backward},
+                      {a.d_initial_state.ptr, a.d_initial_state.bytes, state, true}});
+  if (st != KDA_OK) return st;
+  for (const Rows* r : {&a.q, &a.k, &a.v}) {
+    if (r->stride % 8 != 0) return KDA_ERR_MISALIGNED;
+  }
+  return check_workspace(a.workspace, backward ? linear_bwd_layout(a).total : linear_layout(a.plan, a.H, a.K, a.V).total);
+}
+
 int check_linear_step(const LinearStepArgs& a) {
   int st = check_linear_heads(a.H, a.Hq, a.Hk, a.Hv, a.K, a.V);
   if (st != KDA_OK) return st;

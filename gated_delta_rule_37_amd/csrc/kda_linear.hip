@@ -1,0 +1,232 @@
+// Linear attention with a decay for each head over packed sequences
+// (kda_linear_forward) and its gradients (kda_linear_backward): the passes of
+// kda_linear_pass.h, the scan of the pieces' states between them, and the sums
+// that shared heads and a shared gate need.
+//
+// A plan's pieces run in parallel.  Where a piece goes on within its sequence, its
+// state comes from a first pass over the pieces' keys and values alone and an
+// ordered scan: state_{r+1} = e^{G_r} state_r + update_r.
+#include "kda_linear_pass.h"
+
+#include "kda.h"
+
+namespace kda {
+
+int launch_linear_pass(void (*kernel)(LinearParams), const LinearParams& p, int32_t fragments, hipStream_t stream) {
+  const int32_t threads = p.VW > 64 ? 256 : 128;
+  const int64_t blocks = static_cast<int64_t>(fragments) * p.H;
+  if (blocks * threads > 2147483647LL) return KDA_ERR_UNSUPPORTED;
+  (void)hipGetLastError();
+  hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(blocks)), dim3(threads), 0, stream, p);
+  return finish_launch();
+}
+
+namespace {
+
+// The state before every piece that goes on within its sequence (reversed: the
+// cotangent after every piece whose sequence goes on), in place of the pieces'
+// own updates.  A thread has four elements of one head's state.
+template <bool REV>
+__global__ __launch_bounds__(kRowThreads) void linear_scan_kernel(const int32_t* plan, BlobLayout L, int32_t P, int32_t H,
+                                                                  int32_t quads, const float* decays, float* states) {
+  const int32_t i = static_cast<int32_t>(blockIdx.x) * kRowThreads + static_cast<int32_t>(threadIdx.x);
+  const int32_t head = static_cast<int32_t>(blockIdx.y);
+  if (i >= quads) return;
+  float* own = states + (static_cast<int64_t>(head) * quads + i) * 4;
+  const int64_t step = static_cast<int64_t>(H) * quads * 4;
+  f32x4 state = zero4();
+  for (int32_t n = 0; n < P; ++n) {
+    const int32_t r = REV ? P - 1 - n : n;
+    const bool before = plan[L.seg_carry_in + r] != 0, after = r + 1 < P && plan[L.seg_carry_in + r + 1] != 0;
+    const bool through = before && after && plan[L.seg_transition_live + r] != 0;
+    float* at = own + r * step;
+    const bool has = REV ? before : after;   // the piece's update was made
+    f32x4 update = zero4();
+    if (has) update = ld4(at);
+    if (REV ? after : before) st4(at, state);
+    state = has ? (through ? decays[static_cast<int64_t>(r) * H + head] * state + update : update) : zero4();
+  }
+}
+
+// Sums of `share` neighbouring heads' rows [T, H, W] FP32 into [T, H / share, W].
+__global__ __launch_bounds__(kRowThreads) void linear_heads_kernel(const float* in, int32_t share, int32_t W, int64_t quads,
+                                                                   void* out, int32_t out_fp32) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
+  if (i >= quads) return;
+  const int64_t row = i * 4 / W, ch = i * 4 - row * W;
+  f32x4 sum = ld4(in + row * share * W + ch);
+  for (int32_t m = 1; m < share; ++m) sum += ld4(in + (row * share + m) * W + ch);
+  if (out_fp32) {
+    st4(static_cast<float*>(out) + i * 4, sum);
+  } else {
+    const u32x2 v = {pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + i * 4) = v;
+  }
+}
+
+// Column sums of [rows][H] in FP32: a workgroup a head's range of rows, then the
+// ranges' sums in order.
+constexpr int kGateBlocks = 64;
+__global__ __launch_bounds__(1024) void linear_gate_kernel(const float* in, int32_t rows, int32_t H, float* part) {
+  __shared__ float sums[16][64];
+  const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = static_cast<int32_t>(blockIdx.x) * 64 + lane;
+  const int32_t per = (rows + kGateBlocks - 1) / kGateBlocks, first = static_cast<int32_t>(blockIdx.y) * per;
+  const int32_t n = min(per, rows - first);
+  float sum = col < H && n > 0 ? column_sum(in + static_cast<int64_t>(first) * H + col, H, wave, n) : 0.f;
+  sums[wave][lane] = sum;
+  __syncthreads();
+  if (wave == 0 && col < H) {
+    for (int i = 1; i < 16; ++i) sum += sums[i][lane];
+    part[static_cast<int64_t>(blockIdx.y) * H + col] = sum;
+  }
+}
+__global__ __launch_bounds__(kRowThreads) void linear_gate_sum_kernel(const float* part, int32_t H, void* dg, int32_t bf16_out) {
+  const int32_t h = static_cast<int32_t>(blockIdx.x) * kRowThreads + static_cast<int32_t>(threadIdx.x);
+  if (h >= H) return;
+  float sum = 0.f;
+  for (int i = 0; i < kGateBlocks; ++i) sum += part[static_cast<int64_t>(i) * H + h];
+  if (bf16_out) {
+    static_cast<uint16_t*>(dg)[h] = static_cast<uint16_t>(pack_bf16(sum, 0.f));
+  } else {
+    static_cast<float*>(dg)[h] = sum;
+  }
+}
+
+Tokens tokens_of(const Rows& r, int32_t H, int32_t heads, int32_t width) {
+  return {static_cast<const uint16_t*>(r.ptr), r.stride, H / heads, width};
+}
+
+LinearParams pass_of(const LinearArgs& a, int32_t KW, int32_t VW) {
+  LinearParams p{};
+  p.plan = static_cast<const int32_t*>(a.plan_dev.ptr);
+  p.L = a.plan->layout;
+  p.H = a.H;
+  p.KW = KW;
+  p.VW = VW;
+  p.g = a.g.ptr;
+  p.g_stride = a.g.stride;
+  p.g_bf16 = a.g_dtype == KDA_BF16 ? 1 : 0;
+  return p;
+}
+
+template <bool REV>
+int launch_scan_states(const LinearArgs& a, const float* decays, float* states, hipStream_t stream) {
+  const int32_t quads = a.K * a.V / 4;
+  hipLaunchKernelGGL(linear_scan_kernel<REV>, dim3((quads + kRowThreads - 1) / kRowThreads, a.H), dim3(kRowThreads), 0, stream,
+                     static_cast<const int32_t*>(a.plan_dev.ptr), a.plan->layout, a.plan->P, a.H, quads, decays, states);
+  return finish_launch();
+}
+
+// The states before the pieces, in ws.
+int launch_piece_states(const LinearArgs& a, float* states, float* decays, hipStream_t stream) {
+  LinearParams p = pass_of(a, a.K, a.V);
+  p.y = tokens_of(a.k, a.H, a.Hk, a.K);
+  p.z = tokens_of(a.v, a.H, a.Hv, a.V);
+  p.seq_state = static_cast<const float*>(a.initial_state.ptr);
+  p.piece_out = states;
+  p.decay_out = decays;
+  const int st = launch_linear_pass(linear_kernel_of<2, 2, false, kSummary>(a.K, a.V), p, a.plan->F, stream);
+  return st != KDA_OK ? st : launch_scan_states<false>(a, decays, states, stream);
+}
+
+}  // namespace
+
+int launch_linear(const LinearArgs& a, hipStream_t stream) {
+  const LinearLayout L = linear_layout(a.plan, a.H, a.K, a.V);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace.ptr);
+  float *states = reinterpret_cast<float*>(ws + L.states), *decays = reinterpret_cast<float*>(ws + L.decays);
+  if (a.plan->F > a.plan->N) {
+    const int st = launch_piece_states(a, states, decays, stream);
+    if (st != KDA_OK) return st;
+  }
+  LinearParams p = pass_of(a, a.K, a.V);
+  p.x = tokens_of(a.q, a.H, a.Hq, a.K);
+  p.y = tokens_of(a.k, a.H, a.Hk, a.K);
+  p.z = tokens_of(a.v, a.H, a.Hv, a.V);
+  p.seq_state = static_cast<const float*>(a.initial_state.ptr);
+  p.piece_state = states;
+  p.seq_out = static_cast<float*>(a.final_state.ptr);
+  p.o = a.o.ptr;
+  p.o_fp32 = a.o_format == KDA_FP32 ? 1 : 0;
+  return launch_linear_pass(p.o_fp32 ? linear_kernel_of<3, 3, false, kOutput>(a.K, a.V) : linear_kernel_of<2, 2, false, kOutput>(a.K, a.V),
+                            p, a.plan->F, stream);
+}
+
+int launch_linear_backward(const LinearArgs& a, hipStream_t stream) {
+  const LinearBwdLayout L = linear_bwd_layout(a);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace.ptr);
+  auto at = [ws](size_t offset) { return reinterpret_cast<float*>(ws + offset); };
+  const bool cut = a.plan->F > a.plan->N, fp32 = a.o_format == KDA_FP32, fixed = a.g.stride == 0;
+  const Rows d_o = {a.d_o.ptr, a.d_o.bytes, static_cast<int64_t>(a.H) * a.V};
+  const Tokens q = tokens_of(a.q, a.H, a.Hq, a.K), k = tokens_of(a.k, a.H, a.Hk, a.K), v = tokens_of(a.v, a.H, a.Hv, a.V),
+               d = tokens_of(d_o, a.H, a.H, a.V);
+  const float *h0 = static_cast<const float*>(a.initial_state.ptr), *d_final = static_cast<const float*>(a.d_final.ptr);
+  if (cut) {
+    int st = launch_piece_states(a, at(L.states), at(L.decays), stream);
+    if (st != KDA_OK) return st;
+    LinearParams p = pass_of(a, a.K, a.V);
+    p.y = q;
+    p.z = d;
+    p.seq_state = d_final;
+    p.piece_out = at(L.cotangents);
+    st = launch_linear_pass(linear_kernel_of<2, 2, true, kSummary>(a.K, a.V), p, a.plan->F, stream);
+    if (st == KDA_OK) st = launch_scan_states<true>(a, at(L.decays), at(L.cotangents), stream);
+    if (st != KDA_OK) return st;
+  }
+  // each of the gradients: heads that share a row are added in a launch of their own
+  const auto pass = [&](LinearParams& p, int32_t heads, const Dst& out, void (*kernel)(LinearParams)) -> int {
+    const bool shared = heads != a.H;
+    p.o = shared ? static_cast<void*>(at(L.heads)) : out.ptr;
+    p.o_fp32 = shared || fp32 ? 1 : 0;
+    const int st = launch_linear_pass(kernel, p, a.plan->F, stream);
+    if (st != KDA_OK || !shared) return st;
+    const int64_t quads = static_cast<int64_t>(a.plan->T) * heads * p.VW / 4;
+    if (quads > 2147483647LL - kRowThreads) return KDA_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL(linear_heads_kernel, dim3(static_cast<uint32_t>((quads + kRowThreads - 1) / kRowThreads)),
+                       dim3(kRowThreads), 0, stream, at(L.heads), a.H / heads, p.VW, quads, out.ptr, fp32 ? 1 : 0);
+    return finish_launch();
+  };
+  LinearParams p = pass_of(a, a.V, a.K);
+  p.transposed = 1;
+  p.x = d;
+  p.y = v;
+  p.z = k;
+  p.e = q;
+  p.seq_state = h0;
+  p.piece_state = at(L.states);
+  p.dg_part = at(L.gates);
+  p.rho = at(L.rho);
+  p.anchor = at(L.anchor);
+  p.end_seq = d_final;
+  p.end_piece = at(L.cotangents);
+  int st = pass(p, a.Hq, a.dq, linear_query_kernel(a.V, a.K, fp32));
+  if (st != KDA_OK) return st;
+  p.x = v;
+  p.y = d;
+  p.z = q;
+  p.e = k;
+  p.seq_state = d_final;
+  p.piece_state = at(L.cotangents);
+  p.dg = fixed ? at(L.gates) : a.dg.ptr;
+  p.dg_bf16 = !fixed && a.g_dtype == KDA_BF16 ? 1 : 0;
+  st = pass(p, a.Hk, a.dk, linear_key_kernel(a.V, a.K, fp32));
+  if (st != KDA_OK) return st;
+  if (fixed) {
+    hipLaunchKernelGGL(linear_gate_kernel, dim3((a.H + 63) / 64, kGateBlocks), dim3(1024), 0, stream, at(L.gates), a.plan->T, a.H,
+                       at(L.rho));
+    hipLaunchKernelGGL(linear_gate_sum_kernel, dim3((a.H + kRowThreads - 1) / kRowThreads), dim3(kRowThreads), 0, stream, at(L.rho),
+                       a.H, a.dg.ptr, a.g_dtype == KDA_BF16 ? 1 : 0);
+    st = finish_launch();
+    if (st != KDA_OK) return st;
+  }
+  p = pass_of(a, a.K, a.V);
+  p.x = k;
+  p.y = q;
+  p.z = d;
+  p.seq_state = d_final;
+  p.piece_state = at(L.cotangents);
+  p.seq_out = static_cast<float*>(a.d_initial_state.ptr);
+  return pass(p, a.Hv, a.dv, linear_value_kernel(a.K, a.V, fp32));
+}
+
+}  // namespace kda

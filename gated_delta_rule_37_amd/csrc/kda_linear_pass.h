@@ -1,0 +1,592 @@
+// One pass of linear attention with a decay for each head over a fragment's
+// 64-token chunks, on the bf16 matrix cores.
+//
+// With queries x, keys y, values z, a state S [KD, VD] (rows: channels of y) and
+// the prefix sums G of the chunk's gates, a forward pass has per chunk
+//     out_i = sum_{j <= i} e^{G_i - G_j} (x_i . y_j) z_j + e^{G_i} S^T x_i
+//     S    <- e^{G_C} S + sum_j e^{G_C - G_j} y_j z_j^T
+// and a reversed one, which walks the chunks from the last to the first,
+//     out_j = sum_{i >= j} e^{G_i - G_j} (x_j . y_i) z_i + e^{G_C - G_j} S^T x_j
+//     S    <- e^{G_C} S + sum_i e^{G_i} y_i z_i^T.
+// The operator is the forward pass of (q, k, v); of its gradients, dq is the
+// forward pass of (do, v, k) with the state transposed, dk the reversed pass of
+// (v, do, q) transposed, dv the reversed pass of (k, q, do).
+//
+// A workgroup is one fragment of one head, VD / 32 waves.  A wave holds S's
+// columns 32 w .. 32 w + 31 in FP32 accumulators; x, y, z of the chunk lie in LDS
+// in bf16, exactly as they came.  Whatever is not exact in bf16 is split into bf16
+// parts (8 bits each): two of them leave 2^-16, three 2^-24 of a factor.
+//   * P = (x y^T) o decay: 16 x 16 tiles, a wave owns whole rows of tiles; its
+//     parts go through LDS, as they are every wave's operand.
+//   * out^T = S^T x^T + z^T P^T: transposed, so that a lane has one token and four
+//     neighbouring channels.  S's accumulators are the matrix core's operand as
+//     they are (their rows are its k slots; x is stored so that 16 bytes of LDS
+//     hold a lane's k slots), split in registers.
+//   * S's update: z, read transposed, times its weights, split in registers; y
+//     read transposed.
+// Decays: a gate of a token enters with at least -160 in units of 2 (2^-160 is 0 in
+// FP32), prefix sums are taken in FP64 and kept as a multiple of 2^-9 and the
+// rest, so that the difference of two of them is exact however large they are.
+#ifndef KDA_LINEAR_PASS_H_
+#define KDA_LINEAR_PASS_H_
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "kda_layer.h"
+#include "kda_layer_device.h"
+
+namespace kda {
+
+// The next token's row is `stride` elements on; head h reads row head h / share,
+// `width` elements.
+struct Tokens {
+  const uint16_t* p;
+  int64_t stride;
+  int32_t share, width;
+};
+
+struct LinearParams {
+  const int32_t* plan;
+  BlobLayout L;
+  int32_t H, KW, VW;            // heads, widths in use (KW <= KD, VW <= VD)
+  Tokens x, y, z, e;            // e: q (kQuery) or k (kKey)
+  const void* g;
+  int64_t g_stride;
+  int32_t g_bf16;
+  int32_t transposed;           // states in memory are [VW][KW]
+  const float* seq_state;       // where a sequence begins (reversed: ends), or null
+  const float* piece_state;     // where a piece goes on: its own state before (reversed: after) it
+  float* seq_out;               // at the other end, or null
+  float *piece_out, *decay_out; // kSummary
+  void* o;                      // [T, H, VW]
+  int32_t o_fp32;
+  // gradient of the gates
+  float *dg_part, *rho, *anchor;
+  const float *end_seq, *end_piece;
+  void* dg;
+  int32_t dg_bf16;
+};
+
+// kSummary: a fragment's own state and decay alone.  kQuery: also the gates'
+// gradient as far as the queries see it; kKey: the rest of it.
+enum LinearMode { kSummary, kOutput, kQuery, kKey };
+
+constexpr int kLinearChunk = 64;
+constexpr float kLeastGate = -160.f;
+
+// Tiles of 64 tokens, rows of W bf16 in 16-byte units; the unit's place is xored
+// with bits of the row, so that 16 rows' units of one column, and 4 rows' 64
+// bytes, lie on different banks.
+template <int W>
+__device__ __forceinline__ const bf16* unit_at(const bf16* tile, int row, int unit) {
+  const int f = W == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+  return tile + row * W + ((unit ^ f) << 3);
+}
+template <int W>
+__device__ __forceinline__ bf16* unit_at(bf16* tile, int row, int unit) {
+  return const_cast<bf16*>(unit_at<W>(static_cast<const bf16*>(tile), row, unit));
+}
+__device__ __forceinline__ bf16x8 ld_unit(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
+
+// A thread's share of a tile on its way to LDS: pairs of neighbouring units.
+template <int W, int NT>
+struct Staged {
+  static constexpr int kSteps = kLinearChunk * (W / 16) / NT;
+  u32x4 r[kSteps][2];
+
+  __device__ __forceinline__ void load(const Tokens& t, int head, int64_t t0, int valid) {
+    const uint16_t* base = t.p + t0 * t.stride + static_cast<int64_t>(head / t.share) * t.width;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int pair = i * NT + static_cast<int>(threadIdx.x), row = pair / (W / 16), s = pair % (W / 16);
+      const uint16_t* p = base + row * t.stride + 16 * s;
+      const u32x4 zero = {0, 0, 0, 0};
+      r[i][0] = row < valid && 16 * s < t.width ? *reinterpret_cast<const u32x4*>(p) : zero;
+      r[i][1] = row < valid && 16 * s + 8 < t.width ? *reinterpret_cast<const u32x4*>(p + 8) : zero;
+    }
+  }
+  // SLOTS: the 8-byte pieces 0 1 2 3 of 16 channels as 0 2 1 3, a lane's k slots
+  template <bool SLOTS>
+  __device__ __forceinline__ void store(bf16* tile) const {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int pair = i * NT + static_cast<int>(threadIdx.x), row = pair / (W / 16), s = pair % (W / 16);
+      u32x4 a = r[i][0], b = r[i][1];
+      if (SLOTS) {
+        const u32x4 c = {a[0], a[1], b[0], b[1]}, d = {a[2], a[3], b[2], b[3]};
+        a = c;
+        b = d;
+      }
+      st4(unit_at<W>(tile, row, 2 * s), a);
+      st4(unit_at<W>(tile, row, 2 * s + 1), b);
+    }
+  }
+};
+
+// Eight tokens row0 .. row0 + 7 of column col0 + lane % 32 (col0, row0 multiples of
+// 32 and 8).
+template <int W>
+__device__ __forceinline__ bf16x8 column_tokens(const bf16* tile, int row0, int col0, int lane) {
+  const int s = lane & 15, unit = (col0 >> 3) + 2 * ((lane >> 4) & 1) + ((s & 3) >> 1), row = row0 + (s >> 2);
+  return join8(lds_read_tr(unit_at<W>(tile, row, unit) + 4 * (s & 1)),
+               lds_read_tr(unit_at<W>(tile, row + 4, unit) + 4 * (s & 1)));
+}
+
+// x as N bf16 parts, each the rest of those before it rounded.
+template <int N>
+__device__ __forceinline__ void split_parts(const float (&x)[8], bf16x8 (&part)[N]) {
+  u32x4 w[N];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = x[2 * i], b = x[2 * i + 1];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const uint32_t h = pack_bf16(a, b);
+      w[n][i] = h;
+      a -= __uint_as_float(h << 16);
+      b -= __uint_as_float(h & 0xffff0000u);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) part[n] = __builtin_bit_cast(bf16x8, w[n]);
+}
+
+// P: out tokens i by tokens j of the sum, 32 x 32 blocks of the triangle's side
+// that is not empty (block of i plus block of j), 16-byte units xored as above.
+__device__ __forceinline__ bf16* p_unit(bf16* part, int block, int row, int unit) {
+  return part + block * 1024 + row * 32 + ((unit ^ ((row >> 2) & 3)) << 3);
+}
+
+template <int KD, int VD, int PS, int MODE>
+struct LinearSmem {
+  static constexpr bool kOut = MODE != kSummary;
+  __align__(16) bf16 x[kOut ? kLinearChunk * KD : 8];
+  __align__(16) bf16 y[kLinearChunk * KD];
+  __align__(16) bf16 z[kLinearChunk * VD];
+  __align__(16) bf16 e[MODE == kQuery ? kLinearChunk * VD : 8];
+  __align__(16) bf16 p[kOut ? PS * 3 * 1024 : 8];
+  __align__(16) float high[kLinearChunk], low[kLinearChunk], w_out[kLinearChunk], w_in[kLinearChunk];
+  float whole;
+  __align__(16) float pairs[MODE == kQuery ? 4 : 1][kLinearChunk];
+  float dots[VD / 32][kLinearChunk];
+};
+
+// A wave's part of a state in memory.
+template <int KD, typename F>
+__device__ __forceinline__ void each_quad(const LinearParams& p, int col, int half, F f) {
+#pragma unroll
+  for (int kt = 0; kt < KD / 32; ++kt) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int row = 32 * kt + 8 * q + 4 * half;
+      f(kt, q, row, row < p.KW && col < p.VW);
+    }
+  }
+}
+__device__ __forceinline__ f32x4 load_quad(const LinearParams& p, const float* s, int row, int col) {
+  if (p.transposed) return ld4(s + static_cast<int64_t>(col) * p.KW + row);
+  f32x4 v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = s[(row + j) * p.VW + col];
+  return v;
+}
+__device__ __forceinline__ void store_quad(const LinearParams& p, float* s, int row, int col, const f32x4 v) {
+  if (p.transposed) {
+    st4(s + static_cast<int64_t>(col) * p.KW + row, v);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s[(row + j) * p.VW + col] = v[j];
+}
+
+__device__ __forceinline__ float wave_prefix(float x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const float y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+__device__ __forceinline__ float wave_suffix(float x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const float y = __shfl_down(x, d);
+    if (lane + d < 64) x += y;
+  }
+  return x;
+}
+
+template <int KD, int VD, int SS, int PS, bool REV, int MODE>
+__global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
+  constexpr int NT = 2 * VD, NW = VD / 32, KT = KD / 32, US = 3;
+  constexpr bool kOut = MODE != kSummary;
+  __shared__ LinearSmem<KD, VD, PS, MODE> sm;
+
+  const int32_t f = p.plan[p.L.frag_order + static_cast<int32_t>(blockIdx.x / static_cast<uint32_t>(p.H))];
+  const int32_t head = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(p.H));
+  const int32_t flags = p.plan[p.L.frag_flags + f], seg = p.plan[p.L.frag_seg + f], seq = p.plan[p.L.frag_seq + f];
+  const int32_t begin = p.plan[p.L.frag_begin + f], end = p.plan[p.L.frag_end + f];
+  const bool carried = (flags & kFragCarried) != 0, seq_end = (flags & kFragSeqEnd) != 0;
+  // whether the pass starts (ends) at its sequence's own end, not at a cut
+  const bool starts = REV ? seq_end : !carried, ends = REV ? !carried : seq_end;
+  if (!kOut && ends) return;   // nothing goes on from here
+
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
+  const int half = lane >> 5, l32 = lane & 31, l16 = lane & 15, quad = lane >> 4;
+  const int col = 32 * wave + l32;
+  const int64_t size = static_cast<int64_t>(p.KW) * p.VW;
+
+  f32x16 S[KT];
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) S[kt] = zero16();
+  {
+    const float* from = starts ? p.seq_state : kOut ? p.piece_state : nullptr;
+    if (from != nullptr) {
+      from += (static_cast<int64_t>(starts ? seq : seg) * p.H + head) * size;
+      each_quad<KD>(p, col, half, [&](int kt, int q, int row, bool has) {
+        if (!has) return;
+        const f32x4 v = load_quad(p, from, row, col);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) S[kt][4 * q + j] = v[j];
+      });
+    }
+  }
+  const int chunks = (end - begin + kLinearChunk - 1) / kLinearChunk;
+  float carry = 0.f;   // kKey: what passes from before the chunk's end to after it
+  if (MODE == kKey) carry = p.anchor[static_cast<int64_t>(f) * p.H + head];
+  double total = 0.0;
+
+  Staged<KD, NT> sx, sy;
+  Staged<VD, NT> sz, se;
+  float gate = 0.f;
+  auto fetch = [&](int it) {
+    const int c = REV ? chunks - 1 - it : it;
+    const int64_t t0 = begin + c * kLinearChunk;
+    const int valid = min(kLinearChunk, end - static_cast<int>(t0));
+    if (kOut) sx.load(p.x, head, t0, valid);
+    sy.load(p.y, head, t0, valid);
+    sz.load(p.z, head, t0, valid);
+    if (MODE == kQuery) se.load(p.e, head, t0, valid);
+    if (wave == 0) {
+      const int64_t i = (t0 + lane) * p.g_stride + head;
+      gate = lane < valid ? (p.g_bf16 ? bf2f(static_cast<const uint16_t*>(p.g)[i]) : static_cast<const float*>(p.g)[i]) : 0.f;
+    }
+  };
+  fetch(0);
+
+  for (int it = 0; it < chunks; ++it) {
+    const int c = REV ? chunks - 1 - it : it;
+    const int64_t t0 = begin + c * kLinearChunk;
+    const int valid = min(kLinearChunk, end - static_cast<int>(t0));
+    block_sync();   // the last chunk's readers
+    if (kOut) sx.template store<true>(sm.x);
+    sy.template store<false>(sm.y);
+    sz.template store<false>(sm.z);
+    if (MODE == kQuery) se.template store<false>(sm.e);
+    if (wave == 0) {
+      double G = static_cast<double>(gate) * 1.4426950408889634074;
+      if (G < kLeastGate) G = kLeastGate;   // NaN stays
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const double y = __shfl_up(G, d);
+        if (lane >= d) G += y;
+      }
+      const double last = __shfl(G, 63);
+      const double high = rint(G * 512.0) * (1.0 / 512.0);
+      const float since = __builtin_amdgcn_exp2f(static_cast<float>(G)), until = __builtin_amdgcn_exp2f(static_cast<float>(last - G));
+      sm.high[lane] = static_cast<float>(high);
+      sm.low[lane] = static_cast<float>(G - high);
+      sm.w_out[lane] = REV ? until : since;
+      sm.w_in[lane] = REV ? since : until;
+      if (lane == 0) sm.whole = __builtin_amdgcn_exp2f(static_cast<float>(last));
+      total += last;
+    }
+    block_sync();
+    if (it + 1 < chunks) fetch(it + 1);
+
+    f32x16 out[2];
+    if constexpr (kOut) {
+      // P: tiles of 16 out tokens (columns) by 16 tokens of the sum (rows)
+#pragma unroll
+      for (int n = 0; n < 4 / NW; ++n) {
+        const int a = NW == 4 ? wave : n == 0 ? wave : 3 - wave;   // the longest row of tiles with the shortest
+        bf16x8 xf[KD / 32], ef[MODE == kQuery ? VD / 32 : 1];
+#pragma unroll
+        for (int s = 0; s < KD / 32; ++s) xf[s] = ld_unit(unit_at<KD>(sm.x, 16 * a + l16, 4 * s + quad));
+        if constexpr (MODE == kQuery) {
+#pragma unroll
+          for (int s = 0; s < VD / 32; ++s) ef[s] = ld_unit(unit_at<VD>(sm.e, 16 * a + l16, 4 * s + quad));
+        }
+        const float high = sm.high[16 * a + l16], low = sm.low[16 * a + l16];
+        float before = 0.f;   // kQuery: the pairs' sum over the tiles so far
+        for (int b = REV ? (a & 2) : 0; b < (REV ? 4 : (a | 1) + 1); ++b) {
+          const int block = (a >> 1) + (b >> 1), row = 16 * (a & 1) + l16, unit = 2 * (b & 1) + (quad >> 1);
+          if (REV ? b < a : b > a) {   // the empty corner of a block on the diagonal
+            const bf16x4 zero = {0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < PS; ++s) *reinterpret_cast<bf16x4*>(p_unit(sm.p + s * 3072, block, row, unit) + 4 * (quad & 1)) = zero;
+            continue;
+          }
+          f32x4 acc = zero4();
+#pragma unroll
+          for (int s = 0; s < KD / 32; ++s) {
+            const int g16 = 2 * s + (quad >> 1), h8 = 4 * (quad & 1);
+            const bf16x4 lo = *reinterpret_cast<const bf16x4*>(unit_at<KD>(sm.y, 16 * b + l16, 2 * g16) + h8);
+            const bf16x4 hi = *reinterpret_cast<const bf16x4*>(unit_at<KD>(sm.y, 16 * b + l16, 2 * g16 + 1) + h8);
+            acc = mfma16(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), xf[s], acc);
+          }
+          const f32x4 high_j = ld4(sm.high + 16 * b + 4 * quad), low_j = ld4(sm.low + 16 * b + 4 * quad);
+          float w[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float e = REV ? (high_j[r] - high) + (low_j[r] - low) : (high - high_j[r]) + (low - low_j[r]);
+            const int j = 4 * quad + r;
+            const bool keep = a != b || (REV ? j >= l16 : j <= l16);
+            w[r] = keep ? acc[r] * __builtin_amdgcn_exp2f(e) : 0.f;
+          }
+          if constexpr (MODE == kQuery) {
+            // pairs (i, j < i): sums over j < t for every t <= i of the tile, then over i
+            f32x4 m = zero4();
+#pragma unroll
+            for (int s = 0; s < VD / 32; ++s) m = mfma16(ld_unit(unit_at<VD>(sm.z, 16 * b + l16, 4 * s + quad)), ef[s], m);
+            float pair[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) pair[r] = a != b || 4 * quad + r < l16 ? m[r] * w[r] : 0.f;
+            float incl = (pair[0] + pair[1]) + (pair[2] + pair[3]);
+            float y = __shfl_up(incl, 16);
+            if (quad >= 1) incl += y;
+            y = __shfl_up(incl, 32);
+            if (quad >= 2) incl += y;
+            y = __shfl_up(incl, 16);
+            float sum = before + (quad >= 1 ? y : 0.f);
+            before += __shfl(incl, 48 + l16);
+            f32x4 column;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              column[r] = sum16(a != b || 4 * quad + r <= l16 ? sum : 0.f);
+              sum += pair[r];
+            }
+            if (l16 == 0) st4(&sm.pairs[a][16 * b + 4 * quad], column);
+          }
+          float left[4] = {w[0], w[1], w[2], w[3]};
+#pragma unroll
+          for (int s = 0; s < PS; ++s) {
+            u32x2 h;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              h[i] = pack_bf16(left[2 * i], left[2 * i + 1]);
+              left[2 * i] -= __uint_as_float(h[i] << 16);
+              left[2 * i + 1] -= __uint_as_float(h[i] & 0xffff0000u);
+            }
+            *reinterpret_cast<u32x2*>(p_unit(sm.p + s * 3072, block, row, unit) + 4 * (quad & 1)) = h;
+          }
+        }
+      }
+      // through the state
+      out[0] = zero16();
+      out[1] = zero16();
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          float v[8];
+          tile_kslots(S[kt], s, v);
+          bf16x8 part[SS];
+          split_parts<SS>(v, part);
+#pragma unroll
+          for (int ib = 0; ib < 2; ++ib) {
+            const bf16x8 xf = ld_unit(unit_at<KD>(sm.x, 32 * ib + l32, 2 * (2 * kt + s) + half));
+#pragma unroll
+            for (int n = 0; n < SS; ++n) out[ib] = mfma(part[n], xf, out[ib]);
+          }
+        }
+      }
+#pragma unroll
+      for (int ib = 0; ib < 2; ++ib) {
+        const float w = sm.w_out[32 * ib + l32];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) out[ib][i] *= w;
+      }
+      if constexpr (MODE == kQuery || MODE == kKey) {
+        // q . (dq through the state), k . (dk through the state)
+#pragma unroll
+        for (int ib = 0; ib < 2; ++ib) {
+          const int t = 32 * ib + l32;
+          float dot = 0.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int ch = 32 * wave + 8 * q + 4 * half;
+            bf16x4 v = {0, 0, 0, 0};
+            if constexpr (MODE == kQuery) {
+              v = *reinterpret_cast<const bf16x4*>(unit_at<VD>(sm.e, t, ch >> 3) + 4 * half);
+            } else if (t < valid && ch < p.VW) {
+              v = *reinterpret_cast<const bf16x4*>(p.e.p + (t0 + t) * p.e.stride + static_cast<int64_t>(head / p.e.share) * p.e.width + ch);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dot += static_cast<float>(v[j]) * out[ib][4 * q + j];
+          }
+          dot = t < valid ? dot : 0.f;
+          dot += __shfl_xor(dot, 32);
+          if (half == 0) sm.dots[wave][t] = dot;
+        }
+      }
+      block_sync();   // P, dots and pairs are whole
+    }
+
+    bf16x8 zf[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) zf[s] = column_tokens<VD>(sm.z, 16 * s + 8 * half, 32 * wave, lane);
+    if constexpr (kOut) {
+#pragma unroll
+      for (int ib = 0; ib < 2; ++ib) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const int jb = s >> 1;
+          if (REV ? jb < ib : jb > ib) continue;
+#pragma unroll
+          for (int n = 0; n < PS; ++n) {
+            out[ib] = mfma(zf[s], ld_unit(p_unit(sm.p + n * 3072, ib + jb, l32, 2 * (s & 1) + half)), out[ib]);
+          }
+        }
+      }
+    }
+    // the state after the chunk
+    const float whole = sm.whole;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) S[kt][i] *= whole;
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const u32x4 raw = __builtin_bit_cast(u32x4, zf[s]);
+      const f32x4 w0 = ld4(sm.w_in + 16 * s + 8 * half), w1 = ld4(sm.w_in + 16 * s + 8 * half + 4);
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(raw[i] << 16) * (i < 2 ? w0[2 * i] : w1[2 * i - 4]);
+        v[2 * i + 1] = __uint_as_float(raw[i] & 0xffff0000u) * (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]);
+      }
+      bf16x8 part[US];
+      split_parts<US>(v, part);
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        const bf16x8 yf = column_tokens<KD>(sm.y, 16 * s + 8 * half, 32 * kt, lane);
+#pragma unroll
+        for (int n = 0; n < US; ++n) S[kt] = mfma(yf, part[n], S[kt]);
+      }
+    }
+    if constexpr (kOut) {
+#pragma unroll
+      for (int ib = 0; ib < 2; ++ib) {
+        const int t = 32 * ib + l32;
+        const int64_t at = ((t0 + t) * p.H + head) * p.VW;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int ch = 32 * wave + 8 * q + 4 * half;
+          if (t >= valid || ch >= p.VW) continue;
+          if (p.o_fp32) {
+            const f32x4 v = {out[ib][4 * q], out[ib][4 * q + 1], out[ib][4 * q + 2], out[ib][4 * q + 3]};
+            st4(static_cast<float*>(p.o) + at + ch, v);
+          } else {
+            const u32x2 v = {pack_bf16(out[ib][4 * q], out[ib][4 * q + 1]), pack_bf16(out[ib][4 * q + 2], out[ib][4 * q + 3])};
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.o) + at + ch) = v;
+          }
+        }
+      }
+    }
+    if constexpr (MODE == kQuery || MODE == kKey) {
+      // dg_t = pairs across t in the chunk + what the tokens from t on take from
+      // before the chunk + what those before t give to after it + what passes by
+      if (wave == 0) {
+        float dot = sm.dots[0][lane];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) dot += sm.dots[w][lane];
+        const int64_t at = (t0 + lane) * p.H + head, slot = (static_cast<int64_t>(begin / kLinearChunk) + f + c) * p.H + head;
+        if constexpr (MODE == kQuery) {
+          float sum = 0.f;
+#pragma unroll
+          for (int a = 0; a < 4; ++a) sum += lane < 16 * (a + 1) ? sm.pairs[a][lane] : 0.f;
+          const float after = wave_suffix(dot, lane);
+          if (lane < valid) p.dg_part[at] = sum + after;
+          if (lane == 0) p.rho[slot] = after;
+        } else {
+          const float upto = wave_prefix(dot, lane);
+          float given = __shfl_up(upto, 1);
+          if (lane == 0) given = 0.f;
+          const float by = carry - __shfl(upto, 63);
+          if (lane < valid) {
+            const float d = p.dg_part[at] + given + by;
+            if (p.dg_bf16) {
+              static_cast<uint16_t*>(p.dg)[at] = static_cast<uint16_t>(pack_bf16(d, 0.f));
+            } else {
+              static_cast<float*>(p.dg)[at] = d;
+            }
+          }
+          carry = by + p.rho[slot];
+        }
+      }
+    }
+  }
+
+  if (MODE == kSummary) {
+    float* to = p.piece_out + (static_cast<int64_t>(seg) * p.H + head) * size;
+    each_quad<KD>(p, col, half, [&](int kt, int q, int row, bool has) {
+      const f32x4 v = {S[kt][4 * q], S[kt][4 * q + 1], S[kt][4 * q + 2], S[kt][4 * q + 3]};
+      if (has) store_quad(p, to, row, col, v);
+    });
+    if (p.decay_out != nullptr && tid == 0) {
+      p.decay_out[static_cast<int64_t>(seg) * p.H + head] = __builtin_amdgcn_exp2f(static_cast<float>(total));
+    }
+  } else if (p.seq_out != nullptr && ends) {
+    float* to = p.seq_out + (static_cast<int64_t>(seq) * p.H + head) * size;
+    each_quad<KD>(p, col, half, [&](int kt, int q, int row, bool has) {
+      const f32x4 v = {S[kt][4 * q], S[kt][4 * q + 1], S[kt][4 * q + 2], S[kt][4 * q + 3]};
+      if (has) store_quad(p, to, row, col, v);
+    });
+  }
+  if constexpr (MODE == kQuery) {
+    // <the cotangent of the state after the fragment, that state>
+    const float* with = ends ? p.end_seq : p.end_piece;
+    float dot = 0.f;
+    if (with != nullptr) {
+      with += (static_cast<int64_t>(ends ? seq : seg) * p.H + head) * size;
+      each_quad<KD>(p, col, half, [&](int kt, int q, int row, bool has) {
+        if (!has) return;
+        const f32x4 v = load_quad(p, with, row, col);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dot += v[j] * S[kt][4 * q + j];
+      });
+    }
+    dot = sum64(dot);
+    block_sync();
+    if (lane == 0) sm.dots[wave][0] = dot;
+    block_sync();
+    if (tid == 0) {
+      for (int w = 1; w < NW; ++w) dot += sm.dots[w][0];
+      p.anchor[static_cast<int64_t>(f) * p.H + head] = dot;
+    }
+  }
+}
+
+// KD and VD by the widths in use.
+template <int SS, int PS, bool REV, int MODE>
+void (*linear_kernel_of(int32_t KW, int32_t VW))(LinearParams) {
+  if (KW > 64) return VW > 64 ? linear_kernel<128, 128, SS, PS, REV, MODE> : linear_kernel<128, 64, SS, PS, REV, MODE>;
+  return VW > 64 ? linear_kernel<64, 128, SS, PS, REV, MODE> : linear_kernel<64, 64, SS, PS, REV, MODE>;
+}
+
+// The gradients' passes (kda_linear_query.hip, kda_linear_key.hip,
+// kda_linear_value.hip).
+void (*linear_query_kernel(int32_t KW, int32_t VW, bool fp32))(LinearParams);
+void (*linear_key_kernel(int32_t KW, int32_t VW, bool fp32))(LinearParams);
+void (*linear_value_kernel(int32_t KW, int32_t VW, bool fp32))(LinearParams);
+
+// Launches one pass over all fragments and heads (kda_linear.hip).
+int launch_linear_pass(void (*kernel)(LinearParams), const LinearParams& p, int32_t fragments, hipStream_t stream);
+
+}  // namespace kda
+
+#endif  // KDA_LINEAR_PASS_H_

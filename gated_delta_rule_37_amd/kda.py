@@ -61,6 +61,7 @@ SYMBOLS = (
     "kda_output_norm", "kda_output_norm_backward", "kda_output_norm_backward_workspace_bytes",
     "kda_scan_forward", "kda_scan_backward", "kda_scan_workspace_bytes", "kda_scan_step", "kda_step",
     "kda_qk_norm_rotate", "kda_qk_norm_rotate_backward", "kda_qk_norm_rotate_backward_workspace_bytes",
+    "kda_linear_forward", "kda_linear_workspace_bytes", "kda_linear_backward", "kda_linear_backward_workspace_bytes",
     "kda_linear_step",
 )
 
@@ -144,10 +145,17 @@ def lib() -> ctypes.CDLL:
     rotate = [*[i32] * 7, *rows * 2, *buf * 4, *[f32] * 2]
     L.kda_qk_norm_rotate.argtypes = [*rotate, *buf * 2, p]
     L.kda_qk_norm_rotate_backward.argtypes = [*rotate, *buf * 2, i32, *buf * 4, *buf, p]
+    linear = [p, *buf, *[i32] * 6, *rows * 4, i32, *buf]
+    L.kda_linear_forward.argtypes = [*linear, *buf, i32, *buf, *buf, p]
+    L.kda_linear_backward.argtypes = [*linear, *buf * 2, *buf * 3, i32, *buf * 2, *buf, p]
+    L.kda_linear_workspace_bytes.argtypes = [p, *[i32] * 3]
+    L.kda_linear_workspace_bytes.restype = sz
+    L.kda_linear_backward_workspace_bytes.argtypes = [p, *[i32] * 6]
+    L.kda_linear_backward_workspace_bytes.restype = sz
     L.kda_linear_step.argtypes = [*[i32] * 7, *buf * 3, *rows, i32, *buf, i32, *buf * 3, i32, p]
     for name in ("kda_prepare_inputs", "kda_prepare_inputs_backward", "kda_output_norm", "kda_output_norm_backward",
                  "kda_scan_forward", "kda_scan_backward", "kda_scan_step", "kda_step", "kda_qk_norm_rotate",
-                 "kda_qk_norm_rotate_backward", "kda_linear_step"):
+                 "kda_qk_norm_rotate_backward", "kda_linear_forward", "kda_linear_backward", "kda_linear_step"):
         getattr(L, name).restype = ctypes.c_int
     for name in ("kda_prepare_inputs_backward_workspace_bytes", "kda_output_norm_backward_workspace_bytes"):
         getattr(L, name).argtypes = [i32] * 3

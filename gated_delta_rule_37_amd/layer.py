@@ -443,6 +443,70 @@ def _linear_heads(q, k, v, g):
     return max(Hq, Hk, Hv, g.shape[-1]), Hq, Hk, Hv, K, V
 
 
+def linear_segments(cu_seqlens, H: int) -> int:
+    """The segment count for a plan that only linear attention with ``H`` heads
+    uses: enough pieces to fill the GPU, none under 256 tokens."""
+    T, N = int(cu_seqlens[-1]), len(cu_seqlens) - 1
+    fill = -(-1024 // H)
+    return 1 if N >= fill else max(1, min(fill, T // 256))
+
+
+def _linear(plan, q, k, v, g, initial_state, stream):
+    """H, the other sizes, the device and the arguments that both directions share."""
+    H, Hq, Hk, Hv, K, V = sizes = _linear_heads(q, k, v, g)
+    T, bf, dev = q.shape[0], torch.bfloat16, q.device
+    if T != plan.T:
+        raise ValueError(f"inputs hold {T} tokens, the plan {plan.T}")
+    blob = plan.device_blob(dev, stream)
+    gates = (*_buf(g, g.dtype, (H,), "g", dev), 0) if g.dim() == 1 else _rows(g, g.dtype, (T, H), "g", dev)
+    args = [plan.handle, *_buf(blob, torch.int32, (len(plan.blob),), "plan_dev", dev), *sizes,
+            *_rows(q, bf, (T, Hq, K), "q", dev), *_rows(k, bf, (T, Hk, K), "k", dev), *_rows(v, bf, (T, Hv, V), "v", dev),
+            *gates, _dtype(g, "g"), *_buf(initial_state, torch.float32, (plan.N, H, K, V), "initial_state", dev)]
+    return T, sizes, dev, args
+
+
+def linear_forward(plan: kda.Plan, q, k, v, g, initial_state=None, o_dtype=torch.bfloat16, out=None, stream=None):
+    """``kda_linear_forward``: S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = S_t^T q_t for
+    q [T, Hq, K], k [T, Hk, K], v [T, Hv, V] bf16 (rows may be slices of a wider
+    projection) and g [T, H] or [H] (fp32 or bf16), every sequence of the plan from
+    its ``initial_state`` [N, H, K, V] (default: zero).  There are as many states,
+    H, as the most heads of q, k, v and g; a tensor of fewer heads is shared by
+    neighbours.  The plan's pieces run in parallel (:func:`linear_segments`).
+    Returns dict(o, final_state), o [T, H, V] in ``o_dtype``, final_state fp32."""
+    T, (H, Hq, Hk, Hv, K, V), dev, args = _linear(plan, q, k, v, g, initial_state, stream)
+    f32 = torch.float32
+    if out is None:
+        out = dict(o=_empty(stream, dev, o_dtype, T, H, V), final_state=_empty(stream, dev, f32, plan.N, H, K, V))
+    o = out["o"]
+    workspace = _scratch(kda.lib().kda_linear_workspace_bytes(plan.handle, H, K, V), dev, stream)
+    args += [*_buf(o, o.dtype, (T, H, V), "o", dev), _dtype(o, "o"),
+             *_buf(out["final_state"], f32, (plan.N, H, K, V), "final_state", dev), *_made(workspace)]
+    _call("kda_linear_forward", dev, args, stream)
+    return out
+
+
+def linear_backward(plan: kda.Plan, q, k, v, g, d_o, d_final=None, initial_state=None, want_dh0=None,
+                    grad_dtype=torch.bfloat16, stream=None):
+    """``kda_linear_backward``: gradients for the cotangents ``d_o`` [T, H, V] (bf16)
+    and ``d_final`` [N, H, K, V] (fp32, default: zero) as dict(dq, dk, dv, dg, dh0):
+    dq, dk and dv in ``grad_dtype``, dg like g, dh0 (fp32) None unless ``want_dh0``
+    (default: whether there are initial states)."""
+    T, (H, Hq, Hk, Hv, K, V), dev, args = _linear(plan, q, k, v, g, initial_state, stream)
+    if grad_dtype not in DTYPES:
+        raise TypeError(f"grad_dtype: expected one of {list(DTYPES)}, got {grad_dtype}")
+    f32, state = torch.float32, (plan.N, H, K, V)
+    want = initial_state is not None if want_dh0 is None else want_dh0
+    out = dict(dq=_empty(stream, dev, grad_dtype, T, Hq, K), dk=_empty(stream, dev, grad_dtype, T, Hk, K),
+               dv=_empty(stream, dev, grad_dtype, T, Hv, V), dg=_empty(stream, dev, g.dtype, *g.shape),
+               dh0=_empty(stream, dev, f32, *state) if want else None)
+    workspace = _scratch(kda.lib().kda_linear_backward_workspace_bytes(plan.handle, H, Hq, Hk, Hv, K, V), dev, stream)
+    args += [*_buf(d_o, torch.bfloat16, (T, H, V), "d_o", dev), *_buf(d_final, f32, state, "d_final", dev),
+             *_made(out["dq"]), *_made(out["dk"]), *_made(out["dv"]), DTYPES[grad_dtype], *_made(out["dg"]),
+             *_made(out["dh0"]), *_made(workspace)]
+    _call("kda_linear_backward", dev, args, stream)
+    return out
+
+
 def linear_step(q, k, v, g, state, slots=None, state_out=None, o=None, o_dtype=torch.bfloat16, stream=None):
     """``kda_linear_step``: the next token of B sequences, q [B, Hq, K], k [B, Hk, K]
     and v [B, Hv, V] bf16, g [B, H] or [H] (fp32 or bf16), whose states lie in the

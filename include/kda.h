@@ -660,6 +660,72 @@ int kda_scan_backward(const kda_plan* plan, const int32_t* plan_dev, size_t plan
 size_t kda_scan_workspace_bytes(const kda_plan* plan, int32_t D);
 
 /*
+ * kda_linear_forward -- linear attention with a decay for each head over the
+ * plan's packed sequences: with a state S [K, V] for each of H heads,
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t
+ * where S before a sequence's first token is its initial state.
+ *   q              [T, Hq, K], k [T, Hk, K], v [T, Hv, V] bf16, each with its
+ *                  own token stride, a multiple of 8 elements
+ *                  (KDA_ERR_MISALIGNED)
+ *   heads          H is a multiple of Hq, Hk and Hv (KDA_ERR_INVALID_ARG); head
+ *                  h reads q head h / (H / Hq), k head h / (H / Hk) and v head
+ *                  h / (H / Hv)
+ *   K, V           multiples of 8, at most 128 (KDA_ERR_UNSUPPORTED)
+ *   g              g_dtype (kda_dtype), [T, H] with a token stride, or [H], the
+ *                  same for every token, with g_stride 0; g <= 0, finite or
+ *                  -inf (exp(-inf) = 0 forgets the state)
+ *   initial_state  [N, H, K, V] FP32 or NULL (zero)
+ *   o              [T, H, V] in o_format; final_state [N, H, K, V] FP32
+ * The plan's pieces (its segments, if it has none) run in parallel and change
+ * results only by rounding: a long sequence wants several times as many as fill
+ * the GPU with the heads.  Where a piece goes on within its sequence its state
+ * comes from a first pass over all keys and values.  Values are exact products
+ * of the bf16 inputs in FP32 sums; factors that are not bf16 (decays, states) are
+ * used with 16 bits for a BF16 o and 24 for an FP32 one and for the states.  An
+ * infinity or NaN stays in its own sequence and head; in o it may reach earlier
+ * tokens of the same 64-token chunk.
+ * Workspace: kda_linear_workspace_bytes(plan, H, K, V) bytes, NULL where that is
+ * 0 (no sequence is cut).  Two calls that may run at the same time need a
+ * workspace each.
+ */
+int kda_linear_forward(const kda_plan* plan, const int32_t* plan_dev, size_t plan_dev_bytes, int32_t H, int32_t Hq,
+                       int32_t Hk, int32_t Hv, int32_t K, int32_t V, const uint16_t* q, size_t q_bytes, int64_t q_stride,
+                       const uint16_t* k, size_t k_bytes, int64_t k_stride, const uint16_t* v, size_t v_bytes, int64_t v_stride,
+                       const void* g, size_t g_bytes, int64_t g_stride, int32_t g_dtype,
+                       const float* initial_state, size_t initial_state_bytes,
+                       void* o, size_t o_bytes, int32_t o_format, float* final_state, size_t final_state_bytes,
+                       void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t kda_linear_workspace_bytes(const kda_plan* plan, int32_t H, int32_t K, int32_t V);
+
+/*
+ * kda_linear_backward -- gradients of kda_linear_forward: with the cotangents
+ * d_o [T, H, V] (bf16, dense) and d_final [N, H, K, V] (FP32, or NULL for zero)
+ * and, within every sequence,
+ *     L_t = q_t do_t^T + exp(g_{t+1}) L_{t+1}   (at the end: + d_final)
+ *     dq_t = S_t do_t, dk_t = L_t v_t, dv_t = L_t^T k_t
+ *     dg_t = exp(g_t) <L_t, S_{t-1}>,  d_initial_state = exp(g_1) L_1
+ *   dq, dk, dv       as q, k and v but dense, in grad_format (kda_dtype): heads
+ *                    that share a row add up
+ *   dg               g_dtype, [T, H] dense, or [H] (summed over the tokens)
+ *                    with g_stride 0
+ *   d_initial_state  [N, H, K, V] FP32 or NULL
+ * States are made again from the inputs.  Workspace: as above, by
+ * kda_linear_backward_workspace_bytes (never 0).
+ */
+int kda_linear_backward(const kda_plan* plan, const int32_t* plan_dev, size_t plan_dev_bytes, int32_t H, int32_t Hq,
+                        int32_t Hk, int32_t Hv, int32_t K, int32_t V, const uint16_t* q, size_t q_bytes, int64_t q_stride,
+                        const uint16_t* k, size_t k_bytes, int64_t k_stride, const uint16_t* v, size_t v_bytes, int64_t v_stride,
+                        const void* g, size_t g_bytes, int64_t g_stride, int32_t g_dtype,
+                        const float* initial_state, size_t initial_state_bytes,
+                        const uint16_t* d_o, size_t d_o_bytes, const float* d_final, size_t d_final_bytes,
+                        void* dq, size_t dq_bytes, void* dk, size_t dk_bytes, void* dv, size_t dv_bytes,
+                        int32_t grad_format, void* dg, size_t dg_bytes,
+                        float* d_initial_state, size_t d_initial_state_bytes,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t kda_linear_backward_workspace_bytes(const kda_plan* plan, int32_t H, int32_t Hq, int32_t Hk, int32_t Hv, int32_t K,
+                                           int32_t V);
+
+/*
  * Single tokens over a pool of states (kda_scan_step, kda_step,
  * kda_linear_step).  Row b of the
  * batch is the next token of the sequence whose state lies in slot slots[b] of

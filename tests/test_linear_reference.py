@@ -72,3 +72,70 @@ def test_heads_are_shared_by_neighbours():
     assert y.shape == (5, 6, 3)
     for h in range(6):
         assert torch.equal(y[:, h], x[:, h // 3])
+
+
+def _packed(cu, H, Hq, Hk, Hv, K, V, init, seed):
+    T, N = cu[-1], len(cu) - 1
+    x = dict(q=_randn(T, Hq, K, seed=seed), k=_randn(T, Hk, K, seed=seed + 1), v=_randn(T, Hv, V, seed=seed + 2),
+             g=-torch.rand(T, H, generator=torch.Generator().manual_seed(seed + 3), dtype=F64))
+    if init:
+        x["h0"] = _randn(N, H, K, V, seed=seed + 4)
+    return x, _randn(T, H, V, seed=seed + 5), _randn(N, H, K, V, seed=seed + 6)
+
+
+def test_forward_is_attention_with_decay():
+    """Over all pairs of a sequence's tokens, and the bound's magnitudes."""
+    cu = [0, 1, 6, 17]
+    x, _, _ = _packed(cu, 4, 2, 1, 4, 3, 5, False, 7)
+    out, size = ref.forward(**x, cu=cu)
+    q, k, v = (ref.of_heads(x[n], 4) for n in "qkv")
+    for lo, hi in zip(cu, cu[1:]):
+        G = torch.cumsum(x["g"][lo:hi], 0)
+        D = torch.exp(G[:, None] - G[None]) * torch.ones(hi - lo, hi - lo, dtype=F64).tril()[..., None]
+        o = torch.einsum("ihk,jhk,ijh,jhv->ihv", q[lo:hi], k[lo:hi], D, v[lo:hi])
+        assert torch.allclose(out["o"][lo:hi], o, rtol=1e-11, atol=1e-12)
+    assert (size["o"] >= out["o"].abs() - 1e-12).all()
+
+
+@pytest.mark.parametrize("Hq,Hk,Hv,init", [(4, 4, 4, True), (2, 2, 4, True), (4, 1, 2, False)])
+def test_backward(Hq, Hk, Hv, init):
+    """Against automatic differentiation of the forward pass and differences."""
+    cu = [0, 3, 4, 13]
+    x, d_o, d_final = _packed(cu, 4, Hq, Hk, Hv, 3, 5, init, 11)
+    leaves = {n: t.clone().requires_grad_() for n, t in x.items()}
+    loss = _loss(leaves, cu, d_o, d_final)
+    loss.backward()
+    out, size = ref.backward(**x, cu=cu, d_o=d_o, d_final=d_final)
+    for n, t in leaves.items():
+        name = "dh0" if n == "h0" else "d" + n
+        assert torch.allclose(out[name], t.grad, rtol=1e-10, atol=1e-11), name
+        assert (size[name] >= out[name].abs() - 1e-12).all()
+        u, h = _randn(*t.shape, seed=99), 1e-5
+        with torch.no_grad():
+            f = [float(_loss({**x, n: x[n] + s * u}, cu, d_o, d_final)) for s in (h, -h)]
+        assert math.isclose((f[0] - f[1]) / (2 * h), float((out[name] * u).sum()), rel_tol=1e-6, abs_tol=1e-6)
+
+
+def _loss(x, cu, d_o, d_final):
+    """sum d_o o + sum d_final S_T, by stacking (in place writes cannot be differentiated)."""
+    H = x["g"].shape[1]
+    q, k, v = (ref.of_heads(x[n], H) for n in "qkv")
+    loss = 0.0
+    for n, (lo, hi) in enumerate(zip(cu, cu[1:])):
+        S = x["h0"][n] if "h0" in x else torch.zeros(H, q.shape[-1], v.shape[-1], dtype=F64)
+        for t in range(lo, hi):
+            S = torch.exp(x["g"][t])[:, None, None] * S + k[t][..., None] * v[t][:, None, :]
+            loss = loss + ((S * q[t][..., None]).sum(-2) * d_o[t]).sum()
+        loss = loss + (S * d_final[n]).sum()
+    return loss
+
+
+def test_steps_are_the_forward_pass():
+    cu = [0, 5]
+    x, _, _ = _packed(cu, 2, 2, 2, 2, 3, 4, True, 3)
+    out, _ = ref.forward(**x, cu=cu)
+    S = x["h0"][0]
+    for t in range(5):
+        o, S, _ = ref.step(x["q"][t], x["k"][t], x["v"][t], x["g"][t], S)
+        assert torch.allclose(o, out["o"][t])
+    assert torch.allclose(S, out["final_state"][0])
