@@ -166,7 +166,7 @@ LinearLayout linear_layout(const kda_plan* plan, int32_t H, int32_t K, int32_t V
 // Backward: also the states' cotangents, the gates' gradient [T][H], what each
 // chunk's queries take from before it [ceil(T / 64) + F][H] (chunk c of fragment f
 // in slot floor(begin_f / 64) + f + c; then the 64 ranges' sums of a shared
-// gate), what passes each fragment's end [F][H], and one gradient of every head
+// gate), what passes by each fragment's last chunk [F][H], and one gradient of every head
 // [T][H][max(K, V)] where heads are shared.
 struct LinearBwdLayout {
   size_t states, cotangents, decays, gates, rho, anchor, heads, total;

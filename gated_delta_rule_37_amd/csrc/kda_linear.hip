@@ -207,6 +207,8 @@ int launch_linear_backward(const LinearArgs& a, hipStream_t stream) {
   p.e = k;
   p.seq_state = d_final;
   p.piece_state = at(L.cotangents);
+  p.end_seq = h0;
+  p.end_piece = at(L.states);
   p.dg = fixed ? at(L.gates) : a.dg.ptr;
   p.dg_bf16 = !fixed && a.g_dtype == KDA_BF16 ? 1 : 0;
   st = pass(p, a.Hk, a.dk, linear_key_kernel(a.V, a.K, fp32));

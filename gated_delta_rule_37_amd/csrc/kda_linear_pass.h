@@ -64,7 +64,7 @@ struct LinearParams {
   int32_t o_fp32;
   // gradient of the gates
   float *dg_part, *rho, *anchor;
-  const float *end_seq, *end_piece;
+  const float *end_seq, *end_piece;   // the states of the other gradient where this pass ends (seq: or null)
   void* dg;
   int32_t dg_bf16;
 };
@@ -171,6 +171,7 @@ struct LinearSmem {
   float whole;
   __align__(16) float pairs[MODE == kQuery ? 4 : 1][kLinearChunk];
   float dots[VD / 32][kLinearChunk];
+  float by[VD / 32];
 };
 
 // A wave's part of a state in memory.
@@ -255,7 +256,6 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
   }
   const int chunks = (end - begin + kLinearChunk - 1) / kLinearChunk;
   float carry = 0.f;   // kKey: what passes from before the chunk's end to after it
-  if (MODE == kKey) carry = p.anchor[static_cast<int64_t>(f) * p.H + head];
   double total = 0.0;
 
   Staged<KD, NT> sx, sy;
@@ -432,6 +432,24 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
           if (half == 0) sm.dots[wave][t] = dot;
         }
       }
+      // What passes by the chunk, e^{G_C} <cotangent after it, state before it>, is a
+      // dot product of states at both ends of the fragment, where the other state is
+      // in memory, and between them the difference of what crosses two borders
+      if (MODE == kQuery ? it + 1 == chunks : MODE == kKey && c == 0 && chunks > 1) {
+        const float* with = ends ? p.end_seq : p.end_piece;
+        float dot = 0.f;
+        if (with != nullptr) {
+          with += (static_cast<int64_t>(ends ? seq : seg) * p.H + head) * size;
+          each_quad<KD>(p, col, half, [&](int kt, int q, int row, bool has) {
+            if (!has) return;
+            const f32x4 v = load_quad(p, with, row, col);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dot += v[j] * S[kt][4 * q + j];
+          });
+        }
+        dot = sum64(dot);
+        if (lane == 0) sm.by[wave] = dot;
+      }
       block_sync();   // P, dots and pairs are whole
     }
 
@@ -512,11 +530,25 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
           const float after = wave_suffix(dot, lane);
           if (lane < valid) p.dg_part[at] = sum + after;
           if (lane == 0) p.rho[slot] = after;
+          if (it + 1 == chunks && lane == 0) {
+            float by = sm.by[0];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) by += sm.by[w];
+            p.anchor[static_cast<int64_t>(f) * p.H + head] = sm.whole * by;
+          }
         } else {
           const float upto = wave_prefix(dot, lane);
           float given = __shfl_up(upto, 1);
           if (lane == 0) given = 0.f;
-          const float by = carry - __shfl(upto, 63);
+          float by = carry - __shfl(upto, 63);
+          if (it == 0) {
+            by = p.anchor[static_cast<int64_t>(f) * p.H + head];
+          } else if (c == 0) {
+            by = sm.by[0];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) by += sm.by[w];
+            by *= sm.whole;
+          }
           if (lane < valid) {
             const float d = p.dg_part[at] + given + by;
             if (p.dg_bf16) {
@@ -546,28 +578,6 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
       const f32x4 v = {S[kt][4 * q], S[kt][4 * q + 1], S[kt][4 * q + 2], S[kt][4 * q + 3]};
       if (has) store_quad(p, to, row, col, v);
     });
-  }
-  if constexpr (MODE == kQuery) {
-    // <the cotangent of the state after the fragment, that state>
-    const float* with = ends ? p.end_seq : p.end_piece;
-    float dot = 0.f;
-    if (with != nullptr) {
-      with += (static_cast<int64_t>(ends ? seq : seg) * p.H + head) * size;
-      each_quad<KD>(p, col, half, [&](int kt, int q, int row, bool has) {
-        if (!has) return;
-        const f32x4 v = load_quad(p, with, row, col);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dot += v[j] * S[kt][4 * q + j];
-      });
-    }
-    dot = sum64(dot);
-    block_sync();
-    if (lane == 0) sm.dots[wave][0] = dot;
-    block_sync();
-    if (tid == 0) {
-      for (int w = 1; w < NW; ++w) dot += sm.dots[w][0];
-      p.anchor[static_cast<int64_t>(f) * p.H + head] = dot;
-    }
   }
 }
 

@@ -132,6 +132,23 @@ def test_precision_over_whole_outputs():
     assert max(off.values()) < 1e-6, off
 
 
+def test_gate_gradient_of_nothing_is_zero():
+    """Single tokens from a zero state: their gate scales nothing; and where every
+    gate forgets all (-inf, or far below FP32), nothing crosses it."""
+    cu, H = [0, 1, 2, 3], 2
+    x, g, _, dev = _case(cu, H, H, H, H, 64, 128, "fp32", False, False, seed=5)
+    d_o, d_final = _randn(3, H, 128, seed=50, dtype=BF), _randn(3, H, 64, 128, seed=51)
+    got = layer.linear_backward(kda.Plan(cu, 2), *dev, _d(g), _d(d_o), d_final=_d(d_final))
+    assert (got["dg"] == 0).all()
+    cu = [0, 65, 300]
+    for gate in (float("-inf"), -200.0):
+        x, g, h0, dev = _case(cu, H, H, H, H, 64, 128, "fp32", True, False, seed=6)
+        g.fill_(gate)
+        d_o, d_final = _randn(300, H, 128, seed=50, dtype=BF), _randn(2, H, 64, 128, seed=51)
+        got = layer.linear_backward(kda.Plan(cu, 3), *dev, _d(g), _d(d_o), d_final=_d(d_final), initial_state=_d(h0))
+        assert (got["dg"] == 0).all() and (got["dh0"] == 0).all()
+
+
 def test_sequences_stay_apart():
     """What is not finite stays in its own sequence and head, and reaches no token
     of an earlier chunk."""
