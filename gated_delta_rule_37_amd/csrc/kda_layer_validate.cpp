@@ -21,6 +21,7 @@ constexpr int64_t kMaxNormRow = 1 << 24;   // H * V: the column sums' grid
 constexpr int32_t kMaxHeads = 65535;
 constexpr int32_t kMaxRotateWidth = 256;
 constexpr int32_t kMaxLinearWidth = 128;
+constexpr int32_t kMaxLinearHeads = 16384;
 constexpr int64_t kMaxStride = (int64_t(1) << 31) - 1;   // 2^30 rows of it stay inside 64-bit byte counts
 
 bool known_type(int32_t t) { return t == KDA_FP32 || t == KDA_BF16; }
@@ -391,6 +392,9 @@ int check_linear(const LinearArgs& a, bool backward) {
   st = first_error({check_stride(a.q, static_cast<int64_t>(q_row)), check_stride(a.k, static_cast<int64_t>(k_row)),
                     check_stride(a.v, static_cast<int64_t>(v_row)), fixed ? KDA_OK : check_stride(a.g, a.H)});
   if (st != KDA_OK) return st;
+  // byte offsets inside a chunk of 64 tokens stay below 2^31
+  if (a.q.stride > kMaxScanStride || a.k.stride > kMaxScanStride || a.v.stride > kMaxScanStride) return KDA_ERR_UNSUPPORTED;
+  if (a.H > kMaxLinearHeads) return KDA_ERR_UNSUPPORTED;
   st = check_buffers({{a.plan_dev.ptr, a.plan_dev.bytes, a.plan->blob.size() * sizeof(int32_t), false},
                       {a.q.ptr, a.q.bytes, rows_need(a.q, T, q_row, 2), false},
                       {a.k.ptr, a.k.bytes, rows_need(a.k, T, k_row, 2), false},

@@ -32,19 +32,30 @@ __global__ __launch_bounds__(kRowThreads) void linear_scan_kernel(const int32_t*
   const int32_t i = static_cast<int32_t>(blockIdx.x) * kRowThreads + static_cast<int32_t>(threadIdx.x);
   const int32_t head = static_cast<int32_t>(blockIdx.y);
   if (i >= quads) return;
-  float* own = states + (static_cast<int64_t>(head) * quads + i) * 4;
+  float* const own = states + (static_cast<int64_t>(head) * quads + i) * 4;
   const int64_t step = static_cast<int64_t>(H) * quads * 4;
   f32x4 state = zero4();
-  for (int32_t n = 0; n < P; ++n) {
-    const int32_t r = REV ? P - 1 - n : n;
-    const bool before = plan[L.seg_carry_in + r] != 0, after = r + 1 < P && plan[L.seg_carry_in + r + 1] != 0;
-    const bool through = before && after && plan[L.seg_transition_live + r] != 0;
-    float* at = own + r * step;
-    const bool has = REV ? before : after;   // the piece's update was made
-    f32x4 update = zero4();
-    if (has) update = ld4(at);
-    if (REV ? after : before) st4(at, state);
-    state = has ? (through ? decays[static_cast<int64_t>(r) * H + head] * state + update : update) : zero4();
+  // eight pieces' updates in flight; those that were not made are read and dropped
+  constexpr int kAhead = 8;
+  for (int32_t n0 = 0; n0 < P; n0 += kAhead) {
+    f32x4 update[kAhead];
+    float decay[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int32_t n = min(n0 + i, P - 1), r = REV ? P - 1 - n : n;
+      update[i] = ld4(own + r * step);
+      decay[i] = decays[static_cast<int64_t>(r) * H + head];
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (n0 + i >= P) break;
+      const int32_t r = REV ? P - 1 - n0 - i : n0 + i;
+      const bool before = plan[L.seg_carry_in + r] != 0, after = r + 1 < P && plan[L.seg_carry_in + r + 1] != 0;
+      const bool through = before && after && plan[L.seg_transition_live + r] != 0;
+      const bool has = REV ? before : after;   // the piece's update was made
+      if (REV ? after : before) st4(own + r * step, state);
+      state = has ? (through ? decay[i] * state + update[i] : update[i]) : zero4();
+    }
   }
 }
 

@@ -20,10 +20,13 @@
 //     parts go through LDS, as they are every wave's operand.
 //   * out^T = S^T x^T + z^T P^T: transposed, so that a lane has one token and four
 //     neighbouring channels.  S's accumulators are the matrix core's operand as
-//     they are (their rows are its k slots; x is stored so that 16 bytes of LDS
-//     hold a lane's k slots), split in registers.
+//     they are: its rows stand for channels in the order that makes a lane's k
+//     slots eight neighbouring channels.  They are split in registers.
 //   * S's update: z, read transposed, times its weights, split in registers; y
 //     read transposed.
+// The chunks come by copies from memory to LDS that take no registers: x of the next
+// chunk after its last reader in this one, y into a second buffer a chunk ahead, z
+// beside P, which does not need it.
 // Decays: a gate of a token enters with at least -160 in units of 2 (2^-160 is 0 in
 // FP32), prefix sums are taken in FP64 and kept as a multiple of 2^-9 and the
 // rest, so that the difference of two of them is exact however large they are.
@@ -80,50 +83,97 @@ constexpr float kLeastGate = -160.f;
 // with bits of the row, so that 16 rows' units of one column, and 4 rows' 64
 // bytes, lie on different banks.
 template <int W>
+__device__ __forceinline__ int row_bits(int row) {
+  return W == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+}
+template <int W>
 __device__ __forceinline__ const bf16* unit_at(const bf16* tile, int row, int unit) {
-  const int f = W == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
-  return tile + row * W + ((unit ^ f) << 3);
+  return tile + row * W + ((unit ^ row_bits<W>(row)) << 3);
 }
 template <int W>
 __device__ __forceinline__ bf16* unit_at(bf16* tile, int row, int unit) {
   return const_cast<bf16*>(unit_at<W>(static_cast<const bf16*>(tile), row, unit));
 }
+// 8 bytes, volatile, so that two are not fused into one ds_read2_b64, which takes
+// four times as long
+__device__ __forceinline__ bf16x4 ld_piece(const bf16* p) { return *(lds_bf16x4*)(const_cast<bf16*>(p)); }
 __device__ __forceinline__ bf16x8 ld_unit(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
 
-// A thread's share of a tile on its way to LDS: pairs of neighbouring units.
+// A buffer of `bytes` bytes from p on, for raw 32-bit accesses (the resource's last
+// word says so): loads past it give zero and touch no memory, stores past it are
+// dropped.
+constexpr int kRawBuffer = 0x00020000;
+__device__ __forceinline__ auto buffer_of(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), kRawBuffer);
+}
+constexpr uint32_t kOutside = 0x80000000u;   // no buffer is that long
+
+// A thread's share of a tile on its way to LDS through registers.
 template <int W, int NT>
 struct Staged {
-  static constexpr int kSteps = kLinearChunk * (W / 16) / NT;
-  u32x4 r[kSteps][2];
+  static constexpr int kRows = NT / (W / 8), kSteps = kLinearChunk / kRows;
+  u32x4 r[kSteps];
 
-  __device__ __forceinline__ void load(const Tokens& t, int head, int64_t t0, int valid) {
-    const uint16_t* base = t.p + t0 * t.stride + static_cast<int64_t>(head / t.share) * t.width;
+  // Byte offset of the thread's first unit in the chunk's rows; columns behind the
+  // width are outside.
+  static __device__ __forceinline__ uint32_t offset(const Tokens& t) {
+    const int row = static_cast<int>(threadIdx.x) / (W / 8), c = static_cast<int>(threadIdx.x) % (W / 8);
+    return 8 * c < t.width ? static_cast<uint32_t>(row) * static_cast<uint32_t>(t.stride) * 2 + 16 * c : kOutside;
+  }
+  __device__ __forceinline__ void load(const Tokens& t, uint32_t at, int head, int64_t t0, int valid) {
+    const auto rows = buffer_of(t.p + t0 * t.stride + static_cast<int64_t>(head / t.share) * t.width,
+                                (valid - 1) * t.stride * 2 + t.width * 2);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const int pair = i * NT + static_cast<int>(threadIdx.x), row = pair / (W / 16), s = pair % (W / 16);
-      const uint16_t* p = base + row * t.stride + 16 * s;
-      const u32x4 zero = {0, 0, 0, 0};
-      r[i][0] = row < valid && 16 * s < t.width ? *reinterpret_cast<const u32x4*>(p) : zero;
-      r[i][1] = row < valid && 16 * s + 8 < t.width ? *reinterpret_cast<const u32x4*>(p + 8) : zero;
+      r[i] = __builtin_amdgcn_raw_buffer_load_b128(rows, at + i * (kRows * static_cast<uint32_t>(t.stride) * 2), 0, 0);
     }
   }
-  // SLOTS: the 8-byte pieces 0 1 2 3 of 16 channels as 0 2 1 3, a lane's k slots
-  template <bool SLOTS>
   __device__ __forceinline__ void store(bf16* tile) const {
+    const int row = static_cast<int>(threadIdx.x) / (W / 8), c = static_cast<int>(threadIdx.x) % (W / 8);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) st4(unit_at<W>(tile, i * kRows + row, c), r[i]);
+  }
+};
+
+// A tile on its way from memory to LDS without registers: a wave's copy moves 64
+// 16-byte units to 1 KiB of LDS, lane after lane, so each lane takes the unit whose
+// place its own is.
+template <int W, int NW>
+struct Copy {
+  static constexpr int kRows = 64 / (W / 8);                       // of a copy
+  static constexpr int kSteps = kLinearChunk / kRows / NW;         // of a wave
+  static constexpr int kKinds = W == 128 && NW == 2 ? 2 : 1;       // copies that differ in their units
+  uint32_t at[kKinds], step;
+
+  __device__ __forceinline__ Copy(const Tokens& t, int wave, int lane) : step(kRows * NW * static_cast<uint32_t>(t.stride) * 2) {
+#pragma unroll
+    for (int k = 0; k < kKinds; ++k) {
+      const int row = (k * NW + wave) * kRows + lane / (W / 8), c = (lane % (W / 8)) ^ row_bits<W>(row);
+      at[k] = 8 * c < t.width ? static_cast<uint32_t>(row - k * NW * kRows) * static_cast<uint32_t>(t.stride) * 2 + 16 * c : kOutside;
+    }
+  }
+  // rows behind `valid` become zero
+  __device__ __forceinline__ void start(const Tokens& t, int head, int64_t t0, int valid, bf16* tile, int wave) const {
+    const uint64_t base = reinterpret_cast<uint64_t>(t.p + t0 * t.stride + static_cast<int64_t>(head / t.share) * t.width);
+    u32x4 rows;
+    rows[0] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(base));
+    rows[1] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(base >> 32) & 0xffffu);
+    rows[2] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>((valid - 1) * static_cast<int>(t.stride) * 2 + t.width * 2));
+    rows[3] = kRawBuffer;
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(
+        static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) bf16*)tile)) + wave * 1024);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const int pair = i * NT + static_cast<int>(threadIdx.x), row = pair / (W / 16), s = pair % (W / 16);
-      u32x4 a = r[i][0], b = r[i][1];
-      if (SLOTS) {
-        const u32x4 c = {a[0], a[1], b[0], b[1]}, d = {a[2], a[3], b[2], b[3]};
-        a = c;
-        b = d;
-      }
-      st4(unit_at<W>(tile, row, 2 * s), a);
-      st4(unit_at<W>(tile, row, 2 * s + 1), b);
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                   :: "s"(lds + i * (NW * 1024)), "v"(at[i % kKinds] + i * step), "s"(rows) : "memory", "m0");
     }
   }
 };
+// Waits until at most N of the wave's last memory accesses are under way.
+template <int N>
+__device__ __forceinline__ void copies_done() {
+  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
+}
 
 // Eight tokens row0 .. row0 + 7 of column col0 + lane % 32 (col0, row0 multiples of
 // 32 and 8).
@@ -133,10 +183,31 @@ __device__ __forceinline__ bf16x8 column_tokens(const bf16* tile, int row0, int 
   return join8(lds_read_tr(unit_at<W>(tile, row, unit) + 4 * (s & 1)),
                lds_read_tr(unit_at<W>(tile, row + 4, unit) + 4 * (s & 1)));
 }
+// The same with the second and third four of every 16 columns exchanged: rows of the
+// product are then S's rows as they are kept.
+template <int W>
+__device__ __forceinline__ bf16x8 slot_column_tokens(const bf16* tile, int row0, int col0, int lane) {
+  const int s = lane & 15, n = ((s & 1) << 1) | ((s & 2) >> 1), row = row0 + (s >> 2);
+  const int unit = (col0 >> 3) + 2 * ((lane >> 4) & 1) + (n >> 1);
+  return join8(lds_read_tr(unit_at<W>(tile, row, unit) + 4 * (n & 1)),
+               lds_read_tr(unit_at<W>(tile, row + 4, unit) + 4 * (n & 1)));
+}
+
+// Takes the pair h of bf16 from (a, b), exactly: v_dot2c_f32_bf16 adds products of
+// bf16 to an FP32 value, here -1 and 0 times the pair, and x less its bf16 rounding is
+// an FP32 number.
+struct Minus {
+  bf16x2 first, second;
+  __device__ __forceinline__ Minus() : first(sgpr_bf16x2(0x0000bf80u)), second(sgpr_bf16x2(0xbf800000u)) {}
+  __device__ __forceinline__ void operator()(uint32_t h, float& a, float& b) const {
+    a -= __uint_as_float(h << 16);
+    b -= __uint_as_float(h & 0xffff0000u);
+  }
+};
 
 // x as N bf16 parts, each the rest of those before it rounded.
 template <int N>
-__device__ __forceinline__ void split_parts(const float (&x)[8], bf16x8 (&part)[N]) {
+__device__ __forceinline__ void split_parts(const Minus& minus, const float (&x)[8], bf16x8 (&part)[N]) {
   u32x4 w[N];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -145,8 +216,7 @@ __device__ __forceinline__ void split_parts(const float (&x)[8], bf16x8 (&part)[
     for (int n = 0; n < N; ++n) {
       const uint32_t h = pack_bf16(a, b);
       w[n][i] = h;
-      a -= __uint_as_float(h << 16);
-      b -= __uint_as_float(h & 0xffff0000u);
+      if (n + 1 < N) minus(h, a, b);
     }
   }
 #pragma unroll
@@ -163,12 +233,14 @@ template <int KD, int VD, int PS, int MODE>
 struct LinearSmem {
   static constexpr bool kOut = MODE != kSummary;
   __align__(16) bf16 x[kOut ? kLinearChunk * KD : 8];
-  __align__(16) bf16 y[kLinearChunk * KD];
-  __align__(16) bf16 z[kLinearChunk * VD];
+  __align__(16) bf16 y[MODE == kQuery ? 1 : 2][kLinearChunk * KD];
+  __align__(16) bf16 z[MODE == kSummary ? 2 : 1][kLinearChunk * VD];
   __align__(16) bf16 e[MODE == kQuery ? kLinearChunk * VD : 8];
   __align__(16) bf16 p[kOut ? PS * 3 * 1024 : 8];
-  __align__(16) float high[kLinearChunk], low[kLinearChunk], w_out[kLinearChunk], w_in[kLinearChunk];
-  float whole;
+  struct Gates {
+    __align__(16) float high[kLinearChunk], low[kLinearChunk], w_in[kLinearChunk];
+    float whole;
+  } gates[2];   // of this chunk and the next
   __align__(16) float pairs[MODE == kQuery ? 4 : 1][kLinearChunk];
   float dots[VD / 32][kLinearChunk];
   float by[VD / 32];
@@ -181,7 +253,7 @@ __device__ __forceinline__ void each_quad(const LinearParams& p, int col, int ha
   for (int kt = 0; kt < KD / 32; ++kt) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int row = 32 * kt + 8 * q + 4 * half;
+      const int row = 32 * kt + 16 * (q >> 1) + 8 * half + 4 * (q & 1);
       f(kt, q, row, row < p.KW && col < p.VW);
     }
   }
@@ -219,6 +291,24 @@ __device__ __forceinline__ float wave_suffix(float x, int lane) {
   return x;
 }
 
+// The inclusive prefix sum over the wave's 64 lanes in FP64: within rows of 16 by
+// row shifts, then each row's total broadcast to those behind it.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double prefix_step(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROWS, 0xf, true),
+                 hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROWS, 0xf, true);
+  return x + __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+__device__ __forceinline__ double gate_prefix(double x) {
+  x = prefix_step<0x111, 0xf>(x);
+  x = prefix_step<0x112, 0xf>(x);
+  x = prefix_step<0x114, 0xf>(x);
+  x = prefix_step<0x118, 0xf>(x);
+  x = prefix_step<0x142, 0xa>(x);   // lane 15 to row 1, lane 47 to row 3
+  return prefix_step<0x143, 0xc>(x);   // lane 31 to rows 2 and 3
+}
+
 template <int KD, int VD, int SS, int PS, bool REV, int MODE>
 __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
   constexpr int NT = 2 * VD, NW = VD / 32, KT = KD / 32, US = 3;
@@ -234,8 +324,8 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
   const bool starts = REV ? seq_end : !carried, ends = REV ? !carried : seq_end;
   if (!kOut && ends) return;   // nothing goes on from here
 
-  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
-  const int half = lane >> 5, l32 = lane & 31, l16 = lane & 15, quad = lane >> 4;
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int lane_ = lane, half = lane >> 5, l32 = lane & 31, l16 = lane & 15, quad = lane >> 4;
   const int col = 32 * wave + l32;
   const int64_t size = static_cast<int64_t>(p.KW) * p.VW;
 
@@ -258,53 +348,95 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
   float carry = 0.f;   // kKey: what passes from before the chunk's end to after it
   double total = 0.0;
 
-  Staged<KD, NT> sx, sy;
-  Staged<VD, NT> sz, se;
+  const Minus minus;
+  const Copy<KD, NW> cx(p.x, wave, lane), cy(p.y, wave, lane);
+  Staged<KD, NT> sy;
+  Staged<VD, NT> sz;
+  const uint32_t at_y = MODE == kQuery ? sy.offset(p.y) : 0, at_z = MODE == kQuery ? sz.offset(p.z) : 0;
+  const Copy<VD, NW> cz(p.z, wave, lane), ce(p.e, wave, lane);
+  const uint32_t o_size = p.o_fp32 ? 4 : 2, o_row = static_cast<uint32_t>(p.H) * p.VW * o_size;
+  const uint32_t at_o = l32 * o_row + (32 * wave + 4 * half) * o_size;
   float gate = 0.f;
-  auto fetch = [&](int it) {
-    const int c = REV ? chunks - 1 - it : it;
-    const int64_t t0 = begin + c * kLinearChunk;
-    const int valid = min(kLinearChunk, end - static_cast<int>(t0));
-    if (kOut) sx.load(p.x, head, t0, valid);
-    sy.load(p.y, head, t0, valid);
-    sz.load(p.z, head, t0, valid);
-    if (MODE == kQuery) se.load(p.e, head, t0, valid);
-    if (wave == 0) {
-      const int64_t i = (t0 + lane) * p.g_stride + head;
-      gate = lane < valid ? (p.g_bf16 ? bf2f(static_cast<const uint16_t*>(p.g)[i]) : static_cast<const float*>(p.g)[i]) : 0.f;
-    }
+  // first token of the chunk that is walked as number `it`, and its tokens
+  const auto first_of = [&](int it) { return static_cast<int64_t>(begin) + (REV ? chunks - 1 - it : it) * kLinearChunk; };
+  const auto valid_of = [&](int64_t t0) { return min(kLinearChunk, end - static_cast<int>(t0)); };
+  const auto start_x = [&](int it) {
+    if (!kOut || it >= chunks) return;
+    const int64_t t0 = first_of(it);
+    cx.start(p.x, head, t0, valid_of(t0), sm.x, wave);
+    if (MODE == kQuery) ce.start(p.e, head, t0, valid_of(t0), sm.e, wave);
   };
-  fetch(0);
+  const auto start_y = [&](int it) {
+    if (it >= chunks) return;
+    const int64_t t0 = first_of(it);
+    if constexpr (MODE == kQuery) {   // all four tiles are read to the chunk's end but x and e: no room for two of y
+      sy.load(p.y, at_y, head, t0, valid_of(t0));
+      sz.load(p.z, at_z, head, t0, valid_of(t0));
+    } else
+    cy.start(p.y, head, t0, valid_of(t0), sm.y[it & 1], wave);
+  };
+  const auto start_z = [&](int it) {
+    const int64_t t0 = first_of(it);
+    cz.start(p.z, head, t0, valid_of(t0), sm.z[kOut ? 0 : it & 1], wave);
+  };
+  // the gates are a chunk further ahead: their prefix sums are made beside P
+  auto fetch_gate = [&](int it) {
+    if (wave != 0 || it >= chunks) return;
+    const int64_t t = begin + (REV ? chunks - 1 - it : it) * kLinearChunk + lane, i = t * p.g_stride + head;
+    gate = t < end ? (p.g_bf16 ? bf2f(static_cast<const uint16_t*>(p.g)[i]) : static_cast<const float*>(p.g)[i]) : 0.f;
+  };
+  auto make_gates = [&](int it) {
+    if (wave != 0 || it >= chunks) return;
+    auto& to = sm.gates[it & 1];
+    double G = static_cast<double>(gate) * 1.4426950408889634074;
+    if (G < kLeastGate) G = kLeastGate;   // NaN stays
+    G = gate_prefix(G);
+    const double last = __shfl(G, 63);
+    const double high = rint(G * 512.0) * (1.0 / 512.0);
+    to.high[lane] = static_cast<float>(high);
+    to.low[lane] = static_cast<float>(G - high);
+    to.w_in[lane] = __builtin_amdgcn_exp2f(static_cast<float>(REV ? G : last - G));
+    if (lane == 0) to.whole = __builtin_amdgcn_exp2f(static_cast<float>(last));
+    total += last;
+  };
+  fetch_gate(0);
+  start_y(0);
+  if (kOut) start_x(0);
+  if (!kOut) start_z(0);
+  make_gates(0);
+  fetch_gate(1);
 
   for (int it = 0; it < chunks; ++it) {
     const int c = REV ? chunks - 1 - it : it;
     const int64_t t0 = begin + c * kLinearChunk;
     const int valid = min(kLinearChunk, end - static_cast<int>(t0));
-    block_sync();   // the last chunk's readers
-    if (kOut) sx.template store<true>(sm.x);
-    sy.template store<false>(sm.y);
-    sz.template store<false>(sm.z);
-    if (MODE == kQuery) se.template store<false>(sm.e);
-    if (wave == 0) {
-      double G = static_cast<double>(gate) * 1.4426950408889634074;
-      if (G < kLeastGate) G = kLeastGate;   // NaN stays
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const double y = __shfl_up(G, d);
-        if (lane >= d) G += y;
-      }
-      const double last = __shfl(G, 63);
-      const double high = rint(G * 512.0) * (1.0 / 512.0);
-      const float since = __builtin_amdgcn_exp2f(static_cast<float>(G)), until = __builtin_amdgcn_exp2f(static_cast<float>(last - G));
-      sm.high[lane] = static_cast<float>(high);
-      sm.low[lane] = static_cast<float>(G - high);
-      sm.w_out[lane] = REV ? until : since;
-      sm.w_in[lane] = REV ? since : until;
-      if (lane == 0) sm.whole = __builtin_amdgcn_exp2f(static_cast<float>(last));
-      total += last;
+    // the LDS addresses of a chunk are made anew: all of them kept would not fit
+    if (MODE == kQuery || MODE == kKey) {
+      lane_ = opaque(lane);
+      half = lane_ >> 5, l32 = lane_ & 31, l16 = lane_ & 15, quad = lane_ >> 4;
     }
-    block_sync();
-    if (it + 1 < chunks) fetch(it + 1);
+    const int Y = MODE == kQuery ? 0 : it & 1, Z = kOut ? 0 : it & 1;
+    if constexpr (MODE == kQuery) {
+      block_sync();   // the last chunk's readers
+      sy.store(sm.y[0]);
+      sz.store(sm.z[0]);
+      copies_done<0>();   // x, e
+      block_sync();
+    } else {
+      // x, y (kSummary: y, z), while the last chunk's stores go on
+      if (!kOut || it == 0) {
+        copies_done<0>();
+      } else {
+        copies_done<4>();
+      }
+      block_sync();   // everyone's; and the last chunk's readers are done
+      if (kOut) start_z(it);
+    }
+    start_y(it + 1);
+    if (!kOut && it + 1 < chunks) start_z(it + 1);
+    make_gates(it + 1);
+    fetch_gate(it + 2);
+    const auto& gates = sm.gates[it & 1];
 
     f32x16 out[2];
     if constexpr (kOut) {
@@ -319,9 +451,27 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
 #pragma unroll
           for (int s = 0; s < VD / 32; ++s) ef[s] = ld_unit(unit_at<VD>(sm.e, 16 * a + l16, 4 * s + quad));
         }
-        const float high = sm.high[16 * a + l16], low = sm.low[16 * a + l16];
+        const float high = gates.high[16 * a + l16], low = gates.low[16 * a + l16];
         float before = 0.f;   // kQuery: the pairs' sum over the tiles so far
-        for (int b = REV ? (a & 2) : 0; b < (REV ? 4 : (a | 1) + 1); ++b) {
+        // the products of all four tiles, also where none is needed: other waves
+        // need all of theirs meanwhile
+        f32x4 acc[4], m[MODE == kQuery ? 4 : 1];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          acc[b] = zero4();
+#pragma unroll
+          for (int s = 0; s < KD / 32; ++s) {
+            acc[b] = mfma16(ld_unit(unit_at<KD>(sm.y[Y], 16 * b + l16, 4 * s + quad)), xf[s], acc[b]);
+          }
+          if constexpr (MODE == kQuery) {
+            m[b] = zero4();
+#pragma unroll
+            for (int s = 0; s < VD / 32; ++s) m[b] = mfma16(ld_unit(unit_at<VD>(sm.z[Z], 16 * b + l16, 4 * s + quad)), ef[s], m[b]);
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          if (REV ? b < (a & 2) : b > (a | 1)) continue;
           const int block = (a >> 1) + (b >> 1), row = 16 * (a & 1) + l16, unit = 2 * (b & 1) + (quad >> 1);
           if (REV ? b < a : b > a) {   // the empty corner of a block on the diagonal
             const bf16x4 zero = {0, 0, 0, 0};
@@ -329,31 +479,20 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
             for (int s = 0; s < PS; ++s) *reinterpret_cast<bf16x4*>(p_unit(sm.p + s * 3072, block, row, unit) + 4 * (quad & 1)) = zero;
             continue;
           }
-          f32x4 acc = zero4();
-#pragma unroll
-          for (int s = 0; s < KD / 32; ++s) {
-            const int g16 = 2 * s + (quad >> 1), h8 = 4 * (quad & 1);
-            const bf16x4 lo = *reinterpret_cast<const bf16x4*>(unit_at<KD>(sm.y, 16 * b + l16, 2 * g16) + h8);
-            const bf16x4 hi = *reinterpret_cast<const bf16x4*>(unit_at<KD>(sm.y, 16 * b + l16, 2 * g16 + 1) + h8);
-            acc = mfma16(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), xf[s], acc);
-          }
-          const f32x4 high_j = ld4(sm.high + 16 * b + 4 * quad), low_j = ld4(sm.low + 16 * b + 4 * quad);
+          const f32x4 high_j = ld4(gates.high + 16 * b + 4 * quad), low_j = ld4(gates.low + 16 * b + 4 * quad);
           float w[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float e = REV ? (high_j[r] - high) + (low_j[r] - low) : (high - high_j[r]) + (low - low_j[r]);
             const int j = 4 * quad + r;
             const bool keep = a != b || (REV ? j >= l16 : j <= l16);
-            w[r] = keep ? acc[r] * __builtin_amdgcn_exp2f(e) : 0.f;
+            w[r] = keep ? acc[b][r] * __builtin_amdgcn_exp2f(e) : 0.f;
           }
           if constexpr (MODE == kQuery) {
             // pairs (i, j < i): sums over j < t for every t <= i of the tile, then over i
-            f32x4 m = zero4();
-#pragma unroll
-            for (int s = 0; s < VD / 32; ++s) m = mfma16(ld_unit(unit_at<VD>(sm.z, 16 * b + l16, 4 * s + quad)), ef[s], m);
             float pair[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) pair[r] = a != b || 4 * quad + r < l16 ? m[r] * w[r] : 0.f;
+            for (int r = 0; r < 4; ++r) pair[r] = a != b || 4 * quad + r < l16 ? m[b][r] * w[r] : 0.f;
             float incl = (pair[0] + pair[1]) + (pair[2] + pair[3]);
             float y = __shfl_up(incl, 16);
             if (quad >= 1) incl += y;
@@ -377,8 +516,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               h[i] = pack_bf16(left[2 * i], left[2 * i + 1]);
-              left[2 * i] -= __uint_as_float(h[i] << 16);
-              left[2 * i + 1] -= __uint_as_float(h[i] & 0xffff0000u);
+              if (s + 1 < PS) minus(h[i], left[2 * i], left[2 * i + 1]);
             }
             *reinterpret_cast<u32x2*>(p_unit(sm.p + s * 3072, block, row, unit) + 4 * (quad & 1)) = h;
           }
@@ -394,7 +532,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
           float v[8];
           tile_kslots(S[kt], s, v);
           bf16x8 part[SS];
-          split_parts<SS>(v, part);
+          split_parts<SS>(minus, v, part);
 #pragma unroll
           for (int ib = 0; ib < 2; ++ib) {
             const bf16x8 xf = ld_unit(unit_at<KD>(sm.x, 32 * ib + l32, 2 * (2 * kt + s) + half));
@@ -405,7 +543,8 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
       }
 #pragma unroll
       for (int ib = 0; ib < 2; ++ib) {
-        const float w = sm.w_out[32 * ib + l32];
+        const float high = gates.high[32 * ib + l32], low = gates.low[32 * ib + l32];
+        const float w = __builtin_amdgcn_exp2f(REV ? (gates.high[63] - high) + (gates.low[63] - low) : high + low);
 #pragma unroll
         for (int i = 0; i < 16; ++i) out[ib][i] *= w;
       }
@@ -445,17 +584,26 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
             const f32x4 v = load_quad(p, with, row, col);
 #pragma unroll
             for (int j = 0; j < 4; ++j) dot += v[j] * S[kt][4 * q + j];
+            if (q == 3) asm volatile("" ::: "memory");   // a tile's loads at a time
           });
         }
         dot = sum64(dot);
         if (lane == 0) sm.by[wave] = dot;
       }
-      block_sync();   // P, dots and pairs are whole
+      if constexpr (MODE != kQuery) {   // z; y's copies may go on
+        if (it + 1 < chunks) {
+          copies_done<Copy<KD, NW>::kSteps>();
+        } else {
+          copies_done<0>();
+        }
+      }
+      block_sync();   // P, dots, pairs and z are whole
+      start_x(it + 1);
     }
 
     bf16x8 zf[4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) zf[s] = column_tokens<VD>(sm.z, 16 * s + 8 * half, 32 * wave, lane);
+    for (int s = 0; s < 4; ++s) zf[s] = column_tokens<VD>(sm.z[Z], 16 * s + 8 * half, 32 * wave, lane_);
     if constexpr (kOut) {
 #pragma unroll
       for (int ib = 0; ib < 2; ++ib) {
@@ -471,7 +619,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
       }
     }
     // the state after the chunk
-    const float whole = sm.whole;
+    const float whole = gates.whole;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
@@ -480,7 +628,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const u32x4 raw = __builtin_bit_cast(u32x4, zf[s]);
-      const f32x4 w0 = ld4(sm.w_in + 16 * s + 8 * half), w1 = ld4(sm.w_in + 16 * s + 8 * half + 4);
+      const f32x4 w0 = ld4(gates.w_in + 16 * s + 8 * half), w1 = ld4(gates.w_in + 16 * s + 8 * half + 4);
       float v[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -488,29 +636,36 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
         v[2 * i + 1] = __uint_as_float(raw[i] & 0xffff0000u) * (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]);
       }
       bf16x8 part[US];
-      split_parts<US>(v, part);
+      split_parts<US>(minus, v, part);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
-        const bf16x8 yf = column_tokens<KD>(sm.y, 16 * s + 8 * half, 32 * kt, lane);
+        const bf16x8 yf = slot_column_tokens<KD>(sm.y[Y], 16 * s + 8 * half, 32 * kt, lane_);
 #pragma unroll
         for (int n = 0; n < US; ++n) S[kt] = mfma(yf, part[n], S[kt]);
       }
     }
     if constexpr (kOut) {
+      const auto rows = buffer_of(static_cast<char*>(p.o) + (t0 * p.H + head) * p.VW * o_size, static_cast<int64_t>(valid) * o_row);
 #pragma unroll
       for (int ib = 0; ib < 2; ++ib) {
-        const int t = 32 * ib + l32;
-        const int64_t at = ((t0 + t) * p.H + head) * p.VW;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int ch = 32 * wave + 8 * q + 4 * half;
-          if (t >= valid || ch >= p.VW) continue;
+        for (int q = 0; q < 4; q += 2) {
+          const uint32_t at = 32 * ib * o_row + 8 * q * o_size;
           if (p.o_fp32) {
-            const f32x4 v = {out[ib][4 * q], out[ib][4 * q + 1], out[ib][4 * q + 2], out[ib][4 * q + 3]};
-            st4(static_cast<float*>(p.o) + at + ch, v);
+#pragma unroll
+            for (int n = q; n < q + 2; ++n) {
+              const f32x4 v = {out[ib][4 * n], out[ib][4 * n + 1], out[ib][4 * n + 2], out[ib][4 * n + 3]};
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rows, 32 * wave + 8 * n < p.VW ? at_o + at + 32 * (n - q) : kOutside, 0, 0);
+            }
           } else {
-            const u32x2 v = {pack_bf16(out[ib][4 * q], out[ib][4 * q + 1]), pack_bf16(out[ib][4 * q + 2], out[ib][4 * q + 3])};
-            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.o) + at + ch) = v;
+            // channels 0 .. 7 of 16 to the lower half's lane of a token, 8 .. 15 to the upper's
+            u32x2 lo = {pack_bf16(out[ib][4 * q], out[ib][4 * q + 1]), pack_bf16(out[ib][4 * q + 4], out[ib][4 * q + 5])};
+            u32x2 hi = {pack_bf16(out[ib][4 * q + 2], out[ib][4 * q + 3]), pack_bf16(out[ib][4 * q + 6], out[ib][4 * q + 7])};
+            lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(lo[0], lo[1], false, false));
+            hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(hi[0], hi[1], false, false));
+            const u32x4 v = {lo[0], hi[0], lo[1], hi[1]};
+            const uint32_t where = 32 * wave + 8 * q + 8 * half < p.VW ? at_o + at + 8 * half : kOutside;
+            __builtin_amdgcn_raw_buffer_store_b128(v, rows, where, 0, 0);
           }
         }
       }
@@ -534,7 +689,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
             float by = sm.by[0];
 #pragma unroll
             for (int w = 1; w < NW; ++w) by += sm.by[w];
-            p.anchor[static_cast<int64_t>(f) * p.H + head] = sm.whole * by;
+            p.anchor[static_cast<int64_t>(f) * p.H + head] = gates.whole * by;
           }
         } else {
           const float upto = wave_prefix(dot, lane);
@@ -547,7 +702,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
             by = sm.by[0];
 #pragma unroll
             for (int w = 1; w < NW; ++w) by += sm.by[w];
-            by *= sm.whole;
+            by *= gates.whole;
           }
           if (lane < valid) {
             const float d = p.dg_part[at] + given + by;

@@ -666,8 +666,9 @@ size_t kda_scan_workspace_bytes(const kda_plan* plan, int32_t D);
  * where S before a sequence's first token is its initial state.
  *   q              [T, Hq, K], k [T, Hk, K], v [T, Hv, V] bf16, each with its
  *                  own token stride, a multiple of 8 elements
- *                  (KDA_ERR_MISALIGNED)
- *   heads          H is a multiple of Hq, Hk and Hv (KDA_ERR_INVALID_ARG); head
+ *                  (KDA_ERR_MISALIGNED), at most 2^22 (KDA_ERR_UNSUPPORTED)
+ *   heads          H, at most 16384 (KDA_ERR_UNSUPPORTED), is a multiple of Hq,
+ *                  Hk and Hv (KDA_ERR_INVALID_ARG); head
  *                  h reads q head h / (H / Hq), k head h / (H / Hk) and v head
  *                  h / (H / Hv)
  *   K, V           multiples of 8, at most 128 (KDA_ERR_UNSUPPORTED)
