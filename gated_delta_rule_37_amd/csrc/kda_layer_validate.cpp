@@ -393,7 +393,10 @@ int check_linear(const LinearArgs& a, bool backward) {
                     check_stride(a.v, static_cast<int64_t>(v_row)), fixed ? KDA_OK : check_stride(a.g, a.H)});
   if (st != KDA_OK) return st;
   // byte offsets inside a chunk of 64 tokens stay below 2^31
-  if (a.q.stride > kMaxScanStride || a.k.stride > kMaxScanStride || a.v.stride > kMaxScanStride) return KDA_ERR_UNSUPPORTED;
+  if (a.q.stride > kMaxScanStride || a.k.stride > kMaxScanStride || a.v.stride > kMaxScanStride ||
+      a.g.stride > kMaxScanStride) {
+    return KDA_ERR_UNSUPPORTED;
+  }
   if (a.H > kMaxLinearHeads) return KDA_ERR_UNSUPPORTED;
   st = check_buffers({{a.plan_dev.ptr, a.plan_dev.bytes, a.plan->blob.size() * sizeof(int32_t), false},
                       {a.q.ptr, a.q.bytes, rows_need(a.q, T, q_row, 2), false},

@@ -325,7 +325,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
   if (!kOut && ends) return;   // nothing goes on from here
 
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int lane_ = lane, half = lane >> 5, l32 = lane & 31, l16 = lane & 15, quad = lane >> 4;
+  const int half = lane >> 5, l32 = lane & 31, l16 = lane & 15, quad = lane >> 4;
   const int col = 32 * wave + l32;
   const int64_t size = static_cast<int64_t>(p.KW) * p.VW;
 
@@ -356,7 +356,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
   const Copy<VD, NW> cz(p.z, wave, lane), ce(p.e, wave, lane);
   const uint32_t o_size = p.o_fp32 ? 4 : 2, o_row = static_cast<uint32_t>(p.H) * p.VW * o_size;
   const uint32_t at_o = l32 * o_row + (32 * wave + 4 * half) * o_size;
-  float gate = 0.f;
+  const uint32_t at_key = l32 * static_cast<uint32_t>(p.e.stride) * 2 + (32 * wave + 4 * half) * 2;
   // first token of the chunk that is walked as number `it`, and its tokens
   const auto first_of = [&](int it) { return static_cast<int64_t>(begin) + (REV ? chunks - 1 - it : it) * kLinearChunk; };
   const auto valid_of = [&](int64_t t0) { return min(kLinearChunk, end - static_cast<int>(t0)); };
@@ -372,23 +372,65 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
     if constexpr (MODE == kQuery) {   // all four tiles are read to the chunk's end but x and e: no room for two of y
       sy.load(p.y, at_y, head, t0, valid_of(t0));
       sz.load(p.z, at_z, head, t0, valid_of(t0));
-    } else
-    cy.start(p.y, head, t0, valid_of(t0), sm.y[it & 1], wave);
+    } else {
+      cy.start(p.y, head, t0, valid_of(t0), sm.y[it & 1], wave);
+    }
   };
   const auto start_z = [&](int it) {
     const int64_t t0 = first_of(it);
     cz.start(p.z, head, t0, valid_of(t0), sm.z[kOut ? 0 : it & 1], wave);
   };
-  // the gates are a chunk further ahead: their prefix sums are made beside P
-  auto fetch_gate = [&](int it) {
+  // What comes through registers: wave 0's gates, two chunks ahead as their prefix
+  // sums are made beside P; for kKey a lane's channels of k and, in wave 0, what
+  // kQuery left of the gates' gradient.  The compiler does not know of the copies, so
+  // it would wait for all of them before it uses such a value; `landed` uses them
+  // where the copies before them have been waited for anyway.
+  uint32_t gate = 0, part = 0, rho = 0;
+  u32x2 key[MODE == kKey ? 8 : 1];
+  const auto fetch_gate = [&](int it) {
     if (wave != 0 || it >= chunks) return;
-    const int64_t t = begin + (REV ? chunks - 1 - it : it) * kLinearChunk + lane, i = t * p.g_stride + head;
-    gate = t < end ? (p.g_bf16 ? bf2f(static_cast<const uint16_t*>(p.g)[i]) : static_cast<const float*>(p.g)[i]) : 0.f;
+    const int64_t t0 = first_of(it), size = p.g_bf16 ? 2 : 4;
+    const auto rows = buffer_of(static_cast<const char*>(p.g) + (t0 * p.g_stride + head) * size,
+                                (valid_of(t0) - 1) * p.g_stride * size + size);
+    const uint32_t at = lane * static_cast<uint32_t>(p.g_stride) * static_cast<uint32_t>(size);
+    if (p.g_bf16) {
+      gate = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(rows, at, 0, 0));
+    } else {
+      gate = __builtin_amdgcn_raw_buffer_load_b32(rows, at, 0, 0);
+    }
   };
-  auto make_gates = [&](int it) {
+  const auto fetch_key = [&](int it) {
+    if constexpr (MODE == kKey) {
+      if (it >= chunks) return;
+      const int64_t t0 = first_of(it);
+      const int valid = valid_of(t0);
+      const auto rows = buffer_of(p.e.p + t0 * p.e.stride + static_cast<int64_t>(head / p.e.share) * p.e.width,
+                                  (valid - 1) * p.e.stride * 2 + p.e.width * 2);
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const uint32_t at = at_key + 32 * (n >> 2) * static_cast<uint32_t>(p.e.stride) * 2 + 16 * (n & 3);
+        key[n] = __builtin_amdgcn_raw_buffer_load_b64(rows, 32 * wave + 8 * (n & 3) < p.VW ? at : kOutside, 0, 0);
+      }
+      if (wave == 0) {
+        const int64_t slot = static_cast<int64_t>(begin / kLinearChunk) + f + (chunks - 1 - it);
+        part = __builtin_amdgcn_raw_buffer_load_b32(buffer_of(p.dg_part + t0 * p.H + head, (static_cast<int64_t>(valid) - 1) * p.H * 4 + 4),
+                                                    lane * p.H * 4, 0, 0);
+        rho = __builtin_amdgcn_raw_buffer_load_b32(buffer_of(p.rho + slot * p.H + head, 4), 0, 0, 0);
+      }
+    }
+  };
+  const auto landed = [&] {
+    asm volatile("" : "+v"(gate), "+v"(part), "+v"(rho));
+    if constexpr (MODE == kKey) {
+#pragma unroll
+      for (int n = 0; n < 8; ++n) asm volatile("" : "+v"(key[n]));
+    }
+  };
+  const auto make_gates = [&](int it) {
     if (wave != 0 || it >= chunks) return;
     auto& to = sm.gates[it & 1];
-    double G = static_cast<double>(gate) * 1.4426950408889634074;
+    const float g = lane < valid_of(first_of(it)) ? __uint_as_float(p.g_bf16 ? gate << 16 : gate) : 0.f;
+    double G = static_cast<double>(g) * 1.4426950408889634074;
     if (G < kLeastGate) G = kLeastGate;   // NaN stays
     G = gate_prefix(G);
     const double last = __shfl(G, 63);
@@ -400,27 +442,24 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
     total += last;
   };
   fetch_gate(0);
+  make_gates(0);
+  fetch_gate(1);
+  fetch_key(0);
   start_y(0);
   if (kOut) start_x(0);
   if (!kOut) start_z(0);
-  make_gates(0);
-  fetch_gate(1);
 
   for (int it = 0; it < chunks; ++it) {
     const int c = REV ? chunks - 1 - it : it;
     const int64_t t0 = begin + c * kLinearChunk;
     const int valid = min(kLinearChunk, end - static_cast<int>(t0));
-    // the LDS addresses of a chunk are made anew: all of them kept would not fit
-    if (MODE == kQuery || MODE == kKey) {
-      lane_ = opaque(lane);
-      half = lane_ >> 5, l32 = lane_ & 31, l16 = lane_ & 15, quad = lane_ >> 4;
-    }
     const int Y = MODE == kQuery ? 0 : it & 1, Z = kOut ? 0 : it & 1;
     if constexpr (MODE == kQuery) {
       block_sync();   // the last chunk's readers
       sy.store(sm.y[0]);
       sz.store(sm.z[0]);
       copies_done<0>();   // x, e
+      landed();
       block_sync();
     } else {
       // x, y (kSummary: y, z), while the last chunk's stores go on
@@ -429,6 +468,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
       } else {
         copies_done<4>();
       }
+      landed();
       block_sync();   // everyone's; and the last chunk's readers are done
       if (kOut) start_z(it);
     }
@@ -438,6 +478,8 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
     fetch_gate(it + 2);
     const auto& gates = sm.gates[it & 1];
 
+    // wave 0 needs this chunk's parts at its end
+    const float left = __uint_as_float(part), taken = __uint_as_float(rho);
     f32x16 out[2];
     if constexpr (kOut) {
       // P: tiles of 16 out tokens (columns) by 16 tokens of the sum (rows)
@@ -560,8 +602,8 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
             bf16x4 v = {0, 0, 0, 0};
             if constexpr (MODE == kQuery) {
               v = *reinterpret_cast<const bf16x4*>(unit_at<VD>(sm.e, t, ch >> 3) + 4 * half);
-            } else if (t < valid && ch < p.VW) {
-              v = *reinterpret_cast<const bf16x4*>(p.e.p + (t0 + t) * p.e.stride + static_cast<int64_t>(head / p.e.share) * p.e.width + ch);
+            } else {
+              v = __builtin_bit_cast(bf16x4, key[4 * ib + q]);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) dot += static_cast<float>(v[j]) * out[ib][4 * q + j];
@@ -579,9 +621,10 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
         float dot = 0.f;
         if (with != nullptr) {
           with += (static_cast<int64_t>(ends ? seq : seg) * p.H + head) * size;
-          each_quad<KD>(p, col, half, [&](int kt, int q, int row, bool has) {
+          const int at = opaque(col);   // its addresses are not kept over the chunks
+          each_quad<KD>(p, at, opaque(half), [&](int kt, int q, int row, bool has) {
             if (!has) return;
-            const f32x4 v = load_quad(p, with, row, col);
+            const f32x4 v = load_quad(p, with, row, at);
 #pragma unroll
             for (int j = 0; j < 4; ++j) dot += v[j] * S[kt][4 * q + j];
             if (q == 3) asm volatile("" ::: "memory");   // a tile's loads at a time
@@ -599,11 +642,12 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
       }
       block_sync();   // P, dots, pairs and z are whole
       start_x(it + 1);
+      fetch_key(it + 1);
     }
 
     bf16x8 zf[4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) zf[s] = column_tokens<VD>(sm.z[Z], 16 * s + 8 * half, 32 * wave, lane_);
+    for (int s = 0; s < 4; ++s) zf[s] = column_tokens<VD>(sm.z[Z], 16 * s + 8 * half, 32 * wave, lane);
     if constexpr (kOut) {
 #pragma unroll
       for (int ib = 0; ib < 2; ++ib) {
@@ -639,7 +683,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
       split_parts<US>(minus, v, part);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
-        const bf16x8 yf = slot_column_tokens<KD>(sm.y[Y], 16 * s + 8 * half, 32 * kt, lane_);
+        const bf16x8 yf = slot_column_tokens<KD>(sm.y[Y], 16 * s + 8 * half, 32 * kt, lane);
 #pragma unroll
         for (int n = 0; n < US; ++n) S[kt] = mfma(yf, part[n], S[kt]);
       }
@@ -705,14 +749,14 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
             by *= gates.whole;
           }
           if (lane < valid) {
-            const float d = p.dg_part[at] + given + by;
+            const float d = left + given + by;
             if (p.dg_bf16) {
               static_cast<uint16_t*>(p.dg)[at] = static_cast<uint16_t>(pack_bf16(d, 0.f));
             } else {
               static_cast<float*>(p.dg)[at] = d;
             }
           }
-          carry = by + p.rho[slot];
+          carry = by + taken;
         }
       }
     }

@@ -672,9 +672,9 @@ size_t kda_scan_workspace_bytes(const kda_plan* plan, int32_t D);
  *                  h reads q head h / (H / Hq), k head h / (H / Hk) and v head
  *                  h / (H / Hv)
  *   K, V           multiples of 8, at most 128 (KDA_ERR_UNSUPPORTED)
- *   g              g_dtype (kda_dtype), [T, H] with a token stride, or [H], the
- *                  same for every token, with g_stride 0; g <= 0, finite or
- *                  -inf (exp(-inf) = 0 forgets the state)
+ *   g              g_dtype (kda_dtype), [T, H] with a token stride of at most
+ *                  2^22, or [H], the same for every token, with g_stride 0;
+ *                  g <= 0, finite or -inf (exp(-inf) = 0 forgets the state)
  *   initial_state  [N, H, K, V] FP32 or NULL (zero)
  *   o              [T, H, V] in o_format; final_state [N, H, K, V] FP32
  * The plan's pieces (its segments, if it has none) run in parallel and change
