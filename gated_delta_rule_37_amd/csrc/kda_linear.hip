@@ -12,27 +12,26 @@
 
 namespace kda {
 
-int launch_linear_pass(void (*kernel)(LinearParams), const LinearParams& p, int32_t fragments, hipStream_t stream) {
-  const int32_t threads = p.VW > 64 ? 256 : 128;
-  const int64_t blocks = static_cast<int64_t>(fragments) * p.H;
-  if (blocks * threads > 2147483647LL) return KDA_ERR_UNSUPPORTED;
+namespace {
+
+// One pass over all fragments and heads.
+int launch_pass(void (*kernel)(LinearParams), const LinearParams& p, int32_t fragments, hipStream_t stream) {
   (void)hipGetLastError();
-  hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(blocks)), dim3(threads), 0, stream, p);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(fragments) * static_cast<uint32_t>(p.H)), dim3(kLinearThreads), 0, stream, p);
   return finish_launch();
 }
 
-namespace {
-
-// The state before every piece that goes on within its sequence (reversed: the
-// cotangent after every piece whose sequence goes on), in place of the pieces'
-// own updates.  A thread has four elements of one head's state.
-template <bool REV>
+// The state before every piece that goes on within its sequence and, with
+// blockIdx.z 1, the cotangent after every piece whose sequence goes on, in place of
+// the pieces' own updates.  A thread has four elements of one head's state.
 __global__ __launch_bounds__(kRowThreads) void linear_scan_kernel(const int32_t* plan, BlobLayout L, int32_t P, int32_t H,
-                                                                  int32_t quads, const float* decays, float* states) {
+                                                                  int32_t quads, const float* decays, float* states,
+                                                                  float* cotangents) {
+  const bool rev = blockIdx.z != 0;
   const int32_t i = static_cast<int32_t>(blockIdx.x) * kRowThreads + static_cast<int32_t>(threadIdx.x);
   const int32_t head = static_cast<int32_t>(blockIdx.y);
   if (i >= quads) return;
-  float* const own = states + (static_cast<int64_t>(head) * quads + i) * 4;
+  float* const own = (rev ? cotangents : states) + (static_cast<int64_t>(head) * quads + i) * 4;
   const int64_t step = static_cast<int64_t>(H) * quads * 4;
   f32x4 state = zero4();
   // eight pieces' updates in flight; those that were not made are read and dropped
@@ -42,18 +41,18 @@ __global__ __launch_bounds__(kRowThreads) void linear_scan_kernel(const int32_t*
     float decay[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int32_t n = min(n0 + i, P - 1), r = REV ? P - 1 - n : n;
+      const int32_t n = min(n0 + i, P - 1), r = rev ? P - 1 - n : n;
       update[i] = ld4(own + r * step);
       decay[i] = decays[static_cast<int64_t>(r) * H + head];
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (n0 + i >= P) break;
-      const int32_t r = REV ? P - 1 - n0 - i : n0 + i;
+      const int32_t r = rev ? P - 1 - n0 - i : n0 + i;
       const bool before = plan[L.seg_carry_in + r] != 0, after = r + 1 < P && plan[L.seg_carry_in + r + 1] != 0;
       const bool through = before && after && plan[L.seg_transition_live + r] != 0;
-      const bool has = REV ? before : after;   // the piece's update was made
-      if (REV ? after : before) st4(own + r * step, state);
+      const bool has = rev ? before : after;   // the piece's update was made
+      if (rev ? after : before) st4(own + r * step, state);
       state = has ? (through ? decay[i] * state + update[i] : update[i]) : zero4();
     }
   }
@@ -120,34 +119,49 @@ LinearParams pass_of(const LinearArgs& a, int32_t KW, int32_t VW) {
   return p;
 }
 
-template <bool REV>
-int launch_scan_states(const LinearArgs& a, const float* decays, float* states, hipStream_t stream) {
-  const int32_t quads = a.K * a.V / 4;
-  hipLaunchKernelGGL(linear_scan_kernel<REV>, dim3((quads + kRowThreads - 1) / kRowThreads, a.H), dim3(kRowThreads), 0, stream,
-                     static_cast<const int32_t*>(a.plan_dev.ptr), a.plan->layout, a.plan->P, a.H, quads, decays, states);
-  return finish_launch();
-}
-
-// The states before the pieces, in ws.
-int launch_piece_states(const LinearArgs& a, float* states, float* decays, hipStream_t stream) {
+// The states before the pieces and, where asked for, the cotangents after them.
+int launch_piece_states(const LinearArgs& a, float* states, float* decays, const Tokens* d_o, float* cotangents, hipStream_t stream) {
   LinearParams p = pass_of(a, a.K, a.V);
   p.y = tokens_of(a.k, a.H, a.Hk, a.K);
   p.z = tokens_of(a.v, a.H, a.Hv, a.V);
   p.seq_state = static_cast<const float*>(a.initial_state.ptr);
   p.piece_out = states;
   p.decay_out = decays;
-  const int st = launch_linear_pass(linear_kernel_of<2, 2, false, kSummary>(a.K, a.V), p, a.plan->F, stream);
-  return st != KDA_OK ? st : launch_scan_states<false>(a, decays, states, stream);
+  LinearParams r = p;
+  if (d_o != nullptr) {
+    r.y = tokens_of(a.q, a.H, a.Hq, a.K);
+    r.z = *d_o;
+    r.seq_state = static_cast<const float*>(a.d_final.ptr);
+    r.piece_out = cotangents;
+    r.decay_out = nullptr;   // the same as p's
+    r.reversed = 1;
+  }
+  void (*kernel)(LinearParams, LinearParams) =
+      a.K > 64 ? (a.V > 64 ? linear_summary_kernel<128, 128> : linear_summary_kernel<128, 64>)
+               : (a.V > 64 ? linear_summary_kernel<64, 128> : linear_summary_kernel<64, 64>);
+  const uint32_t both = d_o != nullptr ? 2 : 1;
+  (void)hipGetLastError();
+  hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(a.plan->F) * static_cast<uint32_t>(a.H), both), dim3(kLinearThreads), 0,
+                     stream, p, r);
+  const int st = finish_launch();
+  if (st != KDA_OK) return st;
+  const int32_t quads = a.K * a.V / 4;
+  hipLaunchKernelGGL(linear_scan_kernel, dim3((quads + kRowThreads - 1) / kRowThreads, a.H, both), dim3(kRowThreads), 0, stream,
+                     p.plan, a.plan->layout, a.plan->P, a.H, quads, decays, states, cotangents);
+  return finish_launch();
 }
+
+bool too_many(const LinearArgs& a) { return static_cast<int64_t>(a.plan->F) * a.H * kLinearThreads > 2147483647LL; }
 
 }  // namespace
 
 int launch_linear(const LinearArgs& a, hipStream_t stream) {
+  if (too_many(a)) return KDA_ERR_UNSUPPORTED;
   const LinearLayout L = linear_layout(a.plan, a.H, a.K, a.V);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace.ptr);
   float *states = reinterpret_cast<float*>(ws + L.states), *decays = reinterpret_cast<float*>(ws + L.decays);
   if (a.plan->F > a.plan->N) {
-    const int st = launch_piece_states(a, states, decays, stream);
+    const int st = launch_piece_states(a, states, decays, nullptr, nullptr, stream);
     if (st != KDA_OK) return st;
   }
   LinearParams p = pass_of(a, a.K, a.V);
@@ -159,11 +173,12 @@ int launch_linear(const LinearArgs& a, hipStream_t stream) {
   p.seq_out = static_cast<float*>(a.final_state.ptr);
   p.o = a.o.ptr;
   p.o_fp32 = a.o_format == KDA_FP32 ? 1 : 0;
-  return launch_linear_pass(p.o_fp32 ? linear_kernel_of<3, 3, false, kOutput>(a.K, a.V) : linear_kernel_of<2, 2, false, kOutput>(a.K, a.V),
-                            p, a.plan->F, stream);
+  return launch_pass(p.o_fp32 ? linear_kernel_of<3, 3, false, kOutput>(a.K, a.V) : linear_kernel_of<2, 2, false, kOutput>(a.K, a.V),
+                     p, a.plan->F, stream);
 }
 
 int launch_linear_backward(const LinearArgs& a, hipStream_t stream) {
+  if (too_many(a)) return KDA_ERR_UNSUPPORTED;
   const LinearBwdLayout L = linear_bwd_layout(a);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace.ptr);
   auto at = [ws](size_t offset) { return reinterpret_cast<float*>(ws + offset); };
@@ -172,16 +187,9 @@ int launch_linear_backward(const LinearArgs& a, hipStream_t stream) {
   const Tokens q = tokens_of(a.q, a.H, a.Hq, a.K), k = tokens_of(a.k, a.H, a.Hk, a.K), v = tokens_of(a.v, a.H, a.Hv, a.V),
                d = tokens_of(d_o, a.H, a.H, a.V);
   const float *h0 = static_cast<const float*>(a.initial_state.ptr), *d_final = static_cast<const float*>(a.d_final.ptr);
+  int st = KDA_OK;
   if (cut) {
-    int st = launch_piece_states(a, at(L.states), at(L.decays), stream);
-    if (st != KDA_OK) return st;
-    LinearParams p = pass_of(a, a.K, a.V);
-    p.y = q;
-    p.z = d;
-    p.seq_state = d_final;
-    p.piece_out = at(L.cotangents);
-    st = launch_linear_pass(linear_kernel_of<2, 2, true, kSummary>(a.K, a.V), p, a.plan->F, stream);
-    if (st == KDA_OK) st = launch_scan_states<true>(a, at(L.decays), at(L.cotangents), stream);
+    st = launch_piece_states(a, at(L.states), at(L.decays), &d, at(L.cotangents), stream);
     if (st != KDA_OK) return st;
   }
   // each of the gradients: heads that share a row are added in a launch of their own
@@ -189,7 +197,7 @@ int launch_linear_backward(const LinearArgs& a, hipStream_t stream) {
     const bool shared = heads != a.H;
     p.o = shared ? static_cast<void*>(at(L.heads)) : out.ptr;
     p.o_fp32 = shared || fp32 ? 1 : 0;
-    const int st = launch_linear_pass(kernel, p, a.plan->F, stream);
+    const int st = launch_pass(kernel, p, a.plan->F, stream);
     if (st != KDA_OK || !shared) return st;
     const int64_t quads = static_cast<int64_t>(a.plan->T) * heads * p.VW / 4;
     if (quads > 2147483647LL - kRowThreads) return KDA_ERR_UNSUPPORTED;
@@ -210,7 +218,7 @@ int launch_linear_backward(const LinearArgs& a, hipStream_t stream) {
   p.anchor = at(L.anchor);
   p.end_seq = d_final;
   p.end_piece = at(L.cotangents);
-  int st = pass(p, a.Hq, a.dq, linear_query_kernel(a.V, a.K, fp32));
+  st = pass(p, a.Hq, a.dq, linear_query_kernel(a.V, a.K, fp32));
   if (st != KDA_OK) return st;
   p.x = v;
   p.y = d;

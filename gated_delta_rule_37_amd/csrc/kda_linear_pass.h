@@ -12,8 +12,8 @@
 // forward pass of (do, v, k) with the state transposed, dk the reversed pass of
 // (v, do, q) transposed, dv the reversed pass of (k, q, do).
 //
-// A workgroup is one fragment of one head, VD / 32 waves.  A wave holds S's
-// columns 32 w .. 32 w + 31 in FP32 accumulators; x, y, z of the chunk lie in LDS
+// A workgroup is one fragment of one head, four waves.  A wave holds a quarter of
+// S's columns in FP32 accumulators, tiles of 32 x 32 or, where VD is 64, 16 x 16; x, y, z of the chunk lie in LDS
 // in bf16, exactly as they came.  Whatever is not exact in bf16 is split into bf16
 // parts (8 bits each): two of them leave 2^-16, three 2^-24 of a factor.
 //   * P = (x y^T) o decay: 16 x 16 tiles, a wave owns whole rows of tiles; its
@@ -59,6 +59,7 @@ struct LinearParams {
   int64_t g_stride;
   int32_t g_bf16;
   int32_t transposed;           // states in memory are [VW][KW]
+  int32_t reversed;             // kSummary
   const float* seq_state;       // where a sequence begins (reversed: ends), or null
   const float* piece_state;     // where a piece goes on: its own state before (reversed: after) it
   float* seq_out;               // at the other end, or null
@@ -109,9 +110,9 @@ __device__ __forceinline__ auto buffer_of(const void* p, int64_t bytes) {
 constexpr uint32_t kOutside = 0x80000000u;   // no buffer is that long
 
 // A thread's share of a tile on its way to LDS through registers.
-template <int W, int NT>
+template <int W>
 struct Staged {
-  static constexpr int kRows = NT / (W / 8), kSteps = kLinearChunk / kRows;
+  static constexpr int kRows = 256 / (W / 8), kSteps = kLinearChunk / kRows;
   u32x4 r[kSteps];
 
   // Byte offset of the thread's first unit in the chunk's rows; columns behind the
@@ -138,19 +139,15 @@ struct Staged {
 // A tile on its way from memory to LDS without registers: a wave's copy moves 64
 // 16-byte units to 1 KiB of LDS, lane after lane, so each lane takes the unit whose
 // place its own is.
-template <int W, int NW>
+template <int W>
 struct Copy {
-  static constexpr int kRows = 64 / (W / 8);                       // of a copy
-  static constexpr int kSteps = kLinearChunk / kRows / NW;         // of a wave
-  static constexpr int kKinds = W == 128 && NW == 2 ? 2 : 1;       // copies that differ in their units
-  uint32_t at[kKinds], step;
+  static constexpr int kRows = 64 / (W / 8);             // of a copy
+  static constexpr int kSteps = kLinearChunk / kRows / 4;   // of a wave
+  uint32_t at, step;
 
-  __device__ __forceinline__ Copy(const Tokens& t, int wave, int lane) : step(kRows * NW * static_cast<uint32_t>(t.stride) * 2) {
-#pragma unroll
-    for (int k = 0; k < kKinds; ++k) {
-      const int row = (k * NW + wave) * kRows + lane / (W / 8), c = (lane % (W / 8)) ^ row_bits<W>(row);
-      at[k] = 8 * c < t.width ? static_cast<uint32_t>(row - k * NW * kRows) * static_cast<uint32_t>(t.stride) * 2 + 16 * c : kOutside;
-    }
+  __device__ __forceinline__ Copy(const Tokens& t, int wave, int lane) : step(kRows * 4 * static_cast<uint32_t>(t.stride) * 2) {
+    const int row = wave * kRows + lane / (W / 8), c = (lane % (W / 8)) ^ row_bits<W>(row);   // the same bits 4 kRows rows on
+    at = 8 * c < t.width ? static_cast<uint32_t>(row) * static_cast<uint32_t>(t.stride) * 2 + 16 * c : kOutside;
   }
   // rows behind `valid` become zero
   __device__ __forceinline__ void start(const Tokens& t, int head, int64_t t0, int valid, bf16* tile, int wave) const {
@@ -165,7 +162,7 @@ struct Copy {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                   :: "s"(lds + i * (NW * 1024)), "v"(at[i % kKinds] + i * step), "s"(rows) : "memory", "m0");
+                   :: "s"(lds + i * 4096), "v"(at + i * step), "s"(rows) : "memory", "m0");
     }
   }
 };
@@ -183,7 +180,14 @@ __device__ __forceinline__ bf16x8 column_tokens(const bf16* tile, int row0, int 
   return join8(lds_read_tr(unit_at<W>(tile, row, unit) + 4 * (s & 1)),
                lds_read_tr(unit_at<W>(tile, row + 4, unit) + 4 * (s & 1)));
 }
-// The same with the second and third four of every 16 columns exchanged: rows of the
+// Eight tokens of column col0 + lane % 16.
+template <int W>
+__device__ __forceinline__ bf16x8 column16_tokens(const bf16* tile, int row0, int col0, int lane) {
+  const int s = lane & 15, unit = (col0 >> 3) + ((s & 3) >> 1), row = row0 + (s >> 2);
+  return join8(lds_read_tr(unit_at<W>(tile, row, unit) + 4 * (s & 1)),
+               lds_read_tr(unit_at<W>(tile, row + 4, unit) + 4 * (s & 1)));
+}
+// 32 columns with the second and third four of every 16 columns exchanged: rows of the
 // product are then S's rows as they are kept.
 template <int W>
 __device__ __forceinline__ bf16x8 slot_column_tokens(const bf16* tile, int row0, int col0, int lane) {
@@ -242,20 +246,29 @@ struct LinearSmem {
     float whole;
   } gates[2];   // of this chunk and the next
   __align__(16) float pairs[MODE == kQuery ? 4 : 1][kLinearChunk];
-  float dots[VD / 32][kLinearChunk];
-  float by[VD / 32];
+  float dots[4][kLinearChunk];
+  float by[4];
 };
 
-// A wave's part of a state in memory.
-template <int KD, typename F>
-__device__ __forceinline__ void each_quad(const LinearParams& p, int col, int half, F f) {
+// A wave's part of a state in memory: f(four neighbouring values of the tiles, their
+// first row).  32 x 32 tiles hold rows in the order that makes a lane's k slots
+// neighbouring channels, 16 x 16 tiles as they are.
+template <int CW, typename Acc, int KT, typename F>
+__device__ __forceinline__ void each_quad(Acc (&S)[KT], int lane, F f) {
 #pragma unroll
-  for (int kt = 0; kt < KD / 32; ++kt) {
+  for (int kt = 0; kt < KT; ++kt) {
+    if constexpr (CW == 32) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int row = 32 * kt + 16 * (q >> 1) + 8 * half + 4 * (q & 1);
-      f(kt, q, row, row < p.KW && col < p.VW);
+      for (int q = 0; q < 4; ++q) {
+        f32x4 v = {S[kt][4 * q], S[kt][4 * q + 1], S[kt][4 * q + 2], S[kt][4 * q + 3]};
+        f(v, 32 * kt + 16 * (q >> 1) + 8 * (lane >> 5) + 4 * (q & 1));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) S[kt][4 * q + j] = v[j];
+      }
+    } else {
+      f(S[kt], 16 * kt + 4 * (lane >> 4));
     }
+    asm volatile("" ::: "memory");   // a tile's loads and addresses at a time
   }
 }
 __device__ __forceinline__ f32x4 load_quad(const LinearParams& p, const float* s, int row, int col) {
@@ -309,11 +322,26 @@ __device__ __forceinline__ double gate_prefix(double x) {
   return prefix_step<0x143, 0xc>(x);   // lane 31 to rows 2 and 3
 }
 
+__device__ __forceinline__ f32x16 product(const bf16x8& a, const bf16x8& b, const f32x16& c) { return mfma(a, b, c); }
+__device__ __forceinline__ f32x4 product(const bf16x8& a, const bf16x8& b, const f32x4& c) { return mfma16(a, b, c); }
+template <int N>
+struct LinearAcc;
+template <>
+struct LinearAcc<32> {
+  typedef f32x16 type;
+};
+template <>
+struct LinearAcc<16> {
+  typedef f32x4 type;
+};
+
 template <int KD, int VD, int SS, int PS, bool REV, int MODE>
-__global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
-  constexpr int NT = 2 * VD, NW = VD / 32, KT = KD / 32, US = 3;
+__device__ __forceinline__ void linear_pass(const LinearParams& p) {
+  constexpr int CW = VD / 4, KT = KD / CW, OT = kLinearChunk / CW, US = 3;   // a wave's columns, tiles of S and of out
   constexpr bool kOut = MODE != kSummary;
+  typedef typename LinearAcc<CW>::type Acc;
   __shared__ LinearSmem<KD, VD, PS, MODE> sm;
+  const bool rev = MODE == kSummary ? p.reversed != 0 : REV;
 
   const int32_t f = p.plan[p.L.frag_order + static_cast<int32_t>(blockIdx.x / static_cast<uint32_t>(p.H))];
   const int32_t head = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(p.H));
@@ -321,26 +349,27 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
   const int32_t begin = p.plan[p.L.frag_begin + f], end = p.plan[p.L.frag_end + f];
   const bool carried = (flags & kFragCarried) != 0, seq_end = (flags & kFragSeqEnd) != 0;
   // whether the pass starts (ends) at its sequence's own end, not at a cut
-  const bool starts = REV ? seq_end : !carried, ends = REV ? !carried : seq_end;
+  const bool starts = rev ? seq_end : !carried, ends = rev ? !carried : seq_end;
   if (!kOut && ends) return;   // nothing goes on from here
 
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, l32 = lane & 31, l16 = lane & 15, quad = lane >> 4;
-  const int col = 32 * wave + l32;
+  const int lcol = lane % CW, lrow = lane / CW;   // a tile's column, and which rows
+  const int col = CW * wave + lcol;
   const int64_t size = static_cast<int64_t>(p.KW) * p.VW;
 
-  f32x16 S[KT];
+  Acc S[KT];
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt) S[kt] = zero16();
+  for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll
+    for (int i = 0; i < CW * CW / 64; ++i) S[kt][i] = 0.f;
+  }
   {
     const float* from = starts ? p.seq_state : kOut ? p.piece_state : nullptr;
     if (from != nullptr) {
       from += (static_cast<int64_t>(starts ? seq : seg) * p.H + head) * size;
-      each_quad<KD>(p, col, half, [&](int kt, int q, int row, bool has) {
-        if (!has) return;
-        const f32x4 v = load_quad(p, from, row, col);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) S[kt][4 * q + j] = v[j];
+      each_quad<CW>(S, lane, [&](f32x4& v, int row) {
+        if (row < p.KW && col < p.VW) v = load_quad(p, from, row, col);
       });
     }
   }
@@ -349,16 +378,16 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
   double total = 0.0;
 
   const Minus minus;
-  const Copy<KD, NW> cx(p.x, wave, lane), cy(p.y, wave, lane);
-  Staged<KD, NT> sy;
-  Staged<VD, NT> sz;
+  const Copy<KD> cx(p.x, wave, lane), cy(p.y, wave, lane);
+  Staged<KD> sy;
+  Staged<VD> sz;
   const uint32_t at_y = MODE == kQuery ? sy.offset(p.y) : 0, at_z = MODE == kQuery ? sz.offset(p.z) : 0;
-  const Copy<VD, NW> cz(p.z, wave, lane), ce(p.e, wave, lane);
+  const Copy<VD> cz(p.z, wave, lane), ce(p.e, wave, lane);
   const uint32_t o_size = p.o_fp32 ? 4 : 2, o_row = static_cast<uint32_t>(p.H) * p.VW * o_size;
-  const uint32_t at_o = l32 * o_row + (32 * wave + 4 * half) * o_size;
-  const uint32_t at_key = l32 * static_cast<uint32_t>(p.e.stride) * 2 + (32 * wave + 4 * half) * 2;
+  const uint32_t at_o = lcol * o_row + (CW * wave + 4 * lrow) * o_size;
+  const uint32_t at_key = lcol * static_cast<uint32_t>(p.e.stride) * 2 + (CW * wave + 4 * lrow) * 2;
   // first token of the chunk that is walked as number `it`, and its tokens
-  const auto first_of = [&](int it) { return static_cast<int64_t>(begin) + (REV ? chunks - 1 - it : it) * kLinearChunk; };
+  const auto first_of = [&](int it) { return static_cast<int64_t>(begin) + (rev ? chunks - 1 - it : it) * kLinearChunk; };
   const auto valid_of = [&](int64_t t0) { return min(kLinearChunk, end - static_cast<int>(t0)); };
   const auto start_x = [&](int it) {
     if (!kOut || it >= chunks) return;
@@ -386,7 +415,8 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
   // it would wait for all of them before it uses such a value; `landed` uses them
   // where the copies before them have been waited for anyway.
   uint32_t gate = 0, part = 0, rho = 0;
-  u32x2 key[MODE == kKey ? 8 : 1];
+  constexpr int kKeys = CW * CW / 256 * OT;   // a lane's quads of out
+  u32x2 key[MODE == kKey ? kKeys : 1];
   const auto fetch_gate = [&](int it) {
     if (wave != 0 || it >= chunks) return;
     const int64_t t0 = first_of(it), size = p.g_bf16 ? 2 : 4;
@@ -407,9 +437,10 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
       const auto rows = buffer_of(p.e.p + t0 * p.e.stride + static_cast<int64_t>(head / p.e.share) * p.e.width,
                                   (valid - 1) * p.e.stride * 2 + p.e.width * 2);
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const uint32_t at = at_key + 32 * (n >> 2) * static_cast<uint32_t>(p.e.stride) * 2 + 16 * (n & 3);
-        key[n] = __builtin_amdgcn_raw_buffer_load_b64(rows, 32 * wave + 8 * (n & 3) < p.VW ? at : kOutside, 0, 0);
+      for (int n = 0; n < kKeys; ++n) {
+        const int tile = n / (kKeys / OT), q = n % (kKeys / OT);
+        const uint32_t at = at_key + CW * tile * static_cast<uint32_t>(p.e.stride) * 2 + 16 * q;
+        key[n] = __builtin_amdgcn_raw_buffer_load_b64(rows, CW * wave + 8 * q + 4 * lrow < p.VW ? at : kOutside, 0, 0);
       }
       if (wave == 0) {
         const int64_t slot = static_cast<int64_t>(begin / kLinearChunk) + f + (chunks - 1 - it);
@@ -423,7 +454,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
     asm volatile("" : "+v"(gate), "+v"(part), "+v"(rho));
     if constexpr (MODE == kKey) {
 #pragma unroll
-      for (int n = 0; n < 8; ++n) asm volatile("" : "+v"(key[n]));
+      for (int n = 0; n < kKeys; ++n) asm volatile("" : "+v"(key[n]));
     }
   };
   const auto make_gates = [&](int it) {
@@ -437,7 +468,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
     const double high = rint(G * 512.0) * (1.0 / 512.0);
     to.high[lane] = static_cast<float>(high);
     to.low[lane] = static_cast<float>(G - high);
-    to.w_in[lane] = __builtin_amdgcn_exp2f(static_cast<float>(REV ? G : last - G));
+    to.w_in[lane] = __builtin_amdgcn_exp2f(static_cast<float>(rev ? G : last - G));
     if (lane == 0) to.whole = __builtin_amdgcn_exp2f(static_cast<float>(last));
     total += last;
   };
@@ -450,7 +481,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
   if (!kOut) start_z(0);
 
   for (int it = 0; it < chunks; ++it) {
-    const int c = REV ? chunks - 1 - it : it;
+    const int c = rev ? chunks - 1 - it : it;
     const int64_t t0 = begin + c * kLinearChunk;
     const int valid = min(kLinearChunk, end - static_cast<int>(t0));
     const int Y = MODE == kQuery ? 0 : it & 1, Z = kOut ? 0 : it & 1;
@@ -477,38 +508,30 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
     make_gates(it + 1);
     fetch_gate(it + 2);
     const auto& gates = sm.gates[it & 1];
+    // kQuery: the addresses of what is read by columns are made anew, as all would not fit
+    const int reader = MODE == kQuery ? opaque(lane) : lane;
 
     // wave 0 needs this chunk's parts at its end
     const float left = __uint_as_float(part), taken = __uint_as_float(rho);
-    f32x16 out[2];
+    Acc out[OT];
     if constexpr (kOut) {
       // P: tiles of 16 out tokens (columns) by 16 tokens of the sum (rows)
-#pragma unroll
-      for (int n = 0; n < 4 / NW; ++n) {
-        const int a = NW == 4 ? wave : n == 0 ? wave : 3 - wave;   // the longest row of tiles with the shortest
-        bf16x8 xf[KD / 32], ef[MODE == kQuery ? VD / 32 : 1];
+      {
+        const int a = wave;
+        bf16x8 xf[KD / 32];
 #pragma unroll
         for (int s = 0; s < KD / 32; ++s) xf[s] = ld_unit(unit_at<KD>(sm.x, 16 * a + l16, 4 * s + quad));
-        if constexpr (MODE == kQuery) {
-#pragma unroll
-          for (int s = 0; s < VD / 32; ++s) ef[s] = ld_unit(unit_at<VD>(sm.e, 16 * a + l16, 4 * s + quad));
-        }
         const float high = gates.high[16 * a + l16], low = gates.low[16 * a + l16];
         float before = 0.f;   // kQuery: the pairs' sum over the tiles so far
         // the products of all four tiles, also where none is needed: other waves
         // need all of theirs meanwhile
-        f32x4 acc[4], m[MODE == kQuery ? 4 : 1];
+        f32x4 acc[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           acc[b] = zero4();
 #pragma unroll
           for (int s = 0; s < KD / 32; ++s) {
             acc[b] = mfma16(ld_unit(unit_at<KD>(sm.y[Y], 16 * b + l16, 4 * s + quad)), xf[s], acc[b]);
-          }
-          if constexpr (MODE == kQuery) {
-            m[b] = zero4();
-#pragma unroll
-            for (int s = 0; s < VD / 32; ++s) m[b] = mfma16(ld_unit(unit_at<VD>(sm.z[Z], 16 * b + l16, 4 * s + quad)), ef[s], m[b]);
           }
         }
 #pragma unroll
@@ -532,9 +555,14 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
           }
           if constexpr (MODE == kQuery) {
             // pairs (i, j < i): sums over j < t for every t <= i of the tile, then over i
+            f32x4 m = zero4();
+#pragma unroll
+            for (int s = 0; s < VD / 32; ++s) {
+              m = mfma16(ld_unit(unit_at<VD>(sm.z[Z], 16 * b + l16, 4 * s + quad)), ld_unit(unit_at<VD>(sm.e, 16 * a + l16, 4 * s + quad)), m);
+            }
             float pair[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) pair[r] = a != b || 4 * quad + r < l16 ? m[b][r] * w[r] : 0.f;
+            for (int r = 0; r < 4; ++r) pair[r] = a != b || 4 * quad + r < l16 ? m[r] * w[r] : 0.f;
             float incl = (pair[0] + pair[1]) + (pair[2] + pair[3]);
             float y = __shfl_up(incl, 16);
             if (quad >= 1) incl += y;
@@ -565,52 +593,69 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
         }
       }
       // through the state
-      out[0] = zero16();
-      out[1] = zero16();
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
+      for (int ib = 0; ib < OT; ++ib) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          float v[8];
-          tile_kslots(S[kt], s, v);
-          bf16x8 part[SS];
-          split_parts<SS>(minus, v, part);
+        for (int i = 0; i < CW * CW / 64; ++i) out[ib][i] = 0.f;
+      }
 #pragma unroll
-          for (int ib = 0; ib < 2; ++ib) {
-            const bf16x8 xf = ld_unit(unit_at<KD>(sm.x, 32 * ib + l32, 2 * (2 * kt + s) + half));
+      for (int u = 0; u < KD * CW / 512; ++u) {   // 16 rows of S in 32 x 32 tiles, 32 in 16 x 16
+        float v[8];
+        if constexpr (CW == 32) {
+          tile_kslots(S[u / 2], u % 2, v);
+        } else {
 #pragma unroll
-            for (int n = 0; n < SS; ++n) out[ib] = mfma(part[n], xf, out[ib]);
+          for (int j = 0; j < 4; ++j) {
+            v[j] = S[2 * u][j];
+            v[4 + j] = S[2 * u + 1][j];
           }
+        }
+        bf16x8 part[SS];
+        split_parts<SS>(minus, v, part);
+#pragma unroll
+        for (int ib = 0; ib < OT; ++ib) {
+          const int row = CW * ib + lcol;
+          bf16x8 xf;
+          if constexpr (CW == 32) {
+            xf = ld_unit(unit_at<KD>(sm.x, row, 2 * u + half));
+          } else {   // channels 4 quad .. 4 quad + 3 of both tiles
+            const bf16x4 lo = ld_piece(unit_at<KD>(sm.x, row, 4 * u + (quad >> 1)) + 4 * (quad & 1));
+            const bf16x4 hi = ld_piece(unit_at<KD>(sm.x, row, 4 * u + 2 + (quad >> 1)) + 4 * (quad & 1));
+            xf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+          }
+#pragma unroll
+          for (int n = 0; n < SS; ++n) out[ib] = product(part[n], xf, out[ib]);
         }
       }
 #pragma unroll
-      for (int ib = 0; ib < 2; ++ib) {
-        const float high = gates.high[32 * ib + l32], low = gates.low[32 * ib + l32];
+      for (int ib = 0; ib < OT; ++ib) {
+        const float high = gates.high[CW * ib + lcol], low = gates.low[CW * ib + lcol];
         const float w = __builtin_amdgcn_exp2f(REV ? (gates.high[63] - high) + (gates.low[63] - low) : high + low);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) out[ib][i] *= w;
+        for (int i = 0; i < CW * CW / 64; ++i) out[ib][i] *= w;
       }
       if constexpr (MODE == kQuery || MODE == kKey) {
         // q . (dq through the state), k . (dk through the state)
 #pragma unroll
-        for (int ib = 0; ib < 2; ++ib) {
-          const int t = 32 * ib + l32;
+        for (int ib = 0; ib < OT; ++ib) {
+          const int t = CW * ib + lcol;
           float dot = 0.f;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int ch = 32 * wave + 8 * q + 4 * half;
-            bf16x4 v = {0, 0, 0, 0};
+          for (int q = 0; q < CW * CW / 256; ++q) {
+            bf16x4 v;
             if constexpr (MODE == kQuery) {
-              v = *reinterpret_cast<const bf16x4*>(unit_at<VD>(sm.e, t, ch >> 3) + 4 * half);
+              const int ch = CW * wave + 8 * q + 4 * lrow;
+              v = ld_piece(unit_at<VD>(sm.e, t, ch >> 3) + (ch & 4));
             } else {
-              v = __builtin_bit_cast(bf16x4, key[4 * ib + q]);
+              v = __builtin_bit_cast(bf16x4, key[CW * CW / 256 * ib + q]);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) dot += static_cast<float>(v[j]) * out[ib][4 * q + j];
           }
           dot = t < valid ? dot : 0.f;
+          if (CW == 16) dot += __shfl_xor(dot, 16);
           dot += __shfl_xor(dot, 32);
-          if (half == 0) sm.dots[wave][t] = dot;
+          if (lrow == 0) sm.dots[wave][t] = dot;
         }
       }
       // What passes by the chunk, e^{G_C} <cotangent after it, state before it>, is a
@@ -622,12 +667,11 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
         if (with != nullptr) {
           with += (static_cast<int64_t>(ends ? seq : seg) * p.H + head) * size;
           const int at = opaque(col);   // its addresses are not kept over the chunks
-          each_quad<KD>(p, at, opaque(half), [&](int kt, int q, int row, bool has) {
-            if (!has) return;
-            const f32x4 v = load_quad(p, with, row, at);
+          each_quad<CW>(S, opaque(lane), [&](f32x4& v, int row) {
+            if (row >= p.KW || at >= p.VW) return;
+            const f32x4 w = load_quad(p, with, row, at);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dot += v[j] * S[kt][4 * q + j];
-            if (q == 3) asm volatile("" ::: "memory");   // a tile's loads at a time
+            for (int j = 0; j < 4; ++j) dot += v[j] * w[j];
           });
         }
         dot = sum64(dot);
@@ -635,7 +679,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
       }
       if constexpr (MODE != kQuery) {   // z; y's copies may go on
         if (it + 1 < chunks) {
-          copies_done<Copy<KD, NW>::kSteps>();
+          copies_done<Copy<KD>::kSteps>();
         } else {
           copies_done<0>();
         }
@@ -645,19 +689,30 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
       fetch_key(it + 1);
     }
 
-    bf16x8 zf[4];
+    // z by columns: 16 tokens a product with 32 x 32 tiles, 32 with 16 x 16
+    constexpr int ZT = CW / 8;
+    bf16x8 zf[ZT];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) zf[s] = column_tokens<VD>(sm.z[Z], 16 * s + 8 * half, 32 * wave, lane);
+    for (int s = 0; s < ZT; ++s) {
+      if constexpr (CW == 32) {
+        zf[s] = column_tokens<VD>(sm.z[Z], 16 * s + 8 * half, 32 * wave, reader);
+      } else {
+        zf[s] = column16_tokens<VD>(sm.z[Z], 32 * s + 8 * quad, 16 * wave, reader);
+      }
+    }
     if constexpr (kOut) {
 #pragma unroll
-      for (int ib = 0; ib < 2; ++ib) {
+      for (int ib = 0; ib < OT; ++ib) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int jb = s >> 1;
-          if (REV ? jb < ib : jb > ib) continue;
+        for (int s = 0; s < ZT; ++s) {
+          const int ob = CW == 32 ? ib : ib >> 1, jb = CW == 32 ? s >> 1 : s;   // blocks of 32 tokens
+          if (REV ? jb < ob : jb > ob) continue;
 #pragma unroll
           for (int n = 0; n < PS; ++n) {
-            out[ib] = mfma(zf[s], ld_unit(p_unit(sm.p + n * 3072, ib + jb, l32, 2 * (s & 1) + half)), out[ib]);
+            const bf16* part = sm.p + n * 3072;
+            const bf16x8 pf = CW == 32 ? ld_unit(p_unit(const_cast<bf16*>(part), ob + jb, l32, 2 * (s & 1) + half))
+                                       : ld_unit(p_unit(const_cast<bf16*>(part), ob + jb, 16 * (ib & 1) + l16, quad));
+            out[ib] = product(zf[s], pf, out[ib]);
           }
         }
       }
@@ -667,12 +722,13 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) S[kt][i] *= whole;
+      for (int i = 0; i < CW * CW / 64; ++i) S[kt][i] *= whole;
     }
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < ZT; ++s) {
+      const int t = 512 / CW * s + 8 * lrow;   // the first of the lane's eight tokens
       const u32x4 raw = __builtin_bit_cast(u32x4, zf[s]);
-      const f32x4 w0 = ld4(gates.w_in + 16 * s + 8 * half), w1 = ld4(gates.w_in + 16 * s + 8 * half + 4);
+      const f32x4 w0 = ld4(gates.w_in + t), w1 = ld4(gates.w_in + t + 4);
       float v[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -683,33 +739,38 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
       split_parts<US>(minus, v, part);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
-        const bf16x8 yf = slot_column_tokens<KD>(sm.y[Y], 16 * s + 8 * half, 32 * kt, lane);
+        const bf16x8 yf = CW == 32 ? slot_column_tokens<KD>(sm.y[Y], t, 32 * kt, reader) : column16_tokens<KD>(sm.y[Y], t, 16 * kt, reader);
 #pragma unroll
-        for (int n = 0; n < US; ++n) S[kt] = mfma(yf, part[n], S[kt]);
+        for (int n = 0; n < US; ++n) S[kt] = product(yf, part[n], S[kt]);
       }
     }
     if constexpr (kOut) {
+      // four stores a wave at least, whatever the width: the copies' wait counts them
       const auto rows = buffer_of(static_cast<char*>(p.o) + (t0 * p.H + head) * p.VW * o_size, static_cast<int64_t>(valid) * o_row);
 #pragma unroll
-      for (int ib = 0; ib < 2; ++ib) {
+      for (int ib = 0; ib < OT; ++ib) {
+        if (CW == 16 || p.o_fp32) {
 #pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-          const uint32_t at = 32 * ib * o_row + 8 * q * o_size;
-          if (p.o_fp32) {
-#pragma unroll
-            for (int n = q; n < q + 2; ++n) {
-              const f32x4 v = {out[ib][4 * n], out[ib][4 * n + 1], out[ib][4 * n + 2], out[ib][4 * n + 3]};
-              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rows, 32 * wave + 8 * n < p.VW ? at_o + at + 32 * (n - q) : kOutside, 0, 0);
+          for (int q = 0; q < CW * CW / 256; ++q) {
+            const uint32_t at = CW * wave + 8 * q + 4 * lrow < p.VW ? at_o + CW * ib * o_row + 8 * q * o_size : kOutside;
+            const f32x4 v = {out[ib][4 * q], out[ib][4 * q + 1], out[ib][4 * q + 2], out[ib][4 * q + 3]};
+            if (p.o_fp32) {
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rows, at, 0, 0);
+            } else {
+              __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}, rows, at, 0, 0);
             }
-          } else {
+          }
+        } else if constexpr (CW == 32) {
+#pragma unroll
+          for (int q = 0; q < 4; q += 2) {
             // channels 0 .. 7 of 16 to the lower half's lane of a token, 8 .. 15 to the upper's
             u32x2 lo = {pack_bf16(out[ib][4 * q], out[ib][4 * q + 1]), pack_bf16(out[ib][4 * q + 4], out[ib][4 * q + 5])};
             u32x2 hi = {pack_bf16(out[ib][4 * q + 2], out[ib][4 * q + 3]), pack_bf16(out[ib][4 * q + 6], out[ib][4 * q + 7])};
             lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(lo[0], lo[1], false, false));
             hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(hi[0], hi[1], false, false));
             const u32x4 v = {lo[0], hi[0], lo[1], hi[1]};
-            const uint32_t where = 32 * wave + 8 * q + 8 * half < p.VW ? at_o + at + 8 * half : kOutside;
-            __builtin_amdgcn_raw_buffer_store_b128(v, rows, where, 0, 0);
+            const uint32_t at = at_o + 32 * ib * o_row + 16 * q + 8 * half;
+            __builtin_amdgcn_raw_buffer_store_b128(v, rows, 32 * wave + 8 * q + 8 * half < p.VW ? at : kOutside, 0, 0);
           }
         }
       }
@@ -720,7 +781,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
       if (wave == 0) {
         float dot = sm.dots[0][lane];
 #pragma unroll
-        for (int w = 1; w < NW; ++w) dot += sm.dots[w][lane];
+        for (int w = 1; w < 4; ++w) dot += sm.dots[w][lane];
         const int64_t at = (t0 + lane) * p.H + head, slot = (static_cast<int64_t>(begin / kLinearChunk) + f + c) * p.H + head;
         if constexpr (MODE == kQuery) {
           float sum = 0.f;
@@ -732,7 +793,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
           if (it + 1 == chunks && lane == 0) {
             float by = sm.by[0];
 #pragma unroll
-            for (int w = 1; w < NW; ++w) by += sm.by[w];
+            for (int w = 1; w < 4; ++w) by += sm.by[w];
             p.anchor[static_cast<int64_t>(f) * p.H + head] = gates.whole * by;
           }
         } else {
@@ -745,7 +806,7 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
           } else if (c == 0) {
             by = sm.by[0];
 #pragma unroll
-            for (int w = 1; w < NW; ++w) by += sm.by[w];
+            for (int w = 1; w < 4; ++w) by += sm.by[w];
             by *= gates.whole;
           }
           if (lane < valid) {
@@ -762,22 +823,27 @@ __global__ __launch_bounds__(2 * VD, 2) void linear_kernel(LinearParams p) {
     }
   }
 
-  if (MODE == kSummary) {
-    float* to = p.piece_out + (static_cast<int64_t>(seg) * p.H + head) * size;
-    each_quad<KD>(p, col, half, [&](int kt, int q, int row, bool has) {
-      const f32x4 v = {S[kt][4 * q], S[kt][4 * q + 1], S[kt][4 * q + 2], S[kt][4 * q + 3]};
-      if (has) store_quad(p, to, row, col, v);
-    });
-    if (p.decay_out != nullptr && tid == 0) {
-      p.decay_out[static_cast<int64_t>(seg) * p.H + head] = __builtin_amdgcn_exp2f(static_cast<float>(total));
-    }
-  } else if (p.seq_out != nullptr && ends) {
-    float* to = p.seq_out + (static_cast<int64_t>(seq) * p.H + head) * size;
-    each_quad<KD>(p, col, half, [&](int kt, int q, int row, bool has) {
-      const f32x4 v = {S[kt][4 * q], S[kt][4 * q + 1], S[kt][4 * q + 2], S[kt][4 * q + 3]};
-      if (has) store_quad(p, to, row, col, v);
+  float* to = !kOut ? p.piece_out + (static_cast<int64_t>(seg) * p.H + head) * size
+                    : p.seq_out != nullptr && ends ? p.seq_out + (static_cast<int64_t>(seq) * p.H + head) * size : nullptr;
+  if (to != nullptr) {
+    each_quad<CW>(S, lane, [&](f32x4& v, int row) {
+      if (row < p.KW && col < p.VW) store_quad(p, to, row, col, v);
     });
   }
+  if (!kOut && p.decay_out != nullptr && tid == 0) {
+    p.decay_out[static_cast<int64_t>(seg) * p.H + head] = __builtin_amdgcn_exp2f(static_cast<float>(total));
+  }
+}
+
+constexpr int kLinearThreads = 256;
+template <int KD, int VD, int SS, int PS, bool REV, int MODE>
+__global__ __launch_bounds__(kLinearThreads, 2) void linear_kernel(LinearParams p) {
+  linear_pass<KD, VD, SS, PS, REV, MODE>(p);
+}
+// The pieces' updates, and beside them those of their cotangents.
+template <int KD, int VD>
+__global__ __launch_bounds__(kLinearThreads, 2) void linear_summary_kernel(LinearParams p, LinearParams other) {
+  linear_pass<KD, VD, 1, 1, false, kSummary>(blockIdx.y == 0 ? p : other);
 }
 
 // KD and VD by the widths in use.
@@ -792,9 +858,6 @@ void (*linear_kernel_of(int32_t KW, int32_t VW))(LinearParams) {
 void (*linear_query_kernel(int32_t KW, int32_t VW, bool fp32))(LinearParams);
 void (*linear_key_kernel(int32_t KW, int32_t VW, bool fp32))(LinearParams);
 void (*linear_value_kernel(int32_t KW, int32_t VW, bool fp32))(LinearParams);
-
-// Launches one pass over all fragments and heads (kda_linear.hip).
-int launch_linear_pass(void (*kernel)(LinearParams), const LinearParams& p, int32_t fragments, hipStream_t stream);
 
 }  // namespace kda
 
