@@ -394,13 +394,16 @@ int kda_linear_backward(const kda_plan* plan, const int32_t* plan_dev, size_t pl
 }
 
 size_t kda_linear_workspace_bytes(const kda_plan* plan, int32_t H, int32_t K, int32_t V) {
-  return plan == nullptr || H <= 0 || H > 65535 || K <= 0 || K > 128 || V <= 0 || V > 128
-             ? 0 : kda::linear_layout(plan, H, K, V).total;
+  kda::LinearArgs a{};
+  a.plan = plan;
+  a.H = a.Hq = a.Hk = a.Hv = H;
+  a.K = K;
+  a.V = V;
+  return kda::check_linear_sizes(a) == KDA_OK ? kda::linear_layout(plan, H, K, V).total : 0;
 }
 
 size_t kda_linear_backward_workspace_bytes(const kda_plan* plan, int32_t H, int32_t Hq, int32_t Hk, int32_t Hv, int32_t K,
                                            int32_t V) {
-  if (plan == nullptr || H <= 0 || H > 65535 || K <= 0 || K > 128 || V <= 0 || V > 128) return 0;
   kda::LinearArgs a{};
   a.plan = plan;
   a.H = H;
@@ -409,7 +412,7 @@ size_t kda_linear_backward_workspace_bytes(const kda_plan* plan, int32_t H, int3
   a.Hv = Hv;
   a.K = K;
   a.V = V;
-  return kda::linear_bwd_layout(a).total;
+  return kda::check_linear_sizes(a) == KDA_OK ? kda::linear_bwd_layout(a).total : 0;
 }
 
 int kda_linear_step(int32_t B, int32_t H, int32_t Hq, int32_t Hk, int32_t Hv, int32_t K, int32_t V,

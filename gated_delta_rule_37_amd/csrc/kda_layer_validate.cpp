@@ -379,15 +379,21 @@ LinearBwdLayout linear_bwd_layout(const LinearArgs& a) {
   return L;
 }
 
+int check_linear_sizes(const LinearArgs& a) {
+  if (a.plan == nullptr) return KDA_ERR_INVALID_ARG;
+  const int st = check_linear_heads(a.H, a.Hq, a.Hk, a.Hv, a.K, a.V);
+  return st == KDA_OK && a.H > kMaxLinearHeads ? KDA_ERR_UNSUPPORTED : st;
+}
+
 int check_linear(const LinearArgs& a, bool backward) {
-  if (a.plan == nullptr || a.plan_dev.ptr == nullptr) return KDA_ERR_INVALID_ARG;
-  int st = check_linear_heads(a.H, a.Hq, a.Hk, a.Hv, a.K, a.V);
+  int st = check_linear_sizes(a);
   if (st != KDA_OK) return st;
+  if (a.plan_dev.ptr == nullptr) return KDA_ERR_INVALID_ARG;
   if (!known_type(a.g_dtype) || !known_type(a.o_format)) return KDA_ERR_INVALID_ARG;
   const int32_t T = a.plan->T;
-  const size_t H = static_cast<size_t>(a.H), K = static_cast<size_t>(a.K), V = static_cast<size_t>(a.V), tokens = static_cast<size_t>(T),
-               q_row = static_cast<size_t>(a.Hq) * K, k_row = static_cast<size_t>(a.Hk) * K, v_row = static_cast<size_t>(a.Hv) * V,
-               state = static_cast<size_t>(a.plan->N) * H * K * V * 4, e = size_of(a.o_format), eg = size_of(a.g_dtype);
+  const size_t H = static_cast<size_t>(a.H), K = static_cast<size_t>(a.K), V = static_cast<size_t>(a.V),
+               tokens = static_cast<size_t>(T), q_row = static_cast<size_t>(a.Hq) * K, k_row = static_cast<size_t>(a.Hk) * K,
+               v_row = static_cast<size_t>(a.Hv) * V, state = static_cast<size_t>(a.plan->N) * H * K * V * 4, e = size_of(a.o_format), eg = size_of(a.g_dtype);
   const bool fixed = a.g.stride == 0;
   st = first_error({check_stride(a.q, static_cast<int64_t>(q_row)), check_stride(a.k, static_cast<int64_t>(k_row)),
                     check_stride(a.v, static_cast<int64_t>(v_row)), fixed ? KDA_OK : check_stride(a.g, a.H)});
@@ -397,7 +403,6 @@ int check_linear(const LinearArgs& a, bool backward) {
       a.g.stride > kMaxScanStride) {
     return KDA_ERR_UNSUPPORTED;
   }
-  if (a.H > kMaxLinearHeads) return KDA_ERR_UNSUPPORTED;
   st = check_buffers({{a.plan_dev.ptr, a.plan_dev.bytes, a.plan->blob.size() * sizeof(int32_t), false},
                       {a.q.ptr, a.q.bytes, rows_need(a.q, T, q_row, 2), false},
                       {a.k.ptr, a.k.bytes, rows_need(a.k, T, k_row, 2), false},

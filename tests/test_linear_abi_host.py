@@ -151,9 +151,135 @@ def test_step_options():
     assert c(state_out=[FAKE + pool, BIG], o=[FAKE, 1]) == SMALL
 
 
+# ---------------------------------------------------------------------------
+# kda_linear_forward and kda_linear_backward
+
+T, N, H, HQ, HK, HV, K, V = 300, 3, 6, 2, 3, 6, 64, 40
+PLAN = kda.Plan([0, 7, 64, T], 3)
+
+
+def _linear(backward=False):
+    common = dict(plan=PLAN.handle, plan_dev=[FAKE, BIG], H=H, Hq=HQ, Hk=HK, Hv=HV, K=K, V=V,
+                  q=[FAKE, BIG, HQ * K + 8], k=[FAKE, BIG, HK * K], v=[FAKE, BIG, HV * V], g=[FAKE, BIG, H + 1],
+                  g_dtype=F32, **_buffers("initial_state"))
+    if not backward:
+        return Call("kda_linear_forward", **common, o=[FAKE, BIG], o_format=BF16, **_buffers("final_state", "workspace"))
+    return Call("kda_linear_backward", **common, **_buffers("d_o", "d_final", "dq", "dk", "dv"), grad_format=F32,
+                **_buffers("dg", "d_initial_state", "workspace"))
+
+
+LINEAR = dict(linear=_linear(), linear_bwd=_linear(backward=True))
+_STATE = N * H * K * V * 4
+_LINEAR_IN = dict(plan_dev=len(PLAN.blob) * 4, q=((T - 1) * (HQ * K + 8) + HQ * K) * 2, k=T * HK * K * 2, v=T * HV * V * 2,
+                  g=((T - 1) * (H + 1) + H) * 4, initial_state=_STATE)
+LINEAR_NEED = dict(
+    linear=dict(**_LINEAR_IN, o=T * H * V * 2, final_state=_STATE),
+    linear_bwd=dict(**_LINEAR_IN, d_o=T * H * V * 2, d_final=_STATE, dq=T * HQ * K * 4, dk=T * HK * K * 4,
+                    dv=T * HV * V * 4, dg=T * H * 4, d_initial_state=_STATE))
+LINEAR_OPTIONAL = {"initial_state", "d_final", "d_initial_state"}
+
+
+def _linear_workspace(call):
+    lib = kda.lib()
+    if call == "linear":
+        return lib.kda_linear_workspace_bytes(PLAN.handle, H, K, V)
+    return lib.kda_linear_backward_workspace_bytes(PLAN.handle, H, HQ, HK, HV, K, V)
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c in LINEAR_NEED for n in LINEAR_NEED[c]])
+def test_linear_buffers(call, name):
+    c = LINEAR[call]
+    rest = c.args[name][2:]
+    if name not in LINEAR_OPTIONAL:
+        assert c(**{name: [None, BIG, *rest]}) == INVALID
+    assert c(**{name: [FAKE + 8, BIG, *rest]}) == MISALIGNED
+    assert c(**{name: [FAKE, LINEAR_NEED[call][name] - 1, *rest]}) == SMALL
+
+
+@pytest.mark.parametrize("call", LINEAR)
+def test_linear_options(call):
+    c = LINEAR[call]
+    assert set(LINEAR_NEED[call]) | {"workspace"} == {n for n, v in c.args.items() if isinstance(v, list)}
+    assert c(plan=None) == INVALID
+    for n in ("H", "Hq", "Hk", "Hv", "K", "V"):
+        for bad in (0, -1):
+            assert c(**{n: bad}) == INVALID
+    for n in ("Hq", "Hk", "Hv"):
+        assert c(**{n: 4}) == INVALID and c(**{n: 12}) == INVALID
+    for n in ("K", "V"):
+        assert c(**{n: 136}) == UNSUPPORTED and c(**{n: 44}) == UNSUPPORTED
+    one = dict(Hq=1, Hk=1, Hv=1, q=[FAKE, BIG, K], k=[FAKE, BIG, K], v=[FAKE, BIG, V])
+    assert c(H=16385, **one, g=[FAKE, BIG, 16385]) == UNSUPPORTED
+    assert c(g_dtype=2) == INVALID
+    assert c(**{"o_format" if call == "linear" else "grad_format": 2}) == INVALID
+    for n, row in (("q", HQ * K), ("k", HK * K), ("v", HV * V)):
+        assert c(**{n: [FAKE, BIG, row - 8]}) == INVALID
+        assert c(**{n: [FAKE, BIG, row + 4]}) == MISALIGNED
+        assert c(**{n: [FAKE, BIG, (1 << 22) + 8]}) == UNSUPPORTED
+    for stride in (H - 1, -1):
+        assert c(g=[FAKE, BIG, stride]) == INVALID
+    assert c(g=[FAKE, BIG, (1 << 22) + 1]) == UNSUPPORTED
+    assert c(g=[FAKE, H * 4 - 1, 0]) == SMALL          # one g a head
+    need = _linear_workspace(call)
+    assert need > 0
+    assert c(workspace=[None, 0]) == INVALID
+    assert c(workspace=[FAKE + 8, need]) == MISALIGNED
+    assert c(workspace=[FAKE, need - 1]) == WORKSPACE
+
+
+def test_linear_workspaces():
+    lib = kda.lib()
+    uncut = kda.Plan([0, 7, 64, T], 1)
+    assert lib.kda_linear_workspace_bytes(uncut.handle, H, K, V) == 0
+    assert lib.kda_linear_backward_workspace_bytes(uncut.handle, H, HQ, HK, HV, K, V) > 0
+    forward = lib.kda_linear_workspace_bytes
+    assert [forward(None, H, K, V)] + [forward(PLAN.handle, *a) for a in ((0, K, V), (16385, K, V), (H, 136, V), (H, K, 0))] == [0] * 5
+    backward = lib.kda_linear_backward_workspace_bytes
+    bad = ((0, 1, 1, 1, K, V), (H, 4, HK, HV, K, V), (H, HQ, HK, HV, 136, V), (H, HQ, HK, HV, K, -8))
+    assert [backward(None, H, HQ, HK, HV, K, V)] + [backward(PLAN.handle, *a) for a in bad] == [0] * 5
+
+
+def test_linear_segments():
+    """One where the sequences are short enough, else enough for 512 workgroups, of
+    128 tokens or more each."""
+    count = layer.linear_segments
+    assert count([0, 100], 4) == 1 and count([0, 1], 64) == 1
+    assert count([0, 65536], 32) == 16 and count([0, 65536], 512) == 1 and count([0, 65536], 1) == 512
+    assert count([0, 1024], 1) == 8
+    assert count([0, 64, 16448], 16) == 32
+    assert count(list(range(0, 16385, 512)), 16) == 1
+
+
 def test_binding_refuses_host_tensors():
     q = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="device tensors"):
         layer.qk_norm_rotate(q, q)
     with pytest.raises(ValueError, match="device tensors"):
         layer.linear_step(q, q, q, torch.zeros(3, 2), torch.zeros(3, 2, 64, 64))
+    plan = kda.Plan([0, 3], 1)
+    with pytest.raises(ValueError, match="device tensors"):
+        layer.linear_forward(plan, q, q, q, torch.zeros(3, 2))
+    with pytest.raises(ValueError, match="device tensors"):
+        layer.linear_backward(plan, q, q, q, torch.zeros(2), q)
+
+
+def test_linear_binding_refusals():
+    """Types, shapes and heads that the binding names before any call."""
+    q = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    g, plan = torch.zeros(3, 2), kda.Plan([0, 3], 1)
+    with pytest.raises(ValueError, match="3 tokens, the plan 4"):
+        layer.linear_forward(kda.Plan([0, 4], 1), q, q, q, g)
+    with pytest.raises(TypeError, match="v: expected torch.bfloat16"):
+        layer.linear_forward(plan, q, q, q.float(), g)
+    with pytest.raises(ValueError, match="k: expected shape"):
+        layer.linear_forward(plan, q, q[..., :56], q, g)
+    with pytest.raises(TypeError, match="g: expected one of"):
+        layer.linear_forward(plan, q, q, q, g.double())
+    with pytest.raises(ValueError, match="initial_state: expected shape"):
+        layer.linear_forward(plan, q, q, q, g, torch.zeros(1, 2, 64, 32))
+    with pytest.raises(TypeError, match="grad_dtype"):
+        layer.linear_backward(plan, q, q, q, g, q, grad_dtype=torch.float16)
+    with pytest.raises(TypeError, match="d_o: expected torch.bfloat16"):
+        layer.linear_backward(plan, q, q, q, g, q.float())
+    with pytest.raises(ValueError, match="rows must be dense"):
+        layer.linear_forward(plan, torch.zeros(3, 64, 2, dtype=torch.bfloat16).transpose(1, 2), q, q, g)
