@@ -43,6 +43,8 @@ ValueError.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import kda
@@ -110,6 +112,14 @@ def _rows(t, dtype, shape, name, device):
     n = shape[0]
     if n and t.is_contiguous():
         return (t.data_ptr(), t.nbytes, t.numel() // n)
+    strides, row = t.stride(), 1
+    for i in range(len(shape) - 1, 0, -1):
+        if strides[i] != row:
+            break
+        row *= shape[i]
+    else:   # slices of a wider tensor's rows, the usual case
+        if n > 1 and strides[0] >= row:
+            return (t.data_ptr(), ((n - 1) * strides[0] + row) * dtype.itemsize, strides[0])
     stride = _row_stride(t, name)
     span = (n - 1) * stride + t.numel() // n if n else 0
     return (t.data_ptr(), span * t.element_size(), stride)
@@ -445,13 +455,20 @@ def _linear_heads(q, k, v, g):
 
 def linear_segments(cu_seqlens, H: int) -> int:
     """The segment count for a plan that only linear attention with ``H`` heads
-    uses.  A segment and head is a workgroup's work, 512 of them run at once, and
-    none is worth less than 128 tokens; one where the sequences are short enough as
-    they are.  (One sequence of 65536 tokens x 32 heads: 16 segments 825 us, 32 855,
-    64 906; its gradients at 16384 tokens: 16 769 us, 8 969, 32 853; 24 sequences of
-    16384 x 16: 24 or 32 segments 121 us, 16 153, 64 143, 1 266.)"""
+    uses; one where the sequences are short enough as they are.  A segment and head
+    is a workgroup's work, chunk of 64 tokens after chunk, and 512 of them run at
+    once: more than 512 segments and heads take a second turn.  Whole chunks are
+    shared out, as a part of one costs as much (1501 tokens x 6 heads with their
+    gradients: 11 segments of 3 chunks 101 us, 12 of 2 85, 24 of 1 70), and no more
+    than 5 sqrt(chunks), as each segment lengthens the ordered scan between them (8192
+    x 8: 32 segments 61 us, 64 73, 128 110; 65536 x 1: 147 117, 512 231).  One
+    sequence of 65536 x 32: 8 segments 907 us, 16 801, 32 832; gradients of 16384 x
+    32: 829, 684, 777; 24 sequences of 16384 x 16: uncut 84 us, 32 137."""
     T = int(cu_seqlens[-1])
-    S = min(-(-512 // H), T // 128)
+    chunks = -(-T // 64)
+    if chunks < 4:   # 100 tokens in two 25 us for 16, their gradients 47 for 49
+        return 1
+    S = -(-chunks // math.ceil(chunks / min(-(-512 // H), 5 * math.sqrt(chunks))))
     longest = max(int(b) - int(a) for a, b in zip(cu_seqlens, cu_seqlens[1:]))
     return S if S > 1 and longest * S > 1.5 * T else 1
 

@@ -240,13 +240,13 @@ def test_linear_workspaces():
 
 
 def test_linear_segments():
-    """One where the sequences are short enough, else enough for 512 workgroups, of
-    128 tokens or more each."""
+    """One where the sequences are short enough, else whole chunks for each segment, at
+    most 512 workgroups and 5 sqrt(chunks) segments."""
     count = layer.linear_segments
     assert count([0, 100], 4) == 1 and count([0, 1], 64) == 1
-    assert count([0, 65536], 32) == 16 and count([0, 65536], 512) == 1 and count([0, 65536], 1) == 512
-    assert count([0, 1024], 1) == 8
-    assert count([0, 64, 16448], 16) == 32
+    assert count([0, 65536], 32) == 16 and count([0, 65536], 512) == 1 and count([0, 65536], 1) == 147
+    assert count([0, 1024], 1) == 16 and count([0, 1501], 6) == 24 and count([0, 192], 6) == 1
+    assert count([0, 64, 16448], 16) == 29
     assert count(list(range(0, 16385, 512)), 16) == 1
 
 
