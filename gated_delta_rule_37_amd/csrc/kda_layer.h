@@ -169,7 +169,8 @@ LinearLayout linear_layout(const kda_plan* plan, int32_t H, int32_t K, int32_t V
 // gate), what passes by each fragment's last chunk [F][H], and one gradient of every head
 // [T][H][max(K, V)] where heads are shared.
 struct LinearBwdLayout {
-  size_t states, cotangents, decays, gates, rho, anchor, heads, total;
+  size_t states, cotangents, decays, query_gates, key_gates, query_border, key_border, query_by, key_by, sums, query_heads,
+      key_heads, value_heads, total;
 };
 LinearBwdLayout linear_bwd_layout(const LinearArgs& a);
 

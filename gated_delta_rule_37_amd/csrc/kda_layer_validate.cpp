@@ -365,17 +365,29 @@ LinearLayout linear_layout(const kda_plan* plan, int32_t H, int32_t K, int32_t V
 LinearBwdLayout linear_bwd_layout(const LinearArgs& a) {
   const LinearLayout F = linear_layout(a.plan, a.H, a.K, a.V);
   const size_t H = static_cast<size_t>(a.H), T = static_cast<size_t>(a.plan->T), frags = static_cast<size_t>(a.plan->F),
-               slots = (T + 63) / 64 + frags, width = static_cast<size_t>(a.K > a.V ? a.K : a.V);
-  const bool shared = a.Hq != a.H || a.Hk != a.H || a.Hv != a.H;
+               K = static_cast<size_t>(a.K), V = static_cast<size_t>(a.V), slots = T / 64 + 1 + frags,
+               rows = T > 64 ? T : 64;   // 64 rows of sums take the place of the first
   LinearBwdLayout L{};
+  size_t next = F.total + F.decays;
+  const auto take = [&next](size_t floats) {
+    const size_t at = next;
+    next += up256(floats * sizeof(float));
+    return at;
+  };
   L.states = 0;
   L.cotangents = F.decays;
   L.decays = 2 * F.decays;
-  L.gates = F.total + F.decays;
-  L.rho = L.gates + up256(T * H * sizeof(float));
-  L.anchor = L.rho + up256((slots > 64 ? slots : 64) * H * sizeof(float));
-  L.heads = L.anchor + up256(frags * H * sizeof(float));
-  L.total = L.heads + (shared ? up256(T * H * width * sizeof(float)) : 0);
+  L.query_gates = take(rows * H);
+  L.key_gates = take(T * H);
+  L.query_border = take(slots * H);
+  L.key_border = take(slots * H);
+  L.query_by = take(frags * H);
+  L.key_by = take(frags * H);
+  L.sums = take(frags * H);
+  L.query_heads = take(a.Hq != a.H ? T * H * K : 0);
+  L.key_heads = take(a.Hk != a.H ? T * H * K : 0);
+  L.value_heads = take(a.Hv != a.H ? T * H * V : 0);
+  L.total = next;
   return L;
 }
 

@@ -14,13 +14,6 @@ namespace kda {
 
 namespace {
 
-// One pass over all fragments and heads.
-int launch_pass(void (*kernel)(LinearParams), const LinearParams& p, int32_t fragments, hipStream_t stream) {
-  (void)hipGetLastError();
-  hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(fragments) * static_cast<uint32_t>(p.H)), dim3(kLinearThreads), 0, stream, p);
-  return finish_launch();
-}
-
 // The state before every piece that goes on within its sequence and, with
 // blockIdx.z 1, the cotangent after every piece whose sequence goes on, in place of
 // the pieces' own updates.  A thread has four elements of one head's state.
@@ -58,26 +51,87 @@ __global__ __launch_bounds__(kRowThreads) void linear_scan_kernel(const int32_t*
   }
 }
 
-// Sums of `share` neighbouring heads' rows [T, H, W] FP32 into [T, H / share, W].
-__global__ __launch_bounds__(kRowThreads) void linear_heads_kernel(const float* in, int32_t share, int32_t W, int64_t quads,
-                                                                   void* out, int32_t out_fp32) {
+// Sums of `share` neighbouring heads' rows [T, H, W] FP32 into [T, H / share, W], of
+// as many gradients as have shared heads.
+struct HeadSums {
+  const float* in;
+  void* out;
+  int64_t quads;
+  int32_t share, W;
+};
+__global__ __launch_bounds__(kRowThreads) void linear_heads_kernel(HeadSums a, HeadSums b, HeadSums c, int32_t out_fp32) {
+  const HeadSums s = blockIdx.y == 0 ? a : blockIdx.y == 1 ? b : c;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
-  if (i >= quads) return;
-  const int64_t row = i * 4 / W, ch = i * 4 - row * W;
-  f32x4 sum = ld4(in + row * share * W + ch);
-  for (int32_t m = 1; m < share; ++m) sum += ld4(in + (row * share + m) * W + ch);
+  if (i >= s.quads) return;
+  const int64_t row = i * 4 / s.W, ch = i * 4 - row * s.W;
+  f32x4 sum = ld4(s.in + row * s.share * s.W + ch);
+  for (int32_t m = 1; m < s.share; ++m) sum += ld4(s.in + (row * s.share + m) * s.W + ch);
   if (out_fp32) {
-    st4(static_cast<float*>(out) + i * 4, sum);
+    st4(static_cast<float*>(s.out) + i * 4, sum);
   } else {
     const u32x2 v = {pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + i * 4) = v;
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(s.out) + i * 4) = v;
   }
+}
+
+// The gradient of a fragment's gates:
+//     dg_t = pairs across t in its chunk + what the chunk's tokens from t on take from
+//            before it + what those before t give to after it + what passes by it.
+// What passes by the fragment's first and last chunk is known; between two chunks
+//     by_c + given_c = by_{c+1} + taken_{c+1},
+// as both are what passes the border between them, so that by_c is a suffix sum.
+// [T, H], or with `sums` the fragment's sum of it.
+__global__ __launch_bounds__(kRowThreads) void linear_gate_kernel(const int32_t* plan, BlobLayout L, int32_t T, int32_t H,
+                                                                  GateParts query, GateParts key, void* dg, int32_t dg_bf16,
+                                                                  float* sums) {
+  __shared__ float by[64];
+  __shared__ float total[kRowThreads / 64];
+  const int32_t f = static_cast<int32_t>(blockIdx.x / static_cast<uint32_t>(H)), head = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(H));
+  const int32_t begin = plan[L.frag_begin + f], end = plan[L.frag_end + f], chunks = (end - begin + kLinearChunk - 1) / kLinearChunk;
+  const int64_t cell = static_cast<int64_t>(f) * H + head, slot = static_cast<int64_t>(begin / kLinearChunk) + f;
+  const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
+  float carry = 0.f, sum = 0.f;
+  for (int32_t to = chunks; to > 0; to -= 64) {   // 64 chunks at a time
+    const int32_t from = max(0, to - 64);
+    if (wave == 0) {
+      const int32_t c = from + lane;
+      float x = 0.f;
+      if (c == chunks - 1) {
+        x = query.by[cell];
+      } else if (c < to) {
+        x = query.border[(slot + c + 1) * H + head] - key.border[(slot + c) * H + head];
+      }
+      x = wave_suffix(x, lane) + carry;
+      carry = __shfl(x, 0);
+      by[lane] = c == 0 && chunks > 1 ? key.by[cell] : x;
+    }
+    __syncthreads();
+    for (int32_t c = from + wave; c < to; c += kRowThreads / 64) {
+      const int32_t t = begin + c * kLinearChunk + lane;
+      if (t >= end) continue;
+      const int64_t at = static_cast<int64_t>(head) * T + t;
+      const float d = query.tokens[at] + key.tokens[at] + by[c - from];
+      sum += d;
+      if (sums != nullptr) continue;
+      if (dg_bf16) {
+        static_cast<uint16_t*>(dg)[static_cast<int64_t>(t) * H + head] = static_cast<uint16_t>(pack_bf16(d, 0.f));
+      } else {
+        static_cast<float*>(dg)[static_cast<int64_t>(t) * H + head] = d;
+      }
+    }
+    __syncthreads();
+  }
+  if (sums == nullptr) return;
+  sum = sum64(sum);
+  if (lane == 0) total[wave] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) sums[cell] = (total[0] + total[1]) + (total[2] + total[3]);
 }
 
 // Column sums of [rows][H] in FP32: a workgroup a head's range of rows, then the
 // ranges' sums in order.
 constexpr int kGateBlocks = 64;
-__global__ __launch_bounds__(1024) void linear_gate_kernel(const float* in, int32_t rows, int32_t H, float* part) {
+__global__ __launch_bounds__(1024) void linear_columns_kernel(const float* in, int32_t rows, int32_t H, float* part) {
   __shared__ float sums[16][64];
   const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = static_cast<int32_t>(blockIdx.x) * 64 + lane;
   const int32_t per = (rows + kGateBlocks - 1) / kGateBlocks, first = static_cast<int32_t>(blockIdx.y) * per;
@@ -90,7 +144,7 @@ __global__ __launch_bounds__(1024) void linear_gate_kernel(const float* in, int3
     part[static_cast<int64_t>(blockIdx.y) * H + col] = sum;
   }
 }
-__global__ __launch_bounds__(kRowThreads) void linear_gate_sum_kernel(const float* part, int32_t H, void* dg, int32_t bf16_out) {
+__global__ __launch_bounds__(kRowThreads) void linear_columns_sum_kernel(const float* part, int32_t H, void* dg, int32_t bf16_out) {
   const int32_t h = static_cast<int32_t>(blockIdx.x) * kRowThreads + static_cast<int32_t>(threadIdx.x);
   if (h >= H) return;
   float sum = 0.f;
@@ -102,6 +156,12 @@ __global__ __launch_bounds__(kRowThreads) void linear_gate_sum_kernel(const floa
   }
 }
 
+template <int SS>
+void (*linear_output_of(int32_t K, int32_t V))(LinearParams) {
+  if (K > 64) return V > 64 ? linear_output_kernel<128, 128, SS, SS> : linear_output_kernel<128, 64, SS, SS>;
+  return V > 64 ? linear_output_kernel<64, 128, SS, SS> : linear_output_kernel<64, 64, SS, SS>;
+}
+
 Tokens tokens_of(const Rows& r, int32_t H, int32_t heads, int32_t width) {
   return {static_cast<const uint16_t*>(r.ptr), r.stride, H / heads, width};
 }
@@ -110,6 +170,7 @@ LinearParams pass_of(const LinearArgs& a, int32_t KW, int32_t VW) {
   LinearParams p{};
   p.plan = static_cast<const int32_t*>(a.plan_dev.ptr);
   p.L = a.plan->layout;
+  p.T = a.plan->T;
   p.H = a.H;
   p.KW = KW;
   p.VW = VW;
@@ -173,8 +234,10 @@ int launch_linear(const LinearArgs& a, hipStream_t stream) {
   p.seq_out = static_cast<float*>(a.final_state.ptr);
   p.o = a.o.ptr;
   p.o_fp32 = a.o_format == KDA_FP32 ? 1 : 0;
-  return launch_pass(p.o_fp32 ? linear_kernel_of<3, 3, false, kOutput>(a.K, a.V) : linear_kernel_of<2, 2, false, kOutput>(a.K, a.V),
-                     p, a.plan->F, stream);
+  (void)hipGetLastError();
+  hipLaunchKernelGGL(p.o_fp32 ? linear_output_of<3>(a.K, a.V) : linear_output_of<2>(a.K, a.V),
+                     dim3(static_cast<uint32_t>(a.plan->F) * static_cast<uint32_t>(a.H)), dim3(kLinearThreads), 0, stream, p);
+  return finish_launch();
 }
 
 int launch_linear_backward(const LinearArgs& a, hipStream_t stream) {
@@ -192,62 +255,71 @@ int launch_linear_backward(const LinearArgs& a, hipStream_t stream) {
     st = launch_piece_states(a, at(L.states), at(L.decays), &d, at(L.cotangents), stream);
     if (st != KDA_OK) return st;
   }
-  // each of the gradients: heads that share a row are added in a launch of their own
-  const auto pass = [&](LinearParams& p, int32_t heads, const Dst& out, void (*kernel)(LinearParams)) -> int {
-    const bool shared = heads != a.H;
-    p.o = shared ? static_cast<void*>(at(L.heads)) : out.ptr;
-    p.o_fp32 = shared || fp32 ? 1 : 0;
-    const int st = launch_pass(kernel, p, a.plan->F, stream);
-    if (st != KDA_OK || !shared) return st;
-    const int64_t quads = static_cast<int64_t>(a.plan->T) * heads * p.VW / 4;
-    if (quads > 2147483647LL - kRowThreads) return KDA_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL(linear_heads_kernel, dim3(static_cast<uint32_t>((quads + kRowThreads - 1) / kRowThreads)),
-                       dim3(kRowThreads), 0, stream, at(L.heads), a.H / heads, p.VW, quads, out.ptr, fp32 ? 1 : 0);
-    return finish_launch();
+  const int32_t F = a.plan->F;
+  const uint32_t cells = static_cast<uint32_t>(F) * static_cast<uint32_t>(a.H);
+  // heads that share a row are added in a launch of their own
+  HeadSums sums[3] = {};
+  int shared = 0;
+  int64_t most = 0;
+  const auto out = [&](LinearParams& p, int32_t heads, const Dst& to, size_t offset) {
+    const bool own = heads == a.H;
+    p.o = own ? to.ptr : static_cast<void*>(at(offset));
+    p.o_fp32 = fp32 || !own ? 1 : 0;
+    if (own) return;
+    HeadSums& s = sums[shared++];
+    s = {at(offset), to.ptr, static_cast<int64_t>(a.plan->T) * heads * p.VW / 4, a.H / heads, p.VW};
+    if (s.quads > most) most = s.quads;
   };
-  LinearParams p = pass_of(a, a.V, a.K);
-  p.transposed = 1;
-  p.x = d;
-  p.y = v;
-  p.z = k;
-  p.e = q;
-  p.seq_state = h0;
-  p.piece_state = at(L.states);
-  p.dg_part = at(L.gates);
-  p.rho = at(L.rho);
-  p.anchor = at(L.anchor);
-  p.end_seq = d_final;
-  p.end_piece = at(L.cotangents);
-  st = pass(p, a.Hq, a.dq, linear_query_kernel(a.V, a.K, fp32));
-  if (st != KDA_OK) return st;
-  p.x = v;
-  p.y = d;
-  p.z = q;
-  p.e = k;
-  p.seq_state = d_final;
-  p.piece_state = at(L.cotangents);
-  p.end_seq = h0;
-  p.end_piece = at(L.states);
-  p.dg = fixed ? at(L.gates) : a.dg.ptr;
-  p.dg_bf16 = !fixed && a.g_dtype == KDA_BF16 ? 1 : 0;
-  st = pass(p, a.Hk, a.dk, linear_key_kernel(a.V, a.K, fp32));
-  if (st != KDA_OK) return st;
+  LinearParams query = pass_of(a, a.V, a.K);
+  query.transposed = 1;
+  query.x = d;
+  query.y = v;
+  query.z = k;
+  query.e = q;
+  query.seq_state = h0;
+  query.piece_state = at(L.states);
+  query.gates = {at(L.query_gates), at(L.query_border), at(L.query_by)};
+  query.end_seq = d_final;
+  query.end_piece = at(L.cotangents);
+  out(query, a.Hq, a.dq, L.query_heads);
+  LinearParams key = pass_of(a, a.V, a.K);
+  key.transposed = 1;
+  key.x = v;
+  key.y = d;
+  key.z = q;
+  key.e = k;
+  key.seq_state = d_final;
+  key.piece_state = at(L.cotangents);
+  key.gates = {at(L.key_gates), at(L.key_border), at(L.key_by)};
+  key.end_seq = h0;
+  key.end_piece = at(L.states);
+  out(key, a.Hk, a.dk, L.key_heads);
+  LinearParams value = pass_of(a, a.K, a.V);
+  value.x = k;
+  value.y = q;
+  value.z = d;
+  value.seq_state = d_final;
+  value.piece_state = at(L.cotangents);
+  value.seq_out = static_cast<float*>(a.d_initial_state.ptr);
+  out(value, a.Hv, a.dv, L.value_heads);
+  if (most > 2147483647LL - kRowThreads) return KDA_ERR_UNSUPPORTED;
+
+  (void)hipGetLastError();
+  hipLaunchKernelGGL(fp32 ? linear_grad_fp32(a.K, a.V) : linear_grad_bf16(a.K, a.V), dim3(cells, 3), dim3(kLinearThreads), 0, stream,
+                     query, key, value);
+  hipLaunchKernelGGL(linear_gate_kernel, dim3(cells), dim3(kRowThreads), 0, stream, query.plan, query.L, a.plan->T, a.H, query.gates,
+                     key.gates, a.dg.ptr, a.g_dtype == KDA_BF16 ? 1 : 0, fixed ? at(L.sums) : nullptr);
   if (fixed) {
-    hipLaunchKernelGGL(linear_gate_kernel, dim3((a.H + 63) / 64, kGateBlocks), dim3(1024), 0, stream, at(L.gates), a.plan->T, a.H,
-                       at(L.rho));
-    hipLaunchKernelGGL(linear_gate_sum_kernel, dim3((a.H + kRowThreads - 1) / kRowThreads), dim3(kRowThreads), 0, stream, at(L.rho),
-                       a.H, a.dg.ptr, a.g_dtype == KDA_BF16 ? 1 : 0);
-    st = finish_launch();
-    if (st != KDA_OK) return st;
+    float* const part = at(L.query_gates);   // read by now
+    hipLaunchKernelGGL(linear_columns_kernel, dim3((a.H + 63) / 64, kGateBlocks), dim3(1024), 0, stream, at(L.sums), F, a.H, part);
+    hipLaunchKernelGGL(linear_columns_sum_kernel, dim3((a.H + kRowThreads - 1) / kRowThreads), dim3(kRowThreads), 0, stream, part, a.H,
+                       a.dg.ptr, a.g_dtype == KDA_BF16 ? 1 : 0);
   }
-  p = pass_of(a, a.K, a.V);
-  p.x = k;
-  p.y = q;
-  p.z = d;
-  p.seq_state = d_final;
-  p.piece_state = at(L.cotangents);
-  p.seq_out = static_cast<float*>(a.d_initial_state.ptr);
-  return pass(p, a.Hv, a.dv, linear_value_kernel(a.K, a.V, fp32));
+  if (shared > 0) {
+    hipLaunchKernelGGL(linear_heads_kernel, dim3(static_cast<uint32_t>((most + kRowThreads - 1) / kRowThreads), shared),
+                       dim3(kRowThreads), 0, stream, sums[0], sums[1], sums[2], fp32 ? 1 : 0);
+  }
+  return finish_launch();
 }
 
 }  // namespace kda

@@ -50,10 +50,17 @@ struct Tokens {
   int32_t share, width;
 };
 
+// What a pass finds of the gates' gradient.
+struct GateParts {
+  float* tokens;   // [H][T], the pairs with one token in the chunk
+  float* border;   // [slot][H] what passes a border of the chunk (query: its first token's, key: its last's)
+  float* by;       // [fragment][H] what passes by the chunk where the pass ends
+};
+
 struct LinearParams {
   const int32_t* plan;
   BlobLayout L;
-  int32_t H, KW, VW;            // heads, widths in use (KW <= KD, VW <= VD)
+  int32_t T, H, KW, VW;         // tokens, heads, widths in use (KW <= KD, VW <= VD)
   Tokens x, y, z, e;            // e: q (kQuery) or k (kKey)
   const void* g;
   int64_t g_stride;
@@ -66,15 +73,12 @@ struct LinearParams {
   float *piece_out, *decay_out; // kSummary
   void* o;                      // [T, H, VW]
   int32_t o_fp32;
-  // gradient of the gates
-  float *dg_part, *rho, *anchor;
+  GateParts gates;              // kQuery, kKey
   const float *end_seq, *end_piece;   // the states of the other gradient where this pass ends (seq: or null)
-  void* dg;
-  int32_t dg_bf16;
 };
 
-// kSummary: a fragment's own state and decay alone.  kQuery: also the gates'
-// gradient as far as the queries see it; kKey: the rest of it.
+// kSummary: a fragment's own state and decay alone.  kQuery and kKey: also what
+// queries and keys take and give of the gates' gradient.
 enum LinearMode { kSummary, kOutput, kQuery, kKey };
 
 constexpr int kLinearChunk = 64;
@@ -336,11 +340,10 @@ struct LinearAcc<16> {
 };
 
 template <int KD, int VD, int SS, int PS, bool REV, int MODE>
-__device__ __forceinline__ void linear_pass(const LinearParams& p) {
+__device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD, VD, PS, MODE>& sm) {
   constexpr int CW = VD / 4, KT = KD / CW, OT = kLinearChunk / CW, US = 3;   // a wave's columns, tiles of S and of out
   constexpr bool kOut = MODE != kSummary;
   typedef typename LinearAcc<CW>::type Acc;
-  __shared__ LinearSmem<KD, VD, PS, MODE> sm;
   const bool rev = MODE == kSummary ? p.reversed != 0 : REV;
 
   const int32_t f = p.plan[p.L.frag_order + static_cast<int32_t>(blockIdx.x / static_cast<uint32_t>(p.H))];
@@ -374,7 +377,6 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p) {
     }
   }
   const int chunks = (end - begin + kLinearChunk - 1) / kLinearChunk;
-  float carry = 0.f;   // kKey: what passes from before the chunk's end to after it
   double total = 0.0;
 
   const Minus minus;
@@ -410,11 +412,11 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p) {
     cz.start(p.z, head, t0, valid_of(t0), sm.z[kOut ? 0 : it & 1], wave);
   };
   // What comes through registers: wave 0's gates, two chunks ahead as their prefix
-  // sums are made beside P; for kKey a lane's channels of k and, in wave 0, what
-  // kQuery left of the gates' gradient.  The compiler does not know of the copies, so
-  // it would wait for all of them before it uses such a value; `landed` uses them
-  // where the copies before them have been waited for anyway.
-  uint32_t gate = 0, part = 0, rho = 0;
+  // sums are made beside P, and for kKey a lane's channels of k.  The compiler does
+  // not know of the copies, so it would wait for all of them before it uses such a
+  // value; `landed` uses them where the copies before them have been waited for
+  // anyway.
+  uint32_t gate = 0;
   constexpr int kKeys = CW * CW / 256 * OT;   // a lane's quads of out
   u32x2 key[MODE == kKey ? kKeys : 1];
   const auto fetch_gate = [&](int it) {
@@ -442,16 +444,10 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p) {
         const uint32_t at = at_key + CW * tile * static_cast<uint32_t>(p.e.stride) * 2 + 16 * q;
         key[n] = __builtin_amdgcn_raw_buffer_load_b64(rows, CW * wave + 8 * q + 4 * lrow < p.VW ? at : kOutside, 0, 0);
       }
-      if (wave == 0) {
-        const int64_t slot = static_cast<int64_t>(begin / kLinearChunk) + f + (chunks - 1 - it);
-        part = __builtin_amdgcn_raw_buffer_load_b32(buffer_of(p.dg_part + t0 * p.H + head, (static_cast<int64_t>(valid) - 1) * p.H * 4 + 4),
-                                                    lane * p.H * 4, 0, 0);
-        rho = __builtin_amdgcn_raw_buffer_load_b32(buffer_of(p.rho + slot * p.H + head, 4), 0, 0, 0);
-      }
     }
   };
   const auto landed = [&] {
-    asm volatile("" : "+v"(gate), "+v"(part), "+v"(rho));
+    asm volatile("" : "+v"(gate));
     if constexpr (MODE == kKey) {
 #pragma unroll
       for (int n = 0; n < kKeys; ++n) asm volatile("" : "+v"(key[n]));
@@ -485,6 +481,7 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p) {
     const int64_t t0 = begin + c * kLinearChunk;
     const int valid = min(kLinearChunk, end - static_cast<int>(t0));
     const int Y = MODE == kQuery ? 0 : it & 1, Z = kOut ? 0 : it & 1;
+    const bool last = (MODE == kQuery || (MODE == kKey && chunks > 1)) && it + 1 == chunks;
     if constexpr (MODE == kQuery) {
       block_sync();   // the last chunk's readers
       sy.store(sm.y[0]);
@@ -511,8 +508,6 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p) {
     // kQuery: the addresses of what is read by columns are made anew, as all would not fit
     const int reader = MODE == kQuery ? opaque(lane) : lane;
 
-    // wave 0 needs this chunk's parts at its end
-    const float left = __uint_as_float(part), taken = __uint_as_float(rho);
     Acc out[OT];
     if constexpr (kOut) {
       // P: tiles of 16 out tokens (columns) by 16 tokens of the sum (rows)
@@ -660,8 +655,8 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p) {
       }
       // What passes by the chunk, e^{G_C} <cotangent after it, state before it>, is a
       // dot product of states at both ends of the fragment, where the other state is
-      // in memory, and between them the difference of what crosses two borders
-      if (MODE == kQuery ? it + 1 == chunks : MODE == kKey && c == 0 && chunks > 1) {
+      // in memory (linear_gate_kernel has it for the chunks between them)
+      if (last) {
         const float* with = ends ? p.end_seq : p.end_piece;
         float dot = 0.f;
         if (with != nullptr) {
@@ -776,48 +771,35 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p) {
       }
     }
     if constexpr (MODE == kQuery || MODE == kKey) {
-      // dg_t = pairs across t in the chunk + what the tokens from t on take from
-      // before the chunk + what those before t give to after it + what passes by
       if (wave == 0) {
         float dot = sm.dots[0][lane];
 #pragma unroll
         for (int w = 1; w < 4; ++w) dot += sm.dots[w][lane];
-        const int64_t at = (t0 + lane) * p.H + head, slot = (static_cast<int64_t>(begin / kLinearChunk) + f + c) * p.H + head;
+        float part, border;
         if constexpr (MODE == kQuery) {
-          float sum = 0.f;
+          // pairs across t in the chunk, and what the tokens from t on take from before it
+          part = 0.f;
 #pragma unroll
-          for (int a = 0; a < 4; ++a) sum += lane < 16 * (a + 1) ? sm.pairs[a][lane] : 0.f;
+          for (int a = 0; a < 4; ++a) part += lane < 16 * (a + 1) ? sm.pairs[a][lane] : 0.f;
           const float after = wave_suffix(dot, lane);
-          if (lane < valid) p.dg_part[at] = sum + after;
-          if (lane == 0) p.rho[slot] = after;
-          if (it + 1 == chunks && lane == 0) {
+          part += after;
+          border = after;
+        } else {
+          // what the tokens before t give to after the chunk
+          const float upto = wave_prefix(dot, lane);
+          part = __shfl_up(upto, 1);
+          if (lane == 0) part = 0.f;
+          border = __shfl(upto, 63);
+        }
+        if (lane < valid) p.gates.tokens[static_cast<int64_t>(head) * p.T + t0 + lane] = part;
+        if (lane == 0) {
+          p.gates.border[(static_cast<int64_t>(begin / kLinearChunk) + f + c) * p.H + head] = border;
+          if (last) {
             float by = sm.by[0];
 #pragma unroll
             for (int w = 1; w < 4; ++w) by += sm.by[w];
-            p.anchor[static_cast<int64_t>(f) * p.H + head] = gates.whole * by;
+            p.gates.by[static_cast<int64_t>(f) * p.H + head] = gates.whole * by;
           }
-        } else {
-          const float upto = wave_prefix(dot, lane);
-          float given = __shfl_up(upto, 1);
-          if (lane == 0) given = 0.f;
-          float by = carry - __shfl(upto, 63);
-          if (it == 0) {
-            by = p.anchor[static_cast<int64_t>(f) * p.H + head];
-          } else if (c == 0) {
-            by = sm.by[0];
-#pragma unroll
-            for (int w = 1; w < 4; ++w) by += sm.by[w];
-            by *= gates.whole;
-          }
-          if (lane < valid) {
-            const float d = left + given + by;
-            if (p.dg_bf16) {
-              static_cast<uint16_t*>(p.dg)[at] = static_cast<uint16_t>(pack_bf16(d, 0.f));
-            } else {
-              static_cast<float*>(p.dg)[at] = d;
-            }
-          }
-          carry = by + taken;
         }
       }
     }
@@ -836,28 +818,43 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p) {
 }
 
 constexpr int kLinearThreads = 256;
-template <int KD, int VD, int SS, int PS, bool REV, int MODE>
-__global__ __launch_bounds__(kLinearThreads, 2) void linear_kernel(LinearParams p) {
-  linear_pass<KD, VD, SS, PS, REV, MODE>(p);
+template <int KD, int VD, int SS, int PS>
+__global__ __launch_bounds__(kLinearThreads, 2) void linear_output_kernel(LinearParams p) {
+  __shared__ LinearSmem<KD, VD, PS, kOutput> sm;
+  linear_pass<KD, VD, SS, PS, false, kOutput>(p, sm);
 }
 // The pieces' updates, and beside them those of their cotangents.
 template <int KD, int VD>
 __global__ __launch_bounds__(kLinearThreads, 2) void linear_summary_kernel(LinearParams p, LinearParams other) {
-  linear_pass<KD, VD, 1, 1, false, kSummary>(blockIdx.y == 0 ? p : other);
+  __shared__ LinearSmem<KD, VD, 1, kSummary> sm;
+  linear_pass<KD, VD, 1, 1, false, kSummary>(blockIdx.y == 0 ? p : other, sm);
 }
-
+// The three gradients beside one another: while the last workgroups of one end, those
+// of the next begin, and a few short sequences' fill the GPU together.
+template <int KD, int VD, int PS>
+__global__ __launch_bounds__(kLinearThreads, 2) void linear_grad_kernel(LinearParams query, LinearParams key, LinearParams value) {
+  __shared__ union {
+    LinearSmem<VD, KD, PS, kQuery> query;
+    LinearSmem<VD, KD, PS, kKey> key;
+    LinearSmem<KD, VD, PS, kOutput> value;
+  } sm;
+  if (blockIdx.y == 0) {
+    linear_pass<VD, KD, 3, PS, false, kQuery>(query, sm.query);
+  } else if (blockIdx.y == 1) {
+    linear_pass<VD, KD, 3, PS, true, kKey>(key, sm.key);
+  } else {
+    linear_pass<KD, VD, PS, PS, true, kOutput>(value, sm.value);
+  }
+}
+typedef void (*LinearGrad)(LinearParams, LinearParams, LinearParams);
 // KD and VD by the widths in use.
-template <int SS, int PS, bool REV, int MODE>
-void (*linear_kernel_of(int32_t KW, int32_t VW))(LinearParams) {
-  if (KW > 64) return VW > 64 ? linear_kernel<128, 128, SS, PS, REV, MODE> : linear_kernel<128, 64, SS, PS, REV, MODE>;
-  return VW > 64 ? linear_kernel<64, 128, SS, PS, REV, MODE> : linear_kernel<64, 64, SS, PS, REV, MODE>;
+template <int PS>
+LinearGrad linear_grad_of(int32_t K, int32_t V) {
+  if (K > 64) return V > 64 ? linear_grad_kernel<128, 128, PS> : linear_grad_kernel<128, 64, PS>;
+  return V > 64 ? linear_grad_kernel<64, 128, PS> : linear_grad_kernel<64, 64, PS>;
 }
-
-// The gradients' passes (kda_linear_query.hip, kda_linear_key.hip,
-// kda_linear_value.hip).
-void (*linear_query_kernel(int32_t KW, int32_t VW, bool fp32))(LinearParams);
-void (*linear_key_kernel(int32_t KW, int32_t VW, bool fp32))(LinearParams);
-void (*linear_value_kernel(int32_t KW, int32_t VW, bool fp32))(LinearParams);
+LinearGrad linear_grad_bf16(int32_t K, int32_t V);   // kda_linear_grad.hip
+LinearGrad linear_grad_fp32(int32_t K, int32_t V);   // kda_linear_grad32.hip
 
 }  // namespace kda
 
