@@ -106,10 +106,15 @@ __device__ __forceinline__ bf16x8 ld_unit(const bf16* p) { return *reinterpret_c
 
 // A buffer of `bytes` bytes from p on, for raw 32-bit accesses (the resource's last
 // word says so): loads past it give zero and touch no memory, stores past it are
-// dropped.
+// dropped.  The resource is read from the first lane: where the compiler holds it in
+// vector registers it would walk the lanes at each access.
 constexpr int kRawBuffer = 0x00020000;
 __device__ __forceinline__ auto buffer_of(const void* p, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), kRawBuffer);
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at)),
+                 hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(static_cast<uint64_t>(hi) << 32 | lo), 0,
+                                           __builtin_amdgcn_readfirstlane(static_cast<int>(bytes)), kRawBuffer);
 }
 constexpr uint32_t kOutside = 0x80000000u;   // no buffer is that long
 
