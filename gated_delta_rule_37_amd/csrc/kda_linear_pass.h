@@ -361,7 +361,7 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
   if (!kOut && ends) return;   // nothing goes on from here
 
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int half = lane >> 5, l32 = lane & 31, l16 = lane & 15, quad = lane >> 4;
+  const int half = lane >> 5, l16 = lane & 15, quad = lane >> 4;
   const int lcol = lane % CW, lrow = lane / CW;   // a tile's column, and which rows
   const int col = CW * wave + lcol;
   const int64_t size = static_cast<int64_t>(p.KW) * p.VW;
@@ -391,7 +391,6 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
   const uint32_t at_y = MODE == kQuery ? sy.offset(p.y) : 0, at_z = MODE == kQuery ? sz.offset(p.z) : 0;
   const Copy<VD> cz(p.z, wave, lane), ce(p.e, wave, lane);
   const uint32_t o_size = p.o_fp32 ? 4 : 2, o_row = static_cast<uint32_t>(p.H) * p.VW * o_size;
-  const uint32_t at_o = lcol * o_row + (CW * wave + 4 * lrow) * o_size;
   const uint32_t at_key = lcol * static_cast<uint32_t>(p.e.stride) * 2 + (CW * wave + 4 * lrow) * 2;
   // first token of the chunk that is walked as number `it`, and its tokens
   const auto first_of = [&](int it) { return static_cast<int64_t>(begin) + (rev ? chunks - 1 - it : it) * kLinearChunk; };
@@ -710,8 +709,9 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
 #pragma unroll
           for (int n = 0; n < PS; ++n) {
             const bf16* part = sm.p + n * 3072;
-            const bf16x8 pf = CW == 32 ? ld_unit(p_unit(const_cast<bf16*>(part), ob + jb, l32, 2 * (s & 1) + half))
-                                       : ld_unit(p_unit(const_cast<bf16*>(part), ob + jb, 16 * (ib & 1) + l16, quad));
+            const bf16x8 pf = CW == 32
+                ? ld_unit(p_unit(const_cast<bf16*>(part), ob + jb, reader & 31, 2 * (s & 1) + (reader >> 5)))
+                : ld_unit(p_unit(const_cast<bf16*>(part), ob + jb, 16 * (ib & 1) + (reader & 15), reader >> 4));
             out[ib] = product(zf[s], pf, out[ib]);
           }
         }
@@ -745,6 +745,9 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
       }
     }
     if constexpr (kOut) {
+      // the lane's place, in kQuery and kKey also made anew for each chunk
+      const int writer = MODE == kOutput ? lane : opaque(lane), ocol = writer % CW, orow = writer / CW;
+      const uint32_t at_o = ocol * o_row + (CW * wave + 4 * orow) * o_size;
       // four stores a wave at least, whatever the width: the copies' wait counts them
       const auto rows = buffer_of(static_cast<char*>(p.o) + (t0 * p.H + head) * p.VW * o_size, static_cast<int64_t>(valid) * o_row);
 #pragma unroll
@@ -752,7 +755,7 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
         if (CW == 16 || p.o_fp32) {
 #pragma unroll
           for (int q = 0; q < CW * CW / 256; ++q) {
-            const uint32_t at = CW * wave + 8 * q + 4 * lrow < p.VW ? at_o + CW * ib * o_row + 8 * q * o_size : kOutside;
+            const uint32_t at = CW * wave + 8 * q + 4 * orow < p.VW ? at_o + CW * ib * o_row + 8 * q * o_size : kOutside;
             const f32x4 v = {out[ib][4 * q], out[ib][4 * q + 1], out[ib][4 * q + 2], out[ib][4 * q + 3]};
             if (p.o_fp32) {
               __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rows, at, 0, 0);
@@ -769,8 +772,8 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
             lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(lo[0], lo[1], false, false));
             hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(hi[0], hi[1], false, false));
             const u32x4 v = {lo[0], hi[0], lo[1], hi[1]};
-            const uint32_t at = at_o + 32 * ib * o_row + 16 * q + 8 * half;
-            __builtin_amdgcn_raw_buffer_store_b128(v, rows, 32 * wave + 8 * q + 8 * half < p.VW ? at : kOutside, 0, 0);
+            const uint32_t at = at_o + 32 * ib * o_row + 16 * q + 8 * orow;
+            __builtin_amdgcn_raw_buffer_store_b128(v, rows, 32 * wave + 8 * q + 8 * orow < p.VW ? at : kOutside, 0, 0);
           }
         }
       }
@@ -796,14 +799,16 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
           if (lane == 0) part = 0.f;
           border = __shfl(upto, 63);
         }
-        if (lane < valid) p.gates.tokens[static_cast<int64_t>(head) * p.T + t0 + lane] = part;
+        const int token = opaque(lane);
+        if (token < valid) p.gates.tokens[static_cast<int64_t>(head) * p.T + t0 + token] = part;
         if (lane == 0) {
-          p.gates.border[(static_cast<int64_t>(begin / kLinearChunk) + f + c) * p.H + head] = border;
+          const int at = opaque(head);
+          p.gates.border[(static_cast<int64_t>(begin / kLinearChunk) + f + c) * p.H + at] = border;
           if (last) {
             float by = sm.by[0];
 #pragma unroll
             for (int w = 1; w < 4; ++w) by += sm.by[w];
-            p.gates.by[static_cast<int64_t>(f) * p.H + head] = gates.whole * by;
+            p.gates.by[static_cast<int64_t>(f) * p.H + at] = gates.whole * by;
           }
         }
       }
