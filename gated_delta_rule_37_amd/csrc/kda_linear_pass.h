@@ -479,6 +479,11 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
   start_y(0);
   if (kOut) start_x(0);
   if (!kOut) start_z(0);
+  // What the first chunk needs; the others' is waited for at the end of the chunk
+  // before, so that nothing that the compiler knows of is under way at the loop's
+  // head: it would wait for it where the value is used, after the next copies.
+  copies_done<0>();
+  landed();
 
   for (int it = 0; it < chunks; ++it) {
     const int c = rev ? chunks - 1 - it : it;
@@ -490,17 +495,10 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
       block_sync();   // the last chunk's readers
       sy.store(sm.y[0]);
       sz.store(sm.z[0]);
-      copies_done<0>();   // x, e
+      copies_done<4>();   // x, e, while the last chunk's stores go on
       landed();
       block_sync();
     } else {
-      // x, y (kSummary: y, z), while the last chunk's stores go on
-      if (!kOut || it == 0) {
-        copies_done<0>();
-      } else {
-        copies_done<4>();
-      }
-      landed();
       block_sync();   // everyone's; and the last chunk's readers are done
       if (kOut) start_z(it);
     }
@@ -748,32 +746,43 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
       // the lane's place, in kQuery and kKey also made anew for each chunk
       const int writer = MODE == kOutput ? lane : opaque(lane), ocol = writer % CW, orow = writer / CW;
       const uint32_t at_o = ocol * o_row + (CW * wave + 4 * orow) * o_size;
-      // four stores a wave at least, whatever the width: the copies' wait counts them
+      // Four stores in every case, which the copies' wait counts, and the compiler's
+      // for what came through registers; FP32 has four more.
       const auto rows = buffer_of(static_cast<char*>(p.o) + (t0 * p.H + head) * p.VW * o_size, static_cast<int64_t>(valid) * o_row);
+      const bool wide = p.o_fp32 != 0;
 #pragma unroll
       for (int ib = 0; ib < OT; ++ib) {
-        if (CW == 16 || p.o_fp32) {
+        const uint32_t base = at_o + CW * ib * o_row;
+        if constexpr (CW == 16) {
+          const u32x4 raw = __builtin_bit_cast(u32x4, out[ib]);
+          const uint32_t at = CW * wave + 4 * orow < p.VW ? base : kOutside;
+          u32x2 v = {pack_bf16(out[ib][0], out[ib][1]), pack_bf16(out[ib][2], out[ib][3])};
 #pragma unroll
-          for (int q = 0; q < CW * CW / 256; ++q) {
-            const uint32_t at = CW * wave + 8 * q + 4 * orow < p.VW ? at_o + CW * ib * o_row + 8 * q * o_size : kOutside;
-            const f32x4 v = {out[ib][4 * q], out[ib][4 * q + 1], out[ib][4 * q + 2], out[ib][4 * q + 3]};
-            if (p.o_fp32) {
-              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rows, at, 0, 0);
-            } else {
-              __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}, rows, at, 0, 0);
-            }
-          }
-        } else if constexpr (CW == 32) {
+          for (int j = 0; j < 2; ++j) v[j] = wide ? raw[j] : v[j];
+          __builtin_amdgcn_raw_buffer_store_b64(v, rows, at, 0, 0);
+          if (wide) __builtin_amdgcn_raw_buffer_store_b64(u32x2{raw[2], raw[3]}, rows, at + 8, 0, 0);
+        } else {
 #pragma unroll
           for (int q = 0; q < 4; q += 2) {
+            f32x4 quads[2];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) quads[j / 4][j % 4] = out[ib][4 * q + j];
             // channels 0 .. 7 of 16 to the lower half's lane of a token, 8 .. 15 to the upper's
-            u32x2 lo = {pack_bf16(out[ib][4 * q], out[ib][4 * q + 1]), pack_bf16(out[ib][4 * q + 4], out[ib][4 * q + 5])};
-            u32x2 hi = {pack_bf16(out[ib][4 * q + 2], out[ib][4 * q + 3]), pack_bf16(out[ib][4 * q + 6], out[ib][4 * q + 7])};
+            u32x2 lo = {pack_bf16(quads[0][0], quads[0][1]), pack_bf16(quads[1][0], quads[1][1])};
+            u32x2 hi = {pack_bf16(quads[0][2], quads[0][3]), pack_bf16(quads[1][2], quads[1][3])};
             lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(lo[0], lo[1], false, false));
             hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(hi[0], hi[1], false, false));
-            const u32x4 v = {lo[0], hi[0], lo[1], hi[1]};
-            const uint32_t at = at_o + 32 * ib * o_row + 16 * q + 8 * orow;
-            __builtin_amdgcn_raw_buffer_store_b128(v, rows, 32 * wave + 8 * q + 8 * orow < p.VW ? at : kOutside, 0, 0);
+            u32x4 v = {lo[0], hi[0], lo[1], hi[1]};
+            const u32x4 raw = __builtin_bit_cast(u32x4, quads[0]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = wide ? raw[j] : v[j];
+            // the lane's first channel: four from there on, and four from eight on, or eight
+            const int ch = 32 * wave + 8 * q + (wide ? 4 : 8) * orow;
+            const uint32_t at = base + 8 * q * o_size + (wide ? 0 : 8 * orow);
+            __builtin_amdgcn_raw_buffer_store_b128(v, rows, ch < p.VW ? at : kOutside, 0, 0);
+            if (wide) {
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, quads[1]), rows, ch + 8 < p.VW ? at + 32 : kOutside, 0, 0);
+            }
           }
         }
       }
@@ -812,6 +821,10 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
           }
         }
       }
+    }
+    if constexpr (MODE != kQuery) {   // the next x and y (kSummary: y, z), while this chunk's stores go on
+      copies_done<kOut ? 4 : 0>();
+      landed();
     }
   }
 
