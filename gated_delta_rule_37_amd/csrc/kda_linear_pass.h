@@ -13,23 +13,40 @@
 // (v, do, q) transposed, dv the reversed pass of (k, q, do).
 //
 // A workgroup is one fragment of one head, four waves.  A wave holds a quarter of
-// S's columns in FP32 accumulators, tiles of 32 x 32 or, where VD is 64, 16 x 16; x, y, z of the chunk lie in LDS
-// in bf16, exactly as they came.  Whatever is not exact in bf16 is split into bf16
-// parts (8 bits each): two of them leave 2^-16, three 2^-24 of a factor.
+// S's columns in FP32 accumulators, tiles of 32 x 32 or, where VD is 64, 16 x 16; x,
+// y, z of the chunk lie in LDS in bf16, exactly as they came.  Whatever is not exact
+// in bf16 is split into bf16 parts (8 bits each): two of them leave 2^-16, three 2^-24
+// of a factor.
 //   * P = (x y^T) o decay: 16 x 16 tiles, a wave owns whole rows of tiles; its
-//     parts go through LDS, as they are every wave's operand.
+//     parts go through LDS, as they are every wave's operand.  Two parts where the
+//     output is BF16, three for FP32.
 //   * out^T = S^T x^T + z^T P^T: transposed, so that a lane has one token and four
 //     neighbouring channels.  S's accumulators are the matrix core's operand as
 //     they are: its rows stand for channels in the order that makes a lane's k
-//     slots eight neighbouring channels.  They are split in registers.
-//   * S's update: z, read transposed, times its weights, split in registers; y
-//     read transposed.
+//     slots eight neighbouring channels.  They are split in registers, in two parts
+//     where only a BF16 output comes of it, in three for FP32 and for dq and dk, whose
+//     products with q and k are the gates' gradient.
+//   * S's update: z, read transposed, times its weights, split in registers, always
+//     in three parts, as a state is FP32; y read transposed.
 // The chunks come by copies from memory to LDS that take no registers: x of the next
 // chunk after its last reader in this one, y into a second buffer a chunk ahead, z
-// beside P, which does not need it.
+// beside P, which does not need it.  80 KB of LDS and 256 registers, two workgroups
+// a CU.
 // Decays: a gate of a token enters with at least -160 in units of 2 (2^-160 is 0 in
 // FP32), prefix sums are taken in FP64 and kept as a multiple of 2^-9 and the
 // rest, so that the difference of two of them is exact however large they are.
+//
+// Measured at 128 x 128.  Forward, 65536 tokens x 32 heads: 228 us for the pieces' own
+// updates (1.07 GB, 4.7 TB/s), 17 for their scan, 510 to 560 for the outputs (2.15 GB;
+// the copies and stores of that pass alone take 476, its products alone 400 to 427).
+// Gradients of 16384 x 32: 130 + 17 for both directions' pieces, 523 for the three
+// passes, whose products bound them, 11 for the gates.  What the choices are worth:
+// through registers instead of copies, with spills 974 (forward) and 1153 (gradients)
+// for 825 and 769; 8 waves of 16 columns at this width 1035 for 905; 4 waves of 16
+// columns where VD is 64 102 for 119 (24 sequences of 16384 x 16 in all); the
+// gradients' passes in one launch 45 for 60 (1501 x 6); buffers' resources from the
+// first lane and no address spilt 721 for 761 (16384 x 32); subtraction of parts by
+// dot2 instructions, other schedulers, grouped schedules: the same.
 #ifndef KDA_LINEAR_PASS_H_
 #define KDA_LINEAR_PASS_H_
 
@@ -154,8 +171,10 @@ struct Copy {
   static constexpr int kSteps = kLinearChunk / kRows / 4;   // of a wave
   uint32_t at, step;
 
-  __device__ __forceinline__ Copy(const Tokens& t, int wave, int lane) : step(kRows * 4 * static_cast<uint32_t>(t.stride) * 2) {
-    const int row = wave * kRows + lane / (W / 8), c = (lane % (W / 8)) ^ row_bits<W>(row);   // the same bits 4 kRows rows on
+  __device__ __forceinline__ Copy(const Tokens& t, int wave, int lane)
+      : step(kRows * 4 * static_cast<uint32_t>(t.stride) * 2) {
+    const int row = wave * kRows + lane / (W / 8);
+    const int c = (lane % (W / 8)) ^ row_bits<W>(row);   // the same bits 4 kRows rows on
     at = 8 * c < t.width ? static_cast<uint32_t>(row) * static_cast<uint32_t>(t.stride) * 2 + 16 * c : kOutside;
   }
   // rows behind `valid` become zero
@@ -166,8 +185,9 @@ struct Copy {
     rows[1] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(base >> 32) & 0xffffu);
     rows[2] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>((valid - 1) * static_cast<int>(t.stride) * 2 + t.width * 2));
     rows[3] = kRawBuffer;
+    typedef __attribute__((address_space(3))) bf16* Lds;
     const uint32_t lds = __builtin_amdgcn_readfirstlane(
-        static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) bf16*)tile)) + wave * 1024);
+        static_cast<uint32_t>(reinterpret_cast<uintptr_t>((Lds)tile)) + wave * 1024);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"

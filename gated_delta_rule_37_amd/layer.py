@@ -16,6 +16,14 @@ formula).  Entry points mirror the C names:
   (:func:`scan_segments`)
 * :func:`scan_step` (``kda_scan_step``) and :func:`step` (``kda_step``): single
   tokens over a pool of states
+* :func:`qk_norm_rotate`, :func:`qk_norm_rotate_backward`
+  (``kda_qk_norm_rotate``, ``kda_qk_norm_rotate_backward``): queries and keys
+  normed per head and turned by their positions
+* :func:`linear_forward`, :func:`linear_backward` (``kda_linear_forward``,
+  ``kda_linear_backward``): linear attention with a decay for each head over
+  packed sequences; any plan serves, :func:`linear_segments` counts the segments
+  of one that only they use
+* :func:`linear_step` (``kda_linear_step``): its single tokens over a pool of states
 
 A training step of one layer::
 
@@ -35,10 +43,24 @@ final_state::
     o = layer.step(x["q"], x["k"], v, x["g"], x["beta"], state, slots)
     y = layer.output_norm(o, weight, gate=z, activation="sigmoid")
 
+A layer of linear attention, trained and decoded the same way::
+
+    plan = kda.Plan(cu_seqlens, layer.linear_segments(cu_seqlens, H))
+    x = layer.qk_norm_rotate(q_raw, k_raw, positions, inv_freq, q_weight, k_weight, q_scale=K ** -0.5)
+    f = layer.linear_forward(plan, x["q"], x["k"], v, g)
+    y = layer.output_norm(f["o"], weight, gate=z, activation="silu")
+    ...
+    n = layer.output_norm_backward(dy, f["o"], weight, gate=z, activation="silu", d_o_dtype=torch.bfloat16)
+    b = layer.linear_backward(plan, x["q"], x["k"], v, g, n["d_o"])
+    r = layer.qk_norm_rotate_backward(q_raw, k_raw, positions, inv_freq, q_weight, k_weight, b["dq"], b["dk"],
+                                      q_scale=K ** -0.5)
+
+    o = layer.linear_step(x["q"], x["k"], v, g, state, slots)     # decoding, state as final_state
+
 Every call enqueues on ``stream`` (default: the current stream of its tensors'
 device) and returns without waiting; what it allocates belongs to that stream,
 and a plan's device copy waits for it (``Plan.device_blob``, which a capture of
-a scan needs called before).  A tensor on another device than the rest raises
+a scan or of linear attention needs called before).  A tensor on another device than the rest raises
 ValueError.
 """
 from __future__ import annotations
@@ -463,14 +485,16 @@ def linear_segments(cu_seqlens, H: int) -> int:
     than 5 sqrt(chunks), as each segment lengthens the ordered scan between them (8192
     x 8: 32 segments 61 us, 64 73, 128 110; 65536 x 1: 147 117, 512 231).  One
     sequence of 65536 x 32: 8 segments 907 us, 16 801, 32 832; gradients of 16384 x
-    32: 829, 684, 777; 24 sequences of 16384 x 16: uncut 84 us, 32 137."""
+    32: 829, 684, 777.  Of 16384 tokens x 16: 24 equal sequences uncut 84 us, in 32
+    segments 137, 24 with one of 2790 176 and 94, 64 with one of 1265 87 and 98."""
     T = int(cu_seqlens[-1])
     chunks = -(-T // 64)
     if chunks < 4:   # 100 tokens in two 25 us for 16, their gradients 47 for 49
         return 1
     S = -(-chunks // math.ceil(chunks / min(-(-512 // H), 5 * math.sqrt(chunks))))
     longest = max(int(b) - int(a) for a, b in zip(cu_seqlens, cu_seqlens[1:]))
-    return S if S > 1 and longest * S > 1.5 * T else 1
+    uneven = 1.5 if (len(cu_seqlens) - 1) * H <= 512 else 3   # sequences that fill the GPU as they are
+    return S if S > 1 and longest * S > uneven * T else 1
 
 
 def _linear(plan, q, k, v, g, initial_state, stream):

@@ -248,6 +248,8 @@ def test_linear_segments():
     assert count([0, 1024], 1) == 16 and count([0, 1501], 6) == 24 and count([0, 192], 6) == 1
     assert count([0, 64, 16448], 16) == 29
     assert count(list(range(0, 16385, 512)), 16) == 1
+    many = list(range(0, 15000, 250))
+    assert count([*many, 15900], 16) == 1 and count([*many, 15900], 8) == 63 and count([*many, 20000], 16) == 32
 
 
 def test_binding_refuses_host_tensors():
