@@ -117,8 +117,8 @@ def test_captured_follows_slots():
         torch.cuda.synchronize()
         want = layer.linear_step(dev["q"], dev["k"], dev["v"], gd, pool2, slots)
         assert torch.equal(pool, pool2)
-        want[i] = keep[i]
-        assert torch.equal(got, want)
+        want[i] = keep[i]   # the unused row: what the memory held, NaN or not, so bits are compared
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
 
 
 def test_refusals():

@@ -34,12 +34,13 @@ def test_instructions_and_registers(src, tmp_path):
     found = hazards(asm)
     assert not found, found[:10]
     kernels = re.findall(r"\.amdhsa_kernel (\S+)\n(.*?)\.end_amdhsa_kernel", asm, re.S)
-    assert len(kernels) >= 8
+    assert len(kernels) >= 4
     for name, body in kernels:
         value = lambda key: int(re.search(key + r" (\d+)", body).group(1))  # noqa: E731
         # two workgroups a CU, but for FP32 outputs of the widest heads, one
-        if "Li128ELi128ELi3ELi3E" not in name:
+        if not re.search(r"(output|grad)_kernelILi128ELi128ELi3E", name):
             assert value("amdhsa_group_segment_fixed_size") <= 80 * 1024, name
             assert value("amdhsa_next_free_vgpr") <= 256, name
-        # the widest dq pass keeps four registers in scratch
-        assert value("private_segment_fixed_size") <= (16 if src == "kda_linear_query.hip" else 0), name
+        # the widest gradients keep four registers in scratch
+        wide = "grad_kernelILi128ELi128ELi2E" in name
+        assert value("private_segment_fixed_size") <= (16 if wide else 0), name
