@@ -8,6 +8,8 @@
 // ordered scan: state_{r+1} = e^{G_r} state_r + update_r.
 #include "kda_linear_pass.h"
 
+#include <algorithm>
+
 #include "kda.h"
 
 namespace kda {
@@ -86,8 +88,10 @@ __global__ __launch_bounds__(kRowThreads) void linear_gate_kernel(const int32_t*
                                                                   float* sums) {
   __shared__ float by[64];
   __shared__ float total[kRowThreads / 64];
-  const int32_t f = static_cast<int32_t>(blockIdx.x / static_cast<uint32_t>(H)), head = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(H));
-  const int32_t begin = plan[L.frag_begin + f], end = plan[L.frag_end + f], chunks = (end - begin + kLinearChunk - 1) / kLinearChunk;
+  const int32_t f = static_cast<int32_t>(blockIdx.x / static_cast<uint32_t>(H));
+  const int32_t head = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(H));
+  const int32_t begin = plan[L.frag_begin + f], end = plan[L.frag_end + f];
+  const int32_t chunks = (end - begin + kLinearChunk - 1) / kLinearChunk;
   const int64_t cell = static_cast<int64_t>(f) * H + head, slot = static_cast<int64_t>(begin / kLinearChunk) + f;
   const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
   float carry = 0.f, sum = 0.f;
@@ -144,7 +148,8 @@ __global__ __launch_bounds__(1024) void linear_columns_kernel(const float* in, i
     part[static_cast<int64_t>(blockIdx.y) * H + col] = sum;
   }
 }
-__global__ __launch_bounds__(kRowThreads) void linear_columns_sum_kernel(const float* part, int32_t H, void* dg, int32_t bf16_out) {
+__global__ __launch_bounds__(kRowThreads) void linear_columns_sum_kernel(const float* part, int32_t H, void* dg,
+                                                                         int32_t bf16_out) {
   const int32_t h = static_cast<int32_t>(blockIdx.x) * kRowThreads + static_cast<int32_t>(threadIdx.x);
   if (h >= H) return;
   float sum = 0.f;
@@ -181,7 +186,8 @@ LinearParams pass_of(const LinearArgs& a, int32_t KW, int32_t VW) {
 }
 
 // The states before the pieces and, where asked for, the cotangents after them.
-int launch_piece_states(const LinearArgs& a, float* states, float* decays, const Tokens* d_o, float* cotangents, hipStream_t stream) {
+int launch_piece_states(const LinearArgs& a, float* states, float* decays, const Tokens* d_o, float* cotangents,
+                        hipStream_t stream) {
   LinearParams p = pass_of(a, a.K, a.V);
   p.y = tokens_of(a.k, a.H, a.Hk, a.K);
   p.z = tokens_of(a.v, a.H, a.Hv, a.V);
@@ -202,8 +208,8 @@ int launch_piece_states(const LinearArgs& a, float* states, float* decays, const
                : (a.V > 64 ? linear_summary_kernel<64, 128> : linear_summary_kernel<64, 64>);
   const uint32_t both = d_o != nullptr ? 2 : 1;
   (void)hipGetLastError();
-  hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(a.plan->F) * static_cast<uint32_t>(a.H), both), dim3(kLinearThreads), 0,
-                     stream, p, r);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(a.plan->F) * static_cast<uint32_t>(a.H), both), dim3(kLinearThreads),
+                     0, stream, p, r);
   const int st = finish_launch();
   if (st != KDA_OK) return st;
   const int32_t quads = a.K * a.V / 4;
@@ -241,7 +247,11 @@ int launch_linear(const LinearArgs& a, hipStream_t stream) {
 }
 
 int launch_linear_backward(const LinearArgs& a, hipStream_t stream) {
-  if (too_many(a)) return KDA_ERR_UNSUPPORTED;
+  const auto quads_of = [&](int32_t heads, int32_t width) {
+    return heads == a.H ? 0 : static_cast<int64_t>(a.plan->T) * heads * width / 4;
+  };
+  const int64_t most = std::max({quads_of(a.Hq, a.K), quads_of(a.Hk, a.K), quads_of(a.Hv, a.V)});
+  if (too_many(a) || most > 2147483647LL - kRowThreads) return KDA_ERR_UNSUPPORTED;
   const LinearBwdLayout L = linear_bwd_layout(a);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace.ptr);
   auto at = [ws](size_t offset) { return reinterpret_cast<float*>(ws + offset); };
@@ -260,15 +270,12 @@ int launch_linear_backward(const LinearArgs& a, hipStream_t stream) {
   // heads that share a row are added in a launch of their own
   HeadSums sums[3] = {};
   int shared = 0;
-  int64_t most = 0;
   const auto out = [&](LinearParams& p, int32_t heads, const Dst& to, size_t offset) {
     const bool own = heads == a.H;
     p.o = own ? to.ptr : static_cast<void*>(at(offset));
     p.o_fp32 = fp32 || !own ? 1 : 0;
     if (own) return;
-    HeadSums& s = sums[shared++];
-    s = {at(offset), to.ptr, static_cast<int64_t>(a.plan->T) * heads * p.VW / 4, a.H / heads, p.VW};
-    if (s.quads > most) most = s.quads;
+    sums[shared++] = {at(offset), to.ptr, quads_of(heads, p.VW), a.H / heads, p.VW};
   };
   LinearParams query = pass_of(a, a.V, a.K);
   query.transposed = 1;
@@ -302,18 +309,18 @@ int launch_linear_backward(const LinearArgs& a, hipStream_t stream) {
   value.piece_state = at(L.cotangents);
   value.seq_out = static_cast<float*>(a.d_initial_state.ptr);
   out(value, a.Hv, a.dv, L.value_heads);
-  if (most > 2147483647LL - kRowThreads) return KDA_ERR_UNSUPPORTED;
 
   (void)hipGetLastError();
-  hipLaunchKernelGGL(fp32 ? linear_grad_fp32(a.K, a.V) : linear_grad_bf16(a.K, a.V), dim3(cells, 3), dim3(kLinearThreads), 0, stream,
-                     query, key, value);
-  hipLaunchKernelGGL(linear_gate_kernel, dim3(cells), dim3(kRowThreads), 0, stream, query.plan, query.L, a.plan->T, a.H, query.gates,
-                     key.gates, a.dg.ptr, a.g_dtype == KDA_BF16 ? 1 : 0, fixed ? at(L.sums) : nullptr);
+  hipLaunchKernelGGL(fp32 ? linear_grad_fp32(a.K, a.V) : linear_grad_bf16(a.K, a.V), dim3(cells, 3), dim3(kLinearThreads), 0,
+                     stream, query, key, value);
+  hipLaunchKernelGGL(linear_gate_kernel, dim3(cells), dim3(kRowThreads), 0, stream, query.plan, query.L, a.plan->T, a.H,
+                     query.gates, key.gates, a.dg.ptr, a.g_dtype == KDA_BF16 ? 1 : 0, fixed ? at(L.sums) : nullptr);
   if (fixed) {
     float* const part = at(L.query_gates);   // read by now
-    hipLaunchKernelGGL(linear_columns_kernel, dim3((a.H + 63) / 64, kGateBlocks), dim3(1024), 0, stream, at(L.sums), F, a.H, part);
-    hipLaunchKernelGGL(linear_columns_sum_kernel, dim3((a.H + kRowThreads - 1) / kRowThreads), dim3(kRowThreads), 0, stream, part, a.H,
-                       a.dg.ptr, a.g_dtype == KDA_BF16 ? 1 : 0);
+    hipLaunchKernelGGL(linear_columns_kernel, dim3((a.H + 63) / 64, kGateBlocks), dim3(1024), 0, stream, at(L.sums), F, a.H,
+                       part);
+    hipLaunchKernelGGL(linear_columns_sum_kernel, dim3((a.H + kRowThreads - 1) / kRowThreads), dim3(kRowThreads), 0, stream,
+                       part, a.H, a.dg.ptr, a.g_dtype == KDA_BF16 ? 1 : 0);
   }
   if (shared > 0) {
     hipLaunchKernelGGL(linear_heads_kernel, dim3(static_cast<uint32_t>((most + kRowThreads - 1) / kRowThreads), shared),

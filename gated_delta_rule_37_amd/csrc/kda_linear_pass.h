@@ -258,6 +258,7 @@ __device__ __forceinline__ void split_parts(const Minus& minus, const float (&x)
 
 // P: out tokens i by tokens j of the sum, 32 x 32 blocks of the triangle's side
 // that is not empty (block of i plus block of j), 16-byte units xored as above.
+constexpr int kPartSize = 3 * 1024;
 __device__ __forceinline__ bf16* p_unit(bf16* part, int block, int row, int unit) {
   return part + block * 1024 + row * 32 + ((unit ^ ((row >> 2) & 3)) << 3);
 }
@@ -269,7 +270,7 @@ struct LinearSmem {
   __align__(16) bf16 y[MODE == kQuery ? 1 : 2][kLinearChunk * KD];
   __align__(16) bf16 z[MODE == kSummary ? 2 : 1][kLinearChunk * VD];
   __align__(16) bf16 e[MODE == kQuery ? kLinearChunk * VD : 8];
-  __align__(16) bf16 p[kOut ? PS * 3 * 1024 : 8];
+  __align__(16) bf16 p[kOut ? PS * kPartSize : 8];
   struct Gates {
     __align__(16) float high[kLinearChunk], low[kLinearChunk], w_in[kLinearChunk];
     float whole;
@@ -558,7 +559,9 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
           if (REV ? b < a : b > a) {   // the empty corner of a block on the diagonal
             const bf16x4 zero = {0, 0, 0, 0};
 #pragma unroll
-            for (int s = 0; s < PS; ++s) *reinterpret_cast<bf16x4*>(p_unit(sm.p + s * 3072, block, row, unit) + 4 * (quad & 1)) = zero;
+            for (int s = 0; s < PS; ++s) {
+              *reinterpret_cast<bf16x4*>(p_unit(sm.p + s * kPartSize, block, row, unit) + 4 * (quad & 1)) = zero;
+            }
             continue;
           }
           const f32x4 high_j = ld4(gates.high + 16 * b + 4 * quad), low_j = ld4(gates.low + 16 * b + 4 * quad);
@@ -575,7 +578,8 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
             f32x4 m = zero4();
 #pragma unroll
             for (int s = 0; s < VD / 32; ++s) {
-              m = mfma16(ld_unit(unit_at<VD>(sm.z[Z], 16 * b + l16, 4 * s + quad)), ld_unit(unit_at<VD>(sm.e, 16 * a + l16, 4 * s + quad)), m);
+              m = mfma16(ld_unit(unit_at<VD>(sm.z[Z], 16 * b + l16, 4 * s + quad)),
+                         ld_unit(unit_at<VD>(sm.e, 16 * a + l16, 4 * s + quad)), m);
             }
             float pair[4];
 #pragma unroll
@@ -605,7 +609,7 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
               h[i] = pack_bf16(left[2 * i], left[2 * i + 1]);
               if (s + 1 < PS) minus(h[i], left[2 * i], left[2 * i + 1]);
             }
-            *reinterpret_cast<u32x2*>(p_unit(sm.p + s * 3072, block, row, unit) + 4 * (quad & 1)) = h;
+            *reinterpret_cast<u32x2*>(p_unit(sm.p + s * kPartSize, block, row, unit) + 4 * (quad & 1)) = h;
           }
         }
       }
@@ -726,7 +730,7 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
           if (REV ? jb < ob : jb > ob) continue;
 #pragma unroll
           for (int n = 0; n < PS; ++n) {
-            const bf16* part = sm.p + n * 3072;
+            const bf16* part = sm.p + n * kPartSize;
             const bf16x8 pf = CW == 32
                 ? ld_unit(p_unit(const_cast<bf16*>(part), ob + jb, reader & 31, 2 * (s & 1) + (reader >> 5)))
                 : ld_unit(p_unit(const_cast<bf16*>(part), ob + jb, 16 * (ib & 1) + (reader & 15), reader >> 4));
@@ -757,7 +761,8 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
       split_parts<US>(minus, v, part);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
-        const bf16x8 yf = CW == 32 ? slot_column_tokens<KD>(sm.y[Y], t, 32 * kt, reader) : column16_tokens<KD>(sm.y[Y], t, 16 * kt, reader);
+        const bf16x8 yf = CW == 32 ? slot_column_tokens<KD>(sm.y[Y], t, 32 * kt, reader)
+                                   : column16_tokens<KD>(sm.y[Y], t, 16 * kt, reader);
 #pragma unroll
         for (int n = 0; n < US; ++n) S[kt] = product(yf, part[n], S[kt]);
       }
@@ -768,7 +773,8 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
       const uint32_t at_o = ocol * o_row + (CW * wave + 4 * orow) * o_size;
       // Four stores in every case, which the copies' wait counts, and the compiler's
       // for what came through registers; FP32 has four more.
-      const auto rows = buffer_of(static_cast<char*>(p.o) + (t0 * p.H + head) * p.VW * o_size, static_cast<int64_t>(valid) * o_row);
+      const auto rows = buffer_of(static_cast<char*>(p.o) + (t0 * p.H + head) * p.VW * o_size,
+                                  static_cast<int64_t>(valid) * o_row);
       const bool wide = p.o_fp32 != 0;
 #pragma unroll
       for (int ib = 0; ib < OT; ++ib) {
@@ -801,7 +807,8 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
             const uint32_t at = base + 8 * q * o_size + (wide ? 0 : 8 * orow);
             __builtin_amdgcn_raw_buffer_store_b128(v, rows, ch < p.VW ? at : kOutside, 0, 0);
             if (wide) {
-              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, quads[1]), rows, ch + 8 < p.VW ? at + 32 : kOutside, 0, 0);
+              const uint32_t next = ch + 8 < p.VW ? at + 32 : kOutside;
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, quads[1]), rows, next, 0, 0);
             }
           }
         }
@@ -875,7 +882,8 @@ __global__ __launch_bounds__(kLinearThreads, 2) void linear_summary_kernel(Linea
 // The three gradients beside one another: while the last workgroups of one end, those
 // of the next begin, and a few short sequences' fill the GPU together.
 template <int KD, int VD, int PS>
-__global__ __launch_bounds__(kLinearThreads, 2) void linear_grad_kernel(LinearParams query, LinearParams key, LinearParams value) {
+__global__ __launch_bounds__(kLinearThreads, 2) void linear_grad_kernel(LinearParams query, LinearParams key,
+                                                                        LinearParams value) {
   __shared__ union {
     LinearSmem<VD, KD, PS, kQuery> query;
     LinearSmem<VD, KD, PS, kKey> key;

@@ -678,8 +678,8 @@ size_t kda_scan_workspace_bytes(const kda_plan* plan, int32_t D);
  *   initial_state  [N, H, K, V] FP32 or NULL (zero)
  *   o              [T, H, V] in o_format; final_state [N, H, K, V] FP32
  * The plan's pieces (its segments, if it has none) run in parallel and change
- * results only by rounding: a long sequence wants several times as many as fill
- * the GPU with the heads.  Where a piece goes on within its sequence its state
+ * results only by rounding: a long sequence wants as many as fill the GPU with the
+ * heads, 512 of both together.  Where a piece goes on within its sequence its state
  * comes from a first pass over all keys and values.  Values are exact products
  * of the bf16 inputs in FP32 sums; factors that are not bf16 (decays, states) are
  * used with 16 bits for a BF16 o and 24 for an FP32 one and for the states.  An
