@@ -5,8 +5,8 @@
 // 8 K V bytes a (row, head), which HBM bandwidth bounds.  A workgroup of 256
 // threads holds the whole state: a thread 4 columns of every `span`th row (at
 // most 16 of them), so that neighbouring threads read neighbouring 16 bytes.  256
-// rows x 32 heads of 128 x 128 take 199 us (240 rows in use: 1.01 GB, 5.1 TB/s), one
-// row of 4 heads the host's 11.
+// rows x 32 heads of 128 x 128 take 199 us (some unused: 1.08 GB, 5.4 TB/s), one row
+// of 4 heads the host's 11.
 #include "kda_layer.h"
 #include "kda_layer_device.h"
 
