@@ -381,11 +381,17 @@ LinearBwdLayout linear_bwd_layout(const LinearArgs& a) {
   L.decays = 2 * F.decays;
   L.query_gates = take(rows * H);
   L.key_gates = take(T * H);
-  L.query_border = take(slots * H);
-  L.key_border = take(slots * H);
+  L.query_border = take(slots * H * 4);
+  L.key_border = take(slots * H * 4);
   L.query_by = take(frags * H);
   L.key_by = take(frags * H);
   L.sums = take(frags * H);
+  // anchors lie between a fragment's first and last chunk
+  const int32_t longest = a.plan->blob[a.plan->layout.frag_order];
+  const int32_t tokens = a.plan->blob[a.plan->layout.frag_end + longest] - a.plan->blob[a.plan->layout.frag_begin + longest];
+  const size_t anchors = tokens > (kAnchorChunks + 1) * 64 ? T / (kAnchorChunks * 64) : 0;
+  L.query_anchors = take(anchors * H * K * V);
+  L.key_anchors = take(anchors * H * K * V);
   L.query_heads = take(a.Hq != a.H ? T * H * K : 0);
   L.key_heads = take(a.Hk != a.H ? T * H * K : 0);
   L.value_heads = take(a.Hv != a.H ? T * H * V : 0);

@@ -79,14 +79,22 @@ __global__ __launch_bounds__(kRowThreads) void linear_heads_kernel(HeadSums a, H
 // The gradient of a fragment's gates:
 //     dg_t = pairs across t in its chunk + what the chunk's tokens from t on take from
 //            before it + what those before t give to after it + what passes by it.
-// What passes by the fragment's first and last chunk is known; between two chunks
+// What passes by a chunk c, by_c = e^{G_C} <cotangent after it, state before it>, is
+// that product at the fragment's first and last chunk (from the passes) and at its
+// anchors, every kAnchorChunks-th chunk.  Between two of them
 //     by_c + given_c = by_{c+1} + taken_{c+1},
-// as both are what passes the border between them, so that by_c is a suffix sum.
+// as both are what passes the border between two chunks.  Such a step leaves an error
+// of about 2^-23 |cotangent| |state| at that border (their norms), which would stay in
+// all chunks behind it however little passes by those.  So it is taken from both
+// anchors, |by_c| is held to e^{G_C} |cotangent after c| |state before c|, which is 0
+// behind a gate that forgets all, and the chunk takes the side with the lesser error.
 // [T, H], or with `sums` the fragment's sum of it.
+constexpr int kGateGroups = 64 / kAnchorChunks;   // of the 64 chunks that are worked on at a time
 __global__ __launch_bounds__(kRowThreads) void linear_gate_kernel(const int32_t* plan, BlobLayout L, int32_t T, int32_t H,
-                                                                  GateParts query, GateParts key, void* dg, int32_t dg_bf16,
-                                                                  float* sums) {
+                                                                  int32_t KV, GateParts query, GateParts key, void* dg,
+                                                                  int32_t dg_bf16, float* sums) {
   __shared__ float by[64];
+  __shared__ float products[kGateGroups][kRowThreads / 64];
   __shared__ float total[kRowThreads / 64];
   const int32_t f = static_cast<int32_t>(blockIdx.x / static_cast<uint32_t>(H));
   const int32_t head = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(H));
@@ -94,21 +102,56 @@ __global__ __launch_bounds__(kRowThreads) void linear_gate_kernel(const int32_t*
   const int32_t chunks = (end - begin + kLinearChunk - 1) / kLinearChunk;
   const int64_t cell = static_cast<int64_t>(f) * H + head, slot = static_cast<int64_t>(begin / kLinearChunk) + f;
   const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
-  float carry = 0.f, sum = 0.f;
-  for (int32_t to = chunks; to > 0; to -= 64) {   // 64 chunks at a time
-    const int32_t from = max(0, to - 64);
-    if (wave == 0) {
-      const int32_t c = from + lane;
-      float x = 0.f;
-      if (c == chunks - 1) {
-        x = query.by[cell];
-      } else if (c < to) {
-        x = query.border[(slot + c + 1) * H + head] - key.border[(slot + c) * H + head];
+  const bool back = lane >= 32;     // lanes 0 .. 31 go from an anchor on, 32 .. 63 from the next one back
+  const int r = lane & 31;
+  float sum = 0.f, next = 0.f;      // by of the chunk behind the 64
+  for (int32_t from = (chunks - 1) / 64 * 64; from >= 0; from -= 64) {
+    const int32_t to = min(from + 64, chunks);
+    for (int n = 0; n < kGateGroups; ++n) {
+      const int32_t c = from + n * kAnchorChunks;
+      if (c == 0 || c + 1 >= chunks) continue;
+      const int64_t at = (static_cast<int64_t>(begin / (kAnchorChunks * kLinearChunk) + c / kAnchorChunks - 1) * H + head) * KV;
+      f32x4 dot = zero4();
+#pragma unroll 8
+      for (int32_t i = 4 * static_cast<int32_t>(threadIdx.x); i < KV; i += 4 * kRowThreads) {
+        dot += ld4(query.anchors + at + i) * ld4(key.anchors + at + i);
       }
-      x = wave_suffix(x, lane) + carry;
-      carry = __shfl(x, 0);
-      by[lane] = c == 0 && chunks > 1 ? key.by[cell] : x;
+      const float part = sum64((dot[0] + dot[1]) + (dot[2] + dot[3]));
+      if (lane == 0) products[n][wave] = part;
     }
+    __syncthreads();
+    const auto anchor = [&](int32_t c) {   // by of a chunk where it is a product
+      if (c + 1 == chunks) return query.by[cell];
+      if (c == 0) return key.by[cell];
+      if (c == from + 64) return next;
+      const float* part = products[(c - from) / kAnchorChunks];
+      return query.border[(slot + c) * H + head][2] * ((part[0] + part[1]) + (part[2] + part[3]));
+    };
+    for (int n = wave; n < kGateGroups; n += kRowThreads / 64) {
+      const int32_t a = from + n * kAnchorChunks, b = min(a + kAnchorChunks, chunks - 1), steps = b - a;
+      if (a >= chunks) break;
+      const int32_t c = back ? max(b - r, a) : min(a + r, b);
+      const f32x4 first = query.border[(slot + c) * H + head], second = key.border[(slot + c) * H + head];
+      const float taken = first[0], state = first[1], given = second[0], cotangent = second[1];
+      // the border to the chunk of the lane before
+      const float step = __shfl_up(back ? taken : given, 1) - (back ? given : taken);
+      const float size = __shfl_up(back ? state : cotangent, 1) * (back ? cotangent : state);
+      const float most = first[2] * state * cotangent;
+      float x = anchor(back ? b : a), error = 0x1p-23f * most;
+      for (int i = 1; i < steps; ++i) {
+        const float x0 = __shfl_up(x, 1), error0 = __shfl_up(error, 1);
+        if (r != i) continue;
+        x = x0 + step;
+        x = x > most ? most : x < -most ? -most : x;   // NaN stays
+        error = error0 + 0x1p-23f * size;
+        error = error > most ? most : error;
+      }
+      const int other = 32 + max(steps - r, 0);   // the same chunk from the other anchor
+      const float y = __shfl(x, other), y_error = __shfl(error, other);
+      const bool from_b = r > 0 && (r == steps || x != x || (y_error < error && y == y));
+      if (!back && r <= steps && r < kAnchorChunks) by[a + r - from] = from_b ? y : x;
+    }
+    next = anchor(from);
     __syncthreads();
     for (int32_t c = from + wave; c < to; c += kRowThreads / 64) {
       const int32_t t = begin + c * kLinearChunk + lane;
@@ -285,7 +328,7 @@ int launch_linear_backward(const LinearArgs& a, hipStream_t stream) {
   query.e = q;
   query.seq_state = h0;
   query.piece_state = at(L.states);
-  query.gates = {at(L.query_gates), at(L.query_border), at(L.query_by)};
+  query.gates = {at(L.query_gates), reinterpret_cast<f32x4*>(at(L.query_border)), at(L.query_by), at(L.query_anchors)};
   query.end_seq = d_final;
   query.end_piece = at(L.cotangents);
   out(query, a.Hq, a.dq, L.query_heads);
@@ -297,7 +340,7 @@ int launch_linear_backward(const LinearArgs& a, hipStream_t stream) {
   key.e = k;
   key.seq_state = d_final;
   key.piece_state = at(L.cotangents);
-  key.gates = {at(L.key_gates), at(L.key_border), at(L.key_by)};
+  key.gates = {at(L.key_gates), reinterpret_cast<f32x4*>(at(L.key_border)), at(L.key_by), at(L.key_anchors)};
   key.end_seq = h0;
   key.end_piece = at(L.states);
   out(key, a.Hk, a.dk, L.key_heads);
@@ -314,7 +357,7 @@ int launch_linear_backward(const LinearArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL(fp32 ? linear_grad_fp32(a.K, a.V) : linear_grad_bf16(a.K, a.V), dim3(cells, 3), dim3(kLinearThreads), 0,
                      stream, query, key, value);
   hipLaunchKernelGGL(linear_gate_kernel, dim3(cells), dim3(kRowThreads), 0, stream, query.plan, query.L, a.plan->T, a.H,
-                     query.gates, key.gates, a.dg.ptr, a.g_dtype == KDA_BF16 ? 1 : 0, fixed ? at(L.sums) : nullptr);
+                     a.K * a.V, query.gates, key.gates, a.dg.ptr, a.g_dtype == KDA_BF16 ? 1 : 0, fixed ? at(L.sums) : nullptr);
   if (fixed) {
     float* const part = at(L.query_gates);   // read by now
     hipLaunchKernelGGL(linear_columns_kernel, dim3((a.H + 63) / 64, kGateBlocks), dim3(1024), 0, stream, at(L.sums), F, a.H,

@@ -70,8 +70,10 @@ struct Tokens {
 // What a pass finds of the gates' gradient.
 struct GateParts {
   float* tokens;   // [H][T], the pairs with one token in the chunk
-  float* border;   // [slot][H] what passes a border of the chunk (query: its first token's, key: its last's)
+  f32x4* border;   // [slot][H] what passes a border of the chunk (query: its first token's, key: its last's),
+                   // the norm of the state there, the chunk's decay, nothing
   float* by;       // [fragment][H] what passes by the chunk where the pass ends
+  float* anchors;  // [anchor][H][K][V] the state at that border of every kAnchorChunks-th chunk of a fragment
 };
 
 struct LinearParams {
@@ -277,7 +279,7 @@ struct LinearSmem {
   } gates[2];   // of this chunk and the next
   __align__(16) float pairs[MODE == kQuery ? 4 : 1][kLinearChunk];
   float dots[4][kLinearChunk];
-  float by[4];
+  float by[4], squares[2][4];   // squares: of this chunk's state and the next's
 };
 
 // A wave's part of a state in memory: f(four neighbouring values of the tiles, their
@@ -317,25 +319,16 @@ __device__ __forceinline__ void store_quad(const LinearParams& p, float* s, int 
   for (int j = 0; j < 4; ++j) s[(row + j) * p.VW + col] = v[j];
 }
 
-__device__ __forceinline__ float wave_prefix(float x, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const float y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
-  return x;
+// The inclusive prefix sum over the wave's 64 lanes: within rows of 16 by row shifts,
+// then each row's total broadcast to those behind it.  No lane needs another's address.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float from_lane(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, ROWS, 0xf, true));
 }
-__device__ __forceinline__ float wave_suffix(float x, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const float y = __shfl_down(x, d);
-    if (lane + d < 64) x += y;
-  }
-  return x;
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float prefix_step(float x) {
+  return x + from_lane<CTRL, ROWS>(x);
 }
-
-// The inclusive prefix sum over the wave's 64 lanes in FP64: within rows of 16 by
-// row shifts, then each row's total broadcast to those behind it.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ double prefix_step(double x) {
   const uint64_t b = __builtin_bit_cast(uint64_t, x);
@@ -343,13 +336,17 @@ __device__ __forceinline__ double prefix_step(double x) {
                  hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROWS, 0xf, true);
   return x + __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
 }
-__device__ __forceinline__ double gate_prefix(double x) {
+template <typename X>
+__device__ __forceinline__ X wave_prefix(X x) {
   x = prefix_step<0x111, 0xf>(x);
   x = prefix_step<0x112, 0xf>(x);
   x = prefix_step<0x114, 0xf>(x);
   x = prefix_step<0x118, 0xf>(x);
   x = prefix_step<0x142, 0xa>(x);   // lane 15 to row 1, lane 47 to row 3
   return prefix_step<0x143, 0xc>(x);   // lane 31 to rows 2 and 3
+}
+__device__ __forceinline__ float last_lane(float x) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
 }
 
 __device__ __forceinline__ f32x16 product(const bf16x8& a, const bf16x8& b, const f32x16& c) { return mfma(a, b, c); }
@@ -484,7 +481,7 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
     const float g = lane < valid_of(first_of(it)) ? __uint_as_float(p.g_bf16 ? gate << 16 : gate) : 0.f;
     double G = static_cast<double>(g) * 1.4426950408889634074;
     if (G < kLeastGate) G = kLeastGate;   // NaN stays
-    G = gate_prefix(G);
+    G = wave_prefix(G);
     const double last = __shfl(G, 63);
     const double high = rint(G * 512.0) * (1.0 / 512.0);
     to.high[lane] = static_cast<float>(high);
@@ -500,6 +497,28 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
   start_y(0);
   if (kOut) start_x(0);
   if (!kOut) start_z(0);
+  // the squares of the state at chunk it's border, and there the anchor's copy of it
+  const auto measure = [&](int it) {
+    if constexpr (MODE == kQuery || MODE == kKey) {
+      float squares = 0.f;
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll
+        for (int i = 0; i < CW * CW / 64; ++i) squares += S[kt][i] * S[kt][i];
+      }
+      squares = last_lane(wave_prefix(squares));
+      if (lane == 0) sm.squares[it & 1][wave] = squares;
+      const int c = rev ? chunks - 1 - it : it;
+      if (it > 0 && c > 0 && c + 1 < chunks && c % kAnchorChunks == 0) {
+        const int place = opaque(begin) / (kAnchorChunks * kLinearChunk) + c / kAnchorChunks - 1, at = opaque(col);
+        float* const to = p.gates.anchors + (static_cast<int64_t>(place) * p.H + opaque(head)) * size;
+        each_quad<CW>(S, opaque(lane), [&](f32x4& v, int row) {
+          if (row < p.KW && at < p.VW) store_quad(p, to, row, at, v);
+        });
+      }
+    }
+  };
+  measure(0);
   // What the first chunk needs; the others' is waited for at the end of the chunk
   // before, so that nothing that the compiler knows of is under way at the loop's
   // head: it would wait for it where the value is used, after the next copies.
@@ -681,7 +700,8 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
       }
       // What passes by the chunk, e^{G_C} <cotangent after it, state before it>, is a
       // dot product of states at both ends of the fragment, where the other state is
-      // in memory (linear_gate_kernel has it for the chunks between them)
+      // in memory, and at its anchors, where both passes leave theirs for
+      // linear_gate_kernel
       if (last) {
         const float* with = ends ? p.end_seq : p.end_piece;
         float dot = 0.f;
@@ -815,31 +835,32 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
       }
     }
     if constexpr (MODE == kQuery || MODE == kKey) {
+      if (it + 1 < chunks) measure(it + 1);
       if (wave == 0) {
-        float dot = sm.dots[0][lane];
+        // kQuery's sums run from the chunk's end
+        const int token = MODE == kQuery ? 63 - opaque(lane) : opaque(lane);
+        float dot = sm.dots[0][token];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) dot += sm.dots[w][lane];
-        float part, border;
+        for (int w = 1; w < 4; ++w) dot += sm.dots[w][token];
+        const float sums = wave_prefix(dot), border = last_lane(sums);
+        float part;
         if constexpr (MODE == kQuery) {
           // pairs across t in the chunk, and what the tokens from t on take from before it
           part = 0.f;
 #pragma unroll
-          for (int a = 0; a < 4; ++a) part += lane < 16 * (a + 1) ? sm.pairs[a][lane] : 0.f;
-          const float after = wave_suffix(dot, lane);
-          part += after;
-          border = after;
+          for (int a = 0; a < 4; ++a) part += token < 16 * (a + 1) ? sm.pairs[a][token] : 0.f;
+          part += sums;
         } else {
-          // what the tokens before t give to after the chunk
-          const float upto = wave_prefix(dot, lane);
-          part = __shfl_up(upto, 1);
-          if (lane == 0) part = 0.f;
-          border = __shfl(upto, 63);
+          // what the tokens before t give to after the chunk: the lane before's (lane 0: 0)
+          part = from_lane<0x138, 0xf>(sums);
         }
-        const int token = opaque(lane);
         if (token < valid) p.gates.tokens[static_cast<int64_t>(head) * p.T + t0 + token] = part;
         if (lane == 0) {
           const int at = opaque(head);
-          p.gates.border[(static_cast<int64_t>(begin / kLinearChunk) + f + c) * p.H + at] = border;
+          // less than 2^-63 an element of the state leaves no square: at most 2^-56 in all
+          const float* squares = sm.squares[it & 1];
+          const float norm = sqrtf((squares[0] + squares[1]) + (squares[2] + squares[3])) + 0x1p-56f;
+          p.gates.border[(static_cast<int64_t>(begin / kLinearChunk) + f + c) * p.H + at] = f32x4{border, norm, gates.whole, 0.f};
           if (last) {
             float by = sm.by[0];
 #pragma unroll
