@@ -107,12 +107,13 @@ __global__ __launch_bounds__(kRowThreads) void linear_gate_kernel(const int32_t*
   float sum = 0.f, next = 0.f;      // by of the chunk behind the 64
   for (int32_t from = (chunks - 1) / 64 * 64; from >= 0; from -= 64) {
     const int32_t to = min(from + 64, chunks);
+#pragma unroll 1
     for (int n = 0; n < kGateGroups; ++n) {
       const int32_t c = from + n * kAnchorChunks;
       if (c == 0 || c + 1 >= chunks) continue;
       const int64_t at = (static_cast<int64_t>(begin / (kAnchorChunks * kLinearChunk) + c / kAnchorChunks - 1) * H + head) * KV;
       f32x4 dot = zero4();
-#pragma unroll 8
+#pragma unroll 4
       for (int32_t i = 4 * static_cast<int32_t>(threadIdx.x); i < KV; i += 4 * kRowThreads) {
         dot += ld4(query.anchors + at + i) * ld4(key.anchors + at + i);
       }
@@ -127,6 +128,7 @@ __global__ __launch_bounds__(kRowThreads) void linear_gate_kernel(const int32_t*
       const float* part = products[(c - from) / kAnchorChunks];
       return query.border[(slot + c) * H + head][2] * ((part[0] + part[1]) + (part[2] + part[3]));
     };
+#pragma unroll 1
     for (int n = wave; n < kGateGroups; n += kRowThreads / 64) {
       const int32_t a = from + n * kAnchorChunks, b = min(a + kAnchorChunks, chunks - 1), steps = b - a;
       if (a >= chunks) break;
@@ -138,6 +140,7 @@ __global__ __launch_bounds__(kRowThreads) void linear_gate_kernel(const int32_t*
       const float size = __shfl_up(back ? state : cotangent, 1) * (back ? cotangent : state);
       const float most = first[2] * state * cotangent;
       float x = anchor(back ? b : a), error = 0x1p-23f * most;
+#pragma unroll 1
       for (int i = 1; i < steps; ++i) {
         const float x0 = __shfl_up(x, 1), error0 = __shfl_up(error, 1);
         if (r != i) continue;
