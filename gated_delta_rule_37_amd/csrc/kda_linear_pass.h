@@ -103,6 +103,19 @@ enum LinearMode { kSummary, kOutput, kQuery, kKey };
 constexpr int kLinearChunk = 64;
 constexpr float kLeastGate = -160.f;
 
+// 2^(high + low), high a multiple of 2^-9 and |low| at most that.  EXACT: what the sum
+// lost in FP32, up to half a unit of 2^6, is worked in to first order, as in exact_exp,
+// to 4 units of 2^-24 for 45; without it for what is used with 16 bits.
+template <bool EXACT>
+__device__ __forceinline__ float power2(float high, float low) {
+  const float x = high + low, e = __builtin_amdgcn_exp2f(x);
+  return EXACT ? __fmaf_rn(e, (low - (x - high)) * kLn2, e) : e;
+}
+__device__ __forceinline__ float power2(double x) {
+  const float high = static_cast<float>(x), e = __builtin_amdgcn_exp2f(high);
+  return __fmaf_rn(e, static_cast<float>(x - high) * kLn2, e);
+}
+
 // Tiles of 64 tokens, rows of W bf16 in 16-byte units; the unit's place is xored
 // with bits of the row, so that 16 rows' units of one column, and 4 rows' 64
 // bytes, lie on different banks.
@@ -486,8 +499,8 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
     const double high = rint(G * 512.0) * (1.0 / 512.0);
     to.high[lane] = static_cast<float>(high);
     to.low[lane] = static_cast<float>(G - high);
-    to.w_in[lane] = __builtin_amdgcn_exp2f(static_cast<float>(rev ? G : last - G));
-    if (lane == 0) to.whole = __builtin_amdgcn_exp2f(static_cast<float>(last));
+    to.w_in[lane] = power2(rev ? G : last - G);
+    if (lane == 0) to.whole = power2(last);
     total += last;
   };
   fetch_gate(0);
@@ -587,10 +600,12 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
           float w[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float e = REV ? (high_j[r] - high) + (low_j[r] - low) : (high - high_j[r]) + (low - low_j[r]);
+            // FP32's 24 bits also for kQuery's pairs, which are the gates' gradient
+            const float e = power2<PS == 3 || MODE == kQuery>(REV ? high_j[r] - high : high - high_j[r],
+                                                              REV ? low_j[r] - low : low - low_j[r]);
             const int j = 4 * quad + r;
             const bool keep = a != b || (REV ? j >= l16 : j <= l16);
-            w[r] = keep ? acc[b][r] * __builtin_amdgcn_exp2f(e) : 0.f;
+            w[r] = keep ? acc[b][r] * e : 0.f;
           }
           if constexpr (MODE == kQuery) {
             // pairs (i, j < i): sums over j < t for every t <= i of the tile, then over i
@@ -670,7 +685,7 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
 #pragma unroll
       for (int ib = 0; ib < OT; ++ib) {
         const float high = gates.high[CW * ib + lcol], low = gates.low[CW * ib + lcol];
-        const float w = __builtin_amdgcn_exp2f(REV ? (gates.high[63] - high) + (gates.low[63] - low) : high + low);
+        const float w = power2<SS == 3>(REV ? gates.high[63] - high : high, REV ? gates.low[63] - low : low);
 #pragma unroll
         for (int i = 0; i < CW * CW / 64; ++i) out[ib][i] *= w;
       }
@@ -884,7 +899,7 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
     });
   }
   if (!kOut && p.decay_out != nullptr && tid == 0) {
-    p.decay_out[static_cast<int64_t>(seg) * p.H + head] = __builtin_amdgcn_exp2f(static_cast<float>(total));
+    p.decay_out[static_cast<int64_t>(seg) * p.H + head] = power2(total);
   }
 }
 

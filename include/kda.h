@@ -682,7 +682,8 @@ size_t kda_scan_workspace_bytes(const kda_plan* plan, int32_t D);
  * heads, 512 of both together.  Where a piece goes on within its sequence its state
  * comes from a first pass over all keys and values.  Values are exact products
  * of the bf16 inputs in FP32 sums; factors that are not bf16 (decays, states) are
- * used with 16 bits for a BF16 o and 24 for an FP32 one and for the states.  An
+ * used with 16 bits for a BF16 o and 24 for an FP32 one and for the states, without
+ * those below 2^-126 (the last 8 bits of a factor below 2^-110).  An
  * infinity or NaN stays in its own sequence and head; in o it may reach earlier
  * tokens of the same 64-token chunk.
  * Workspace: kda_linear_workspace_bytes(plan, H, K, V) bytes, NULL where that is
