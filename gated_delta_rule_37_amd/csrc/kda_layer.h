@@ -186,6 +186,7 @@ LinearBwdLayout linear_bwd_layout(const LinearArgs& a);
 int check_prepare(const PrepareArgs& a, bool backward);
 int check_rotate(const RotateArgs& a, bool backward);
 int check_linear_sizes(const LinearArgs& a);
+bool linear_grid_fits(const LinearArgs& a, bool backward);   // sizes that passed the check
 int check_linear(const LinearArgs& a, bool backward);
 int check_linear_step(const LinearStepArgs& a);
 int check_norm(const NormArgs& a, bool backward);

@@ -399,7 +399,8 @@ size_t kda_linear_workspace_bytes(const kda_plan* plan, int32_t H, int32_t K, in
   a.H = a.Hq = a.Hk = a.Hv = H;
   a.K = K;
   a.V = V;
-  return kda::check_linear_sizes(a) == KDA_OK ? kda::linear_layout(plan, H, K, V).total : 0;
+  const bool fits = kda::check_linear_sizes(a) == KDA_OK && kda::linear_grid_fits(a, false);
+  return fits ? kda::linear_layout(plan, H, K, V).total : 0;
 }
 
 size_t kda_linear_backward_workspace_bytes(const kda_plan* plan, int32_t H, int32_t Hq, int32_t Hk, int32_t Hv, int32_t K,
@@ -412,7 +413,8 @@ size_t kda_linear_backward_workspace_bytes(const kda_plan* plan, int32_t H, int3
   a.Hv = Hv;
   a.K = K;
   a.V = V;
-  return kda::check_linear_sizes(a) == KDA_OK ? kda::linear_bwd_layout(a).total : 0;
+  const bool fits = kda::check_linear_sizes(a) == KDA_OK && kda::linear_grid_fits(a, true);
+  return fits ? kda::linear_bwd_layout(a).total : 0;
 }
 
 int kda_linear_step(int32_t B, int32_t H, int32_t Hq, int32_t Hk, int32_t Hv, int32_t K, int32_t V,

@@ -405,6 +405,18 @@ int check_linear_sizes(const LinearArgs& a) {
   return st == KDA_OK && a.H > kMaxLinearHeads ? KDA_ERR_UNSUPPORTED : st;
 }
 
+// Grids are below 2^31 threads: a workgroup a fragment and head, and backward four
+// channels of a shared head's gradient a thread.
+bool linear_grid_fits(const LinearArgs& a, bool backward) {
+  constexpr int64_t kMost = 2147483647LL;
+  const auto threads = [&a](int32_t heads, int32_t width) {
+    return heads == a.H ? 0 : static_cast<int64_t>(a.plan->T) * heads * width / 4;
+  };
+  if (static_cast<int64_t>(a.plan->F) * a.H * kRowThreads > kMost) return false;
+  return !backward || (threads(a.Hq, a.K) <= kMost - kRowThreads && threads(a.Hk, a.K) <= kMost - kRowThreads &&
+                       threads(a.Hv, a.V) <= kMost - kRowThreads);
+}
+
 int check_linear(const LinearArgs& a, bool backward) {
   int st = check_linear_sizes(a);
   if (st != KDA_OK) return st;

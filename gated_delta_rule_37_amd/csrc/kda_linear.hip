@@ -264,12 +264,10 @@ int launch_piece_states(const LinearArgs& a, float* states, float* decays, const
   return finish_launch();
 }
 
-bool too_many(const LinearArgs& a) { return static_cast<int64_t>(a.plan->F) * a.H * kLinearThreads > 2147483647LL; }
-
 }  // namespace
 
 int launch_linear(const LinearArgs& a, hipStream_t stream) {
-  if (too_many(a)) return KDA_ERR_UNSUPPORTED;
+  if (!linear_grid_fits(a, false)) return KDA_ERR_UNSUPPORTED;
   const LinearLayout L = linear_layout(a.plan, a.H, a.K, a.V);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace.ptr);
   float *states = reinterpret_cast<float*>(ws + L.states), *decays = reinterpret_cast<float*>(ws + L.decays);
@@ -293,11 +291,11 @@ int launch_linear(const LinearArgs& a, hipStream_t stream) {
 }
 
 int launch_linear_backward(const LinearArgs& a, hipStream_t stream) {
+  if (!linear_grid_fits(a, true)) return KDA_ERR_UNSUPPORTED;
   const auto quads_of = [&](int32_t heads, int32_t width) {
     return heads == a.H ? 0 : static_cast<int64_t>(a.plan->T) * heads * width / 4;
   };
   const int64_t most = std::max({quads_of(a.Hq, a.K), quads_of(a.Hk, a.K), quads_of(a.Hv, a.V)});
-  if (too_many(a) || most > 2147483647LL - kRowThreads) return KDA_ERR_UNSUPPORTED;
   const LinearBwdLayout L = linear_bwd_layout(a);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace.ptr);
   auto at = [ws](size_t offset) { return reinterpret_cast<float*>(ws + offset); };

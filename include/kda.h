@@ -672,6 +672,7 @@ size_t kda_scan_workspace_bytes(const kda_plan* plan, int32_t D);
  *                  h reads q head h / (H / Hq), k head h / (H / Hk) and v head
  *                  h / (H / Hv)
  *   K, V           multiples of 8, at most 128 (KDA_ERR_UNSUPPORTED)
+ *   fragments      the plan's F * H at most 8388607 (KDA_ERR_UNSUPPORTED)
  *   g              g_dtype (kda_dtype), [T, H] with a token stride of at most
  *                  2^22, or [H], the same for every token, with g_stride 0;
  *                  g <= 0, finite or -inf (exp(-inf) = 0 forgets the state)
@@ -711,8 +712,10 @@ size_t kda_linear_workspace_bytes(const kda_plan* plan, int32_t H, int32_t K, in
  *   dg               g_dtype, [T, H] dense, or [H] (summed over the tokens)
  *                    with g_stride 0
  *   d_initial_state  [N, H, K, V] FP32 or NULL
- * States are made again from the inputs.  Workspace: as above, by
- * kda_linear_backward_workspace_bytes (never 0).
+ * T * heads * width of a q, k or v with fewer heads than H at most 8589933564
+ * (KDA_ERR_UNSUPPORTED).  States are made again from the inputs.  Workspace: as
+ * above, by kda_linear_backward_workspace_bytes (never 0 for sizes that the call
+ * takes; both queries give 0 for sizes that it refuses).
  */
 int kda_linear_backward(const kda_plan* plan, const int32_t* plan_dev, size_t plan_dev_bytes, int32_t H, int32_t Hq,
                         int32_t Hk, int32_t Hv, int32_t K, int32_t V, const uint16_t* q, size_t q_bytes, int64_t q_stride,
