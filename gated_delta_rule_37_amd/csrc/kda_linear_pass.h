@@ -241,21 +241,16 @@ __device__ __forceinline__ bf16x8 slot_column_tokens(const bf16* tile, int row0,
                lds_read_tr(unit_at<W>(tile, row + 4, unit) + 4 * (n & 1)));
 }
 
-// Takes the pair h of bf16 from (a, b), exactly: v_dot2c_f32_bf16 adds products of
-// bf16 to an FP32 value, here -1 and 0 times the pair, and x less its bf16 rounding is
-// an FP32 number.
-struct Minus {
-  bf16x2 first, second;
-  __device__ __forceinline__ Minus() : first(sgpr_bf16x2(0x0000bf80u)), second(sgpr_bf16x2(0xbf800000u)) {}
-  __device__ __forceinline__ void operator()(uint32_t h, float& a, float& b) const {
-    a -= __uint_as_float(h << 16);
-    b -= __uint_as_float(h & 0xffff0000u);
-  }
-};
+// Takes the pair h of bf16 from (a, b), exactly: x less its bf16 rounding is an FP32
+// number.
+__device__ __forceinline__ void minus(uint32_t h, float& a, float& b) {
+  a -= __uint_as_float(h << 16);
+  b -= __uint_as_float(h & 0xffff0000u);
+}
 
 // x as N bf16 parts, each the rest of those before it rounded.
 template <int N>
-__device__ __forceinline__ void split_parts(const Minus& minus, const float (&x)[8], bf16x8 (&part)[N]) {
+__device__ __forceinline__ void split_parts(const float (&x)[8], bf16x8 (&part)[N]) {
   u32x4 w[N];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -415,7 +410,6 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
   const int chunks = (end - begin + kLinearChunk - 1) / kLinearChunk;
   double total = 0.0;
 
-  const Minus minus;
   const Copy<KD> cx(p.x, wave, lane), cy(p.y, wave, lane);
   Staged<KD> sy;
   Staged<VD> sz;
@@ -666,7 +660,7 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
           }
         }
         bf16x8 part[SS];
-        split_parts<SS>(minus, v, part);
+        split_parts<SS>(v, part);
 #pragma unroll
         for (int ib = 0; ib < OT; ++ib) {
           const int row = CW * ib + lcol;
@@ -793,7 +787,7 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
         v[2 * i + 1] = __uint_as_float(raw[i] & 0xffff0000u) * (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]);
       }
       bf16x8 part[US];
-      split_parts<US>(minus, v, part);
+      split_parts<US>(v, part);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
         const bf16x8 yf = CW == 32 ? slot_column_tokens<KD>(sm.y[Y], t, 32 * kt, reader)
