@@ -533,8 +533,9 @@ size_t kda_prepare_inputs_backward_workspace_bytes(int32_t T, int32_t H, int32_t
  *                  (KDA_ERR_UNSUPPORTED)
  *   R              even, 0 <= R <= D; interleaved 0 or 1
  *   positions      [T] int32, any values; inv_freq [R / 2].  Both may be NULL
- *                  where R is 0.  Angles are taken in FP64: to 1e-9 at
- *                  positions up to 2^23, whatever the frequency up to 1.
+ *                  where R is 0.  Angles are reduced in FP64, to 3e-9 at
+ *                  positions up to 2^23 whatever the frequency up to 1, and
+ *                  what is left of a turn goes into FP32: to 1e-7 in all.
  *   q_weight, k_weight  [D] or NULL (one)
  *   q, k           dtype, dense; each may be its dense raw input itself, in
  *                  place
