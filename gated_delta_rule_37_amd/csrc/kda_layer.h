@@ -170,13 +170,15 @@ LinearLayout linear_layout(const kda_plan* plan, int32_t H, int32_t K, int32_t V
 // chunks: 734 us, with 16 (none inside) 720.  Gates' gradients of tokens 2^17 times
 // smaller than those around them are within 3.8e-6 of their own norm, with 16 6.1e-6.
 constexpr int kAnchorChunks = 8;
-// Backward: also the states' cotangents, the gates' gradient [T][H], what each
-// chunk's queries take from before it [ceil(T / 64) + F][H] (chunk c of fragment f
-// in slot floor(begin_f / 64) + f + c; then the 64 ranges' sums of a shared
-// gate), what passes by each fragment's last chunk [F][H], the states and cotangents
-// at the anchors [T / (64 kAnchorChunks)][H][K][V] (chunk c of fragment f in place
-// floor(begin_f / (64 kAnchorChunks)) + c / kAnchorChunks - 1), and one gradient of
-// every head [T][H][max(K, V)] where heads are shared.
+// Backward, behind those: the states' cotangents; of both passes the gates' gradient
+// within the chunks [H][T] (at least 64 rows: then query_gates holds the 64 ranges' sums
+// of a shared gate), four numbers at each chunk's border [T / 64 + 1 + F][H][4] (chunk c
+// of fragment f in slot floor(begin_f / 64) + f + c), what passes by the chunk where the
+// pass ends [F][H] and the states at the anchors [T / (64 kAnchorChunks)][H][K][V] (chunk
+// c of fragment f in place floor(begin_f / (64 kAnchorChunks)) + c / kAnchorChunks - 1;
+// none where no fragment has one); the fragments' sums of a shared gate [F][H]; and for
+// each of q, k, v that heads share its gradient for every head [T][H][K] or [T][H][V].
+// All FP32, divisions rounded down.
 struct LinearBwdLayout {
   size_t states, cotangents, decays, query_gates, key_gates, query_border, key_border, query_by, key_by, sums, query_anchors,
       key_anchors, query_heads, key_heads, value_heads, total;
