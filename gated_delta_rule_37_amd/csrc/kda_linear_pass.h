@@ -36,17 +36,24 @@
 // FP32), prefix sums are taken in FP64 and kept as a multiple of 2^-9 and the
 // rest, so that the difference of two of them is exact however large they are.
 //
-// Measured at 128 x 128.  Forward, 65536 tokens x 32 heads: 228 us for the pieces' own
-// updates (1.07 GB, 4.7 TB/s), 17 for their scan, 510 to 560 for the outputs (2.15 GB;
-// the copies and stores of that pass alone take 476, its products alone 400 to 427).
-// Gradients of 16384 x 32: 130 + 17 for both directions' pieces, 523 for the three
-// passes, whose products bound them, 11 for the gates.  What the choices are worth:
-// through registers instead of copies, with spills 974 (forward) and 1153 (gradients)
-// for 825 and 769; 8 waves of 16 columns at this width 1035 for 905; 4 waves of 16
-// columns where VD is 64 102 for 119 (24 sequences of 16384 x 16 in all); the
+// Measured at 128 x 128, in a row of launches at 2.0 GHz (in the first after a pause the
+// clock falls to 1.5, with the same cycles and a third more time).  Forward, 65536 tokens
+// x 32 heads: 230 us for the pieces' own updates (1.07 GB, 4.7 TB/s), 18 for their scan,
+// 510 for the outputs (2.25 GB, 4.4 TB/s; the copies and stores of that pass alone take
+// 476, its products alone 400 to 427; matrix cores busy 42 %, vector units 39 %).  The
+// same with FP32 outputs, one workgroup a CU: 1164 in all for 813.  Gradients of 16384 x
+// 32: 125 + 27 for both directions' pieces, 545 for the three passes, 28 for the gates.
+// No unit bounds those passes: matrix cores are busy 30 %, vector units 40 %, LDS 20 %,
+// and waves wait 43 % of their cycles, for barriers and copies that two workgroups a CU
+// do not cover.  FP32 gradients 1090 in all for 742.  What the choices are worth, each
+// when it was made: through registers instead of copies, with spills 974 (forward) and
+// 1153 (gradients) for 825 and 769; 8 waves of 16 columns at this width 1035 for 905; 4
+// waves of 16 columns where VD is 64 102 for 119 (24 sequences of 16384 x 16 in all); the
 // gradients' passes in one launch 45 for 60 (1501 x 6); buffers' resources from the
-// first lane and no address spilt 721 for 761 (16384 x 32); subtraction of parts by
-// dot2 instructions, other schedulers, grouped schedules: the same.
+// first lane and fewer addresses spilt (12 bytes are) 721 for 761 (16384 x 32);
+// subtraction of parts by dot2 instructions, other schedulers, grouped schedules: the
+// same.  Then exactness of the gates' gradient: 707 to 734 for what passes by a chunk,
+// 746 with decays of 24 bits in it.
 #ifndef KDA_LINEAR_PASS_H_
 #define KDA_LINEAR_PASS_H_
 

@@ -480,13 +480,13 @@ def linear_segments(cu_seqlens, H: int) -> int:
     uses; one where the sequences are short enough as they are.  A segment and head
     is a workgroup's work, chunk of 64 tokens after chunk, and 512 of them run at
     once: more than 512 segments and heads take a second turn.  Whole chunks are
-    shared out, as a part of one costs as much (1501 tokens x 6 heads with their
-    gradients: 11 segments of 3 chunks 101 us, 12 of 2 85, 24 of 1 70), and no more
-    than 5 sqrt(chunks), as each segment lengthens the ordered scan between them (8192
-    x 8: 32 segments 61 us, 64 73, 128 110; 65536 x 1: 147 117, 512 231).  One
-    sequence of 65536 x 32: 8 segments 907 us, 16 801, 32 832; gradients of 16384 x
-    32: 829, 684, 777.  Of 16384 tokens x 16: 24 equal sequences uncut 84 us, in 32
-    segments 137, 24 with one of 2790 176 and 94, 64 with one of 1265 87 and 98."""
+    shared out, as a part of one costs as much (gradients of 1501 tokens x 6 heads: 8
+    segments of 3 chunks 51 us, 12 of 2 45, 24 of 1 46), and no more than 5
+    sqrt(chunks), as each segment lengthens the ordered scan between them (8192 x 8: 32
+    segments 60 us, 64 76, 128 111; 65536 x 1: 73 134, 147 115, 512 229).  One sequence
+    of 65536 x 32: 8 segments 904 us, 16 812, 32 841; gradients of 16384 x 32: 779,
+    741, 797.  Of 16384 tokens x 16: 24 equal sequences uncut 64 us, in 32 segments 91,
+    24 with one of 2790 179 and 94, 64 with one of 1265 88 and 94."""
     T = int(cu_seqlens[-1])
     chunks = -(-T // 64)
     if chunks < 4:   # 100 tokens in two 25 us for 16, their gradients 47 for 49
