@@ -511,9 +511,11 @@ __device__ __forceinline__ void linear_pass(const LinearParams& p, LinearSmem<KD
   start_y(0);
   if (kOut) start_x(0);
   if (!kOut) start_z(0);
-  // the squares of the state at chunk it's border, and there the anchor's copy of it
+  // the squares of the state at chunk it's border, and there the anchor's copy of it,
+  // where a chunk lies between the first and the last
   const auto measure = [&](int it) {
     if constexpr (MODE == kQuery || MODE == kKey) {
+      if (chunks < 3) return;
       float squares = 0.f;
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
